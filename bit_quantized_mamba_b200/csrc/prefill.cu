@@ -29,6 +29,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "umma.cuh"
 
 namespace dfssm {
 namespace prefill {
@@ -46,7 +47,6 @@ constexpr int STAGE_BYTES = A_BYTES + B_BYTES + BITS_BYTES;
 // tf f32 [BN][16] | s f64 [BN] | sum of codes i32 [BN] | exact-LoRA flag i32 [BN]
 constexpr int TAB_TF = 0, TAB_S = BN * DFSSM_MAX_RANK * 4, TAB_SQ = TAB_S + BN * 8, TAB_EX = TAB_SQ + BN * 4;
 constexpr int TAB_BYTES = TAB_EX + BN * 4;
-constexpr long long kWaitBudget = 4000000000LL;  // clock cycles per wait (~2 s)
 
 struct EpiArgs {
   const unsigned char* tab;  // [ceil(M / BN)][TAB_BYTES] token tables (tf, s, sum of codes, exact flag)
@@ -62,64 +62,6 @@ struct EpiArgs {
 
 // ------------------------------------------------------------------------------ PTX helpers
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// Bounded wait for the given phase parity; false when the budget ran out or another role aborted.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*abort_flag) return false;
-    if (clock64() - t0 > kWaitBudget) return false;
-  }
-  return true;
-}
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int c0, int c1,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-      "[%4];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// Bulk copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) from global to shared memory,
-// completion counted on `bar`.
-__device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
-// K-major operand in 128-byte-swizzled rows of 128 bytes: 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t umma_desc_k_sw128(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);  // start address (16-byte units)
-  d |= (uint64_t)1 << 16;                        // leading byte offset (unused with swizzle)
-  d |= (uint64_t)(1024 >> 4) << 32;              // stride byte offset: next 8-row group
-  d |= (uint64_t)1 << 46;                        // descriptor version for sm_100
-  d |= (uint64_t)2 << 61;                        // 128-byte swizzle
-  return d;
-}
 // kind::i8 instruction descriptor: D s32, A s8 (0/1 masks), B s8 (codes), both K-major, M = BM, N = BN.
 constexpr uint32_t kIdesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
                             ((uint32_t)(BM >> 4) << 24);
@@ -132,11 +74,6 @@ __device__ __forceinline__ void umma_i8(uint32_t tmem_d, uint64_t adesc, uint64_
       "l"(adesc), "l"(bdesc), "r"(kIdesc), "r"(accum)
       : "memory");
 }
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
-}
 // d += A (16 x 4) B (4 x 8) in fp64 on the tensor core (the warp-wide legacy MMA).  Fragments: lane (g, t4)
 // = (lane / 4, lane % 4) holds A[g][t4] (a0) and A[g + 8][t4] (a1), B[t4][g] (b), and D[g][2 t4 + {0, 1}]
 // (d[0], d[1]) and D[g + 8][2 t4 + {0, 1}] (d[2], d[3]).
@@ -145,13 +82,6 @@ __device__ __forceinline__ void dmma_m16n8k4(double (&d)[4], double a0, double a
                : "+d"(d[0]), "+d"(d[1]), "+d"(d[2]), "+d"(d[3])
                : "d"(a0), "d"(a1), "d"(b));
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
 // ------------------------------------------------------------------------------ kernels
 
 // Quantization for the prefill: one warp per token.  Codes and scale exactly as the decode quantizer,
@@ -380,13 +310,6 @@ constexpr size_t OFF_BARS = (size_t)STAGES * STAGE_BYTES;
 constexpr size_t OFF_TAB = OFF_BARS + 512;                          // [2][TAB_BYTES] token tables
 constexpr size_t OFF_LO = OFF_TAB + 2 * (size_t)TAB_BYTES;          // [EPI_WARPS][32][8] LoRA sums
 constexpr size_t PSMEM_BYTES = 1024 + OFF_LO + (size_t)EPI_WARPS * 32 * 8 * 8;
-
-// Bounded wait that ignores the abort flag (used to drain work already issued).
-__device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > kWaitBudget) return;
-}
 
 template <bool RESID>  // RESID: y[m][n] = fl32(y[m][n] + out), a residual add in place
 __global__ void __launch_bounds__(PNT, 1)
