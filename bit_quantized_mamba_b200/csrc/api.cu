@@ -122,17 +122,7 @@ int enqueue_head(const int8_t* W, const float* s_row, int V, int d, const float*
 // Clock budget of one device-side wait of the fused decode kernel (about 1 s at 2 GHz).
 constexpr long long kSpinLimitCycles = 2000000000LL;
 
-// The current device is an sm_100 part (asked every call: the answer depends on the calling thread's
-// current device, and the two runtime queries cost well under a microsecond).
-bool device_ok() {
-  int dev = 0, major = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  return major == 10;
-}
+using dfssm::device_ok;
 
 dfssm::GemvArgs gemv_args(const dfssm_linear_t* L, int B, const dfssm::QuantScratch& qs) {
   dfssm::GemvArgs g{};
@@ -269,6 +259,30 @@ int check_field(int rows, int N) {
 
 }  // namespace
 
+// The current device is an sm_100 part (asked every call: the answer depends on the calling thread's
+// current device, and the two runtime queries cost well under a microsecond).
+bool dfssm::device_ok() {
+  int dev = 0, major = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return major == 10;
+}
+
+int dfssm::check_int8_matrix(const int8_t* W, int V, int d) {
+  if (!W || V < 1 || d < 16 || d % 16) return DFSSM_EINVAL;
+  if (d > 8192) return DFSSM_EUNSUPPORTED;
+  return aligned(W, 16) ? DFSSM_OK : DFSSM_EALIGN;
+}
+
+int dfssm::check_rows(const void* x, int x_type, int64_t ldx, int d) {
+  if (!x || (x_type != DFSSM_F32 && x_type != DFSSM_BF16) || ldx < d) return DFSSM_EINVAL;
+  const int64_t size = x_type == DFSSM_F32 ? 4 : 2;
+  return aligned(x, 16) && ldx * size % 16 == 0 ? DFSSM_OK : DFSSM_EALIGN;
+}
+
 // Argument checks of one linear descriptor: d_in a multiple of 32 (above 8192: unsupported), rank 0..16,
 // the pointers present and aligned as the header states.
 int dfssm::check_linear(const dfssm_linear_t* L) {
@@ -349,7 +363,18 @@ size_t dfssm_workspace_size(int op, int a, int b, int c) {
       return prefill_layer_ws(a, b, c).total;
     case DFSSM_OP_LINEAR_MULTI:
     case DFSSM_OP_EMBED:
+    case DFSSM_OP_EMBED_TOKENS:
       return dfssm::kStatusBytes;
+    case DFSSM_OP_LINEAR_INT8:
+    case DFSSM_OP_EMBED_BACKWARD:
+    case DFSSM_OP_HEAD_LOSS:
+    case DFSSM_OP_HEAD_LOSS_BACKWARD:
+      if (a < 0 || b < 16 || b % 16 || b > 8192 || c < 1) return 0;
+      if (a == 0) return dfssm::kStatusBytes;
+      if (op == DFSSM_OP_LINEAR_INT8) return dfssm::linear_int8_workspace_bytes(a, b);
+      if (op == DFSSM_OP_EMBED_BACKWARD) return dfssm::embed_backward_workspace_bytes(a, b, c);
+      if (op == DFSSM_OP_HEAD_LOSS) return dfssm::head_loss_workspace_bytes(a, b, c);
+      return dfssm::head_loss_backward_workspace_bytes(a, b, c);
     default: return 0;
   }
 }

@@ -1,0 +1,294 @@
+// Int8 matrix product on the 5th-generation tensor cores, shared by the many-token operators: a
+// persistent, warp-specialised main loop (TMA producer, MMA issuer, eight epilogue warps) around a policy P
+// that says which tiles a CTA works on, how a K step is loaded and what becomes of the accumulators.
+//
+//   D[128 lanes][n columns] (int32, exact) = sum over K of A[lane][k] B[column][k]   (int8, both K-major)
+//
+// One CTA per SM, 128 x up to 256 tiles, K steps of 128 bytes through a ring of shared-memory stages, two
+// accumulators of 256 tensor-memory columns, so that a tile's epilogue runs while the next tile's products
+// accumulate.
+//
+// Every wait on an mbarrier is bounded: a wait that runs out of budget sets the status word, the CTA stops
+// issuing work, waits (bounded) for its copies and products in flight, frees its tensor memory and returns.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "umma.cuh"
+
+namespace dfssm {
+namespace gemm_i8 {
+
+constexpr int BM = 128;      // lanes of a tile (the MMA's M)
+constexpr int BN_MAX = 256;  // columns of a tile at most (the MMA's N)
+constexpr int BK = 128;      // K bytes of a stage
+constexpr int UMMA_K = 32;   // K bytes of one kind::i8 MMA
+constexpr int A_BYTES = BM * BK;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = (2 + EPI_WARPS) * 32;
+constexpr int MAX_STAGES = 12;
+constexpr int SMEM_LIMIT = 232448;  // 227 KB: the shared memory a CTA may have, all of it dynamic here
+constexpr int BAR_BYTES = 256;
+constexpr int TMEM_COLS = 2 * BN_MAX;
+
+// One output tile of a CTA: lanes a0 .. a0 + na, columns b0 .. b0 + nb, K steps kb0 .. kb1.
+struct Tile {
+  int a0, na, b0, nb;
+  int kb0, kb1;
+};
+
+// kind::i8 instruction descriptor: D s32, A and B s8, both K-major, M = 128, N = n (a multiple of 16).
+__device__ __forceinline__ uint32_t idesc(int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+}
+__device__ __forceinline__ void umma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t id,
+                                     uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(id), "r"(accum)
+      : "memory");
+}
+// 32 lanes x 16 / 32 columns of tensor memory, one lane per thread (to be awaited with tmem_wait).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+      "%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// What every policy's arguments start with.
+struct Common {
+  int b_tile;   // columns a stage has room for
+  int stages;
+  int* err;     // status word: kDeviceTimeout after a wait ran out of budget
+};
+__host__ __device__ inline int stage_bytes(const Common& c) { return A_BYTES + c.b_tile * BK; }
+// Ring depth for b_tile columns beside epi_bytes of epilogue scratch, and the shared memory it takes.
+inline int ring_stages(int b_tile, int epi_bytes) {
+  const int n = (SMEM_LIMIT - 1024 - BAR_BYTES - epi_bytes) / (A_BYTES + b_tile * BK);
+  return n < MAX_STAGES ? n : MAX_STAGES;
+}
+inline size_t smem_bytes(const Common& c, int epi_bytes) {
+  return 1024 + (size_t)c.stages * stage_bytes(c) + BAR_BYTES + epi_bytes;
+}
+
+template <class P>
+__global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ typename P::Args ar) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  // aligned by an offset from the array itself, so that every access stays a shared-memory access
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int stages = ar.c.stages, sbytes = stage_bytes(ar.c);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)stages * sbytes);  // [stages] TMA -> MMA
+  uint64_t* empty = full + MAX_STAGES;      // [stages] MMA -> producer
+  uint64_t* acc_full = empty + MAX_STAGES;  // [2] MMA -> epilogue
+  uint64_t* acc_empty = acc_full + 2;       // [2] epilogue -> MMA
+  uint64_t* mma_done = acc_empty + 2;       // every MMA of this CTA complete
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int& abort_flag = *reinterpret_cast<volatile int*>(tmem_holder + 1);
+  unsigned char* epi_smem = smem + (size_t)stages * sbytes + BAR_BYTES;
+  static_assert((2 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], EPI_WARPS);
+    }
+    mbar_init(mma_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_holder)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem_base = *tmem_holder;
+  if (threadIdx.x == 0) pdl_launch_dependents();
+
+  if (warp == 0 && lane == 0) {
+    // ---- producer: each tile's K steps through the stage ring
+    pdl_wait();
+    int it = 0;
+    bool ok = true;
+    Tile t;
+    for (int j = 0; ok && P::tile(ar, j, t); ++j) {
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        const int s = it % stages;
+        if (it >= stages && !mbar_wait(&empty[s], ((it / stages) - 1) & 1, &abort_flag)) {
+          abort_flag = 1;
+          ok = false;
+          break;
+        }
+        unsigned char* st = smem + (size_t)s * sbytes;
+        P::load(ar, t, kb, st, st + A_BYTES, &full[s]);
+      }
+    }
+    // the last copies land before this CTA may exit
+    for (int j = (it > stages ? it - stages : 0); j < it; ++j) mbar_wait_drain(&full[j % stages], (j / stages) & 1);
+  } else if (warp == 1 && lane == 0) {
+    // ---- MMA issuer
+    int it = 0, local = 0;
+    bool ok = true, issued = false;
+    Tile t;
+    for (; ok && P::tile(ar, local, t); ++local) {
+      const int buf = local & 1;
+      if (local >= 2 && !mbar_wait(&acc_empty[buf], ((local >> 1) - 1) & 1, &abort_flag)) {
+        abort_flag = 1;
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN_MAX);
+      const uint32_t id = idesc((t.nb + 15) & ~15);
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        const int s = it % stages;
+        if (!mbar_wait(&full[s], (it / stages) & 1, &abort_flag)) {
+          abort_flag = 1;
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t a_addr = smem_u32(smem + (size_t)s * sbytes);
+#pragma unroll
+        for (int kk = 0; kk < BK / UMMA_K; ++kk)
+          umma(d_tmem, P::adesc(a_addr, kk), P::bdesc(ar, a_addr + A_BYTES, kk), id,
+               (kb > t.kb0 || kk > 0) ? 1u : 0u);
+        umma_commit(&empty[s]);
+        issued = true;
+      }
+      if (!ok) break;
+      umma_commit(&acc_full[buf]);
+    }
+    // every MMA this thread issued completes before the tensor memory is released
+    if (issued) {
+      umma_commit(mma_done);
+      mbar_wait_drain(mma_done, 0);
+    }
+  } else if (warp >= 2) {
+    // ---- epilogue: warp drains TMEM lanes [32 (warp % 4), +32); the two warps of a quadrant share its columns
+    pdl_wait();
+    typename P::Epilogue epi(ar, epi_smem, warp & 3, (warp - 2) >> 2, lane);
+    int local = 0;
+    Tile t;
+    for (; P::tile(ar, local, t); ++local) {
+      const int buf = local & 1;
+      if (abort_flag || !mbar_wait(&acc_full[buf], (local >> 1) & 1, &abort_flag)) {
+        abort_flag = 1;
+        break;
+      }
+      __syncwarp();
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      epi.tile(ar, t, tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(buf * BN_MAX));
+      // this warp's reads of the accumulator are complete
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&acc_empty[buf])) : "memory");
+    }
+    __syncwarp();
+    epi.finish(ar);
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (abort_flag && threadIdx.x == 0) atomicExch(ar.c.err, kDeviceTimeout);
+  if (warp == 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ row-major operands through TMA
+// Both operands are row-major int8 matrices with K contiguous, loaded as 128-byte-swizzled boxes of 128 bytes
+// of K (bytes past a row's end and rows past the last read as zero).  The rows of one operand are the
+// tokens, of the other the matrix W.
+enum Mode {
+  kGrid = 0,    // tiles of tile_a x b_tile, strided over the CTAs, the token index fastest (W read once)
+  kRangeA = 1,  // every CTA takes a balanced range of A rows (W) in groups of 32, and all columns (one tile)
+  kRangeB = 2   // every CTA takes a balanced range of B rows (W), and for it all tiles of A rows (tokens)
+};
+struct RowArgs {
+  Common c;
+  int mode;
+  int rows_a, rows_b;
+  int kblocks;
+  int box_a, box_b;  // rows of one TMA box of each operand
+  int b_first;       // first B row of the product (a piece of the vocabulary); rows_b counts from there
+};
+
+__device__ __forceinline__ bool row_tile(const RowArgs& r, int w_is_a, int j, Tile& t) {
+  t.kb0 = 0;
+  t.kb1 = r.kblocks;
+  if (r.mode == kGrid) {
+    const int ta = (r.rows_a + BM - 1) / BM, tb = (r.rows_b + r.c.b_tile - 1) / r.c.b_tile;
+    const long long i = blockIdx.x + (long long)j * gridDim.x;
+    if (i >= (long long)ta * tb) return false;
+    const int ia = w_is_a ? (int)(i / tb) : (int)(i % ta);
+    const int ib = w_is_a ? (int)(i % tb) : (int)(i / ta);
+    t.a0 = ia * BM;
+    t.b0 = ib * r.c.b_tile;
+    t.na = min(BM, r.rows_a - t.a0);
+    t.nb = min(r.c.b_tile, r.rows_b - t.b0);
+    return true;
+  }
+  const int rows_w = r.mode == kRangeA ? r.rows_a : r.rows_b;
+  const long long groups = (rows_w + 31) / 32;
+  const int w0 = (int)(groups * blockIdx.x / gridDim.x) * 32;
+  const int w1 = min((int)(groups * (blockIdx.x + 1) / gridDim.x) * 32, rows_w);
+  if (r.mode == kRangeA) {
+    t.a0 = w0 + BM * j;
+    if (t.a0 >= w1) return false;
+    t.na = min(BM, w1 - t.a0);
+    t.b0 = 0;
+    t.nb = r.rows_b;
+    return true;
+  }
+  const int nt = (w1 - w0 + r.c.b_tile - 1) / r.c.b_tile;
+  const int ta = (r.rows_a + BM - 1) / BM;
+  if (nt == 0 || j >= nt * ta) return false;
+  t.a0 = (j / nt) * BM;
+  t.na = min(BM, r.rows_a - t.a0);
+  t.b0 = w0 + (j % nt) * r.c.b_tile;
+  t.nb = min(r.c.b_tile, w1 - t.b0);
+  return true;
+}
+
+// One K step of both operands: whole boxes up to the tile's last row.
+__device__ __forceinline__ void row_load(const RowArgs& r, const CUtensorMap* ma, const CUtensorMap* mb,
+                                         const Tile& t, int kb, unsigned char* sa, unsigned char* sb,
+                                         uint64_t* bar) {
+  const int n_a = (t.na + r.box_a - 1) / r.box_a, n_b = (t.nb + r.box_b - 1) / r.box_b;
+  mbar_expect_tx(bar, (uint32_t)(n_a * r.box_a + n_b * r.box_b) * BK);
+  for (int i = 0; i < n_a; ++i) tma_load_2d(sa + i * r.box_a * BK, ma, kb * BK, t.a0 + i * r.box_a, bar);
+  for (int i = 0; i < n_b; ++i)
+    tma_load_2d(sb + i * r.box_b * BK, mb, kb * BK, r.b_first + t.b0 + i * r.box_b, bar);
+}
+
+}  // namespace gemm_i8
+}  // namespace dfssm

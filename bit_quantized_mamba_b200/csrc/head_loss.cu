@@ -1,0 +1,958 @@
+// Softmax cross entropy of int8-head logits over the vocabulary, without keeping the logits, and its
+// gradient (include/dfssm.h, dfssm_head_loss and dfssm_head_loss_backward).
+//
+// With l_v = acc_v s s_row_v the logits of a token (acc the exact int32 product of the int8 codes, as in the LM
+// head), y its label, and the other rows' m = max_{v != y} l_v, S = sum_{v != y} exp(l_v - m):
+//   z = m + log S - l_y,   loss = log(1 + exp z),   1 - p_y = 1 / (1 + exp(-z)),   p_v = exp(l_v - m) (1 - p_y) / S
+// The label is kept out of m and S, so neither a loss near zero nor 1 - p_y is a difference of nearly equal
+// numbers.
+//
+// Forward: the int8 product with tokens on the tensor memory's lanes and rows of W on its columns; a thread
+// owns a token's logits of a tile and folds them into a running (max, sum), one pass, 8 bytes kept per
+// token, tile and column half; a second kernel joins them.
+//
+// Gradient with respect to the (dequantised) normalised token:  du = g [sum_{v != y} p_v s_row_v W_v -
+// (1 - p_y) s_row_y W_y].  The coefficients c_v = exp(l_v - m) s_row_v / max|s_row| lie in [0, 1] (or [-1, 1]
+// with negative scales) whatever the token, so they are rounded to 24-bit fixed point (half a step: 2^-25 of
+// the largest possible coefficient) and split into three base-256 digits: the sum over v becomes three exact
+// int8 products with W, twice the rate of one bf16 product each and free of the bf16 rounding and of the
+// order of summation.  The vocabulary is taken in pieces whose digits stay in L2:
+//   1. transpose: the piece's W as K-major operand of the second product, and W's column sums;
+//   2. the first product again, its epilogue turning logits into digits (and the row scales' gradient
+//      into partial column sums);
+//   3. the second product: digits x transposed W, added to int32 accumulators in memory by integer
+//      atomics (any order gives the same sum), the (tile, digit, K) space split evenly over the CTAs.
+// At the end one kernel joins the digits and the label's row in fp64 and applies the norm's backward.
+// The digits are stored as signed bytes (digit - 128); the column sums of W give the 128s back.
+
+#include "gemm_i8.cuh"
+#include "rows.cuh"
+
+namespace dfssm {
+namespace {
+
+using namespace gemm_i8;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLn2 = 0.69314718055994530942;
+constexpr int kMaxRangeCtas = 160;  // partial slots are sized without asking the device
+
+inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ------------------------------------------------------------------------------------ forward
+
+struct ForwardPolicy {
+  struct Args {
+    CUtensorMap map_a, map_b;  // codes, W
+    RowArgs r;
+    Common c;
+    const double* s_tok;    // [M]
+    const float* s_row;     // [V]
+    const int32_t* labels;  // [M]
+    float* label_logit;     // [M]
+    float2* part;           // [slots][M] (max, sum) in units of log 2
+    int M, V;
+  };
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile(a.r, 0, j, t); }
+  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int kb, unsigned char* sa,
+                                              unsigned char* sb, uint64_t* bar) {
+    row_load(a.r, &a.map_a, &a.map_b, t, kb, sa, sb, bar);
+  }
+  static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
+    return umma_desc_k_sw128(addr + kk * UMMA_K);
+  }
+  static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr, int kk) {
+    return umma_desc_k_sw128(addr + kk * UMMA_K);
+  }
+  static constexpr int EPI_SMEM = EPI_WARPS * 32 * 4;
+  struct Epilogue {
+    int q, half, lane;
+    float* sr;        // this warp's 32 row scales of a chunk
+    int tok = -1;     // the token whose running (m, S) this thread holds
+    int slot = 0;
+    float m = -INFINITY, S = 0.0f;
+    __device__ __forceinline__ Epilogue(const Args&, unsigned char* sm, int q_, int half_, int lane_)
+        : q(q_), half(half_), lane(lane_), sr(reinterpret_cast<float*>(sm) + (half_ * 4 + q_) * 32) {}
+    __device__ __forceinline__ void flush(const Args& a) {
+      if (tok >= 0 && tok < a.M) a.part[(size_t)slot * a.M + tok] = make_float2(m, S);
+      m = -INFINITY;
+      S = 0.0f;
+    }
+    __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
+      const int tk = t.a0 + q * 32 + lane;
+      const int sl = (a.r.mode == kGrid ? t.b0 / a.r.c.b_tile : (int)blockIdx.x) * 2 + half;
+      if (tk != tok || sl != slot) {
+        flush(a);
+        tok = tk;
+        slot = sl;
+      }
+      const bool valid = tk < a.M;
+      const float s2 = valid ? (float)a.s_tok[tk] * kLog2e : 0.0f;
+      const int label = valid ? a.labels[tk] : -1;
+      for (int c = half * 32; c < t.nb; c += 64) {
+        uint32_t v[32];
+        tmem_ld32(taddr + (uint32_t)c, v);
+        const int v0 = t.b0 + c;
+        __syncwarp();
+        sr[lane] = c + lane < t.nb ? __ldg(a.s_row + v0 + lane) : 0.0f;
+        __syncwarp();
+        // columns that do not count: past the tile's end, and the token's own label
+        uint32_t skip = c + 32 > t.nb ? 0xFFFFFFFFu << (t.nb - c) : 0u;
+        const uint32_t lc = (uint32_t)(label - v0);
+        if (lc < 32u) skip |= 1u << lc;
+        tmem_wait();
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = (float)(int)v[j] * s2;
+        if (lc < 32u && c + (int)lc < t.nb) {
+          int al = 0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j == (int)lc) al = (int)v[j];
+          a.label_logit[tk] = __double2float_rn(dmul(dmul(int_to_f64(al), a.s_tok[tk]), (double)sr[lc]));
+        }
+        float mx = m;
+        const float4* sr4 = reinterpret_cast<const float4*>(sr);
+        if (!__any_sync(0xffffffffu, skip != 0u)) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 w = sr4[j / 4];
+            mx = fmaxf(mx, fmaxf(fmaxf(x[j] * w.x, x[j + 1] * w.y), fmaxf(x[j + 2] * w.z, x[j + 3] * w.w)));
+          }
+          float s = S * ex2(m - mx);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 w = sr4[j / 4];
+            s += ex2(fmaf(x[j], w.x, -mx)) + ex2(fmaf(x[j + 1], w.y, -mx)) + ex2(fmaf(x[j + 2], w.z, -mx)) +
+                 ex2(fmaf(x[j + 3], w.w, -mx));
+          }
+          S = s;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (!((skip >> j) & 1u)) mx = fmaxf(mx, x[j] * sr[j]);
+          const float mz = mx == -INFINITY ? 0.0f : mx;  // nothing counted yet
+          float s = S * ex2(m - mz);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (!((skip >> j) & 1u)) s += ex2(fmaf(x[j], sr[j], -mz));
+          S = s;
+        }
+        m = mx;
+      }
+    }
+    __device__ __forceinline__ void finish(const Args& a) { flush(a); }
+  };
+};
+
+// Joins the partial (max, sum) of a token and forms its loss.  32 tokens per CTA, eight slices of slots.
+__global__ void __launch_bounds__(256) loss_finish_kernel(const float2* __restrict__ part, int slots, int M, int V,
+                                                          const int32_t* __restrict__ labels,
+                                                          float* __restrict__ stats, float* __restrict__ loss,
+                                                          int* status) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ float sm[8][32];
+  __shared__ double ss[8][32];
+  const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int t = blockIdx.x * 32 + lane;
+  float m = -INFINITY;
+  double S = 0.0;
+  if (t < M) {
+    for (int s = sl; s < slots; s += 8) {
+      const float2 p = part[(size_t)s * M + t];
+      const float mn = fmaxf(m, p.x);
+      if (mn > -INFINITY) S = S * exp2((double)m - mn) + (double)p.y * exp2((double)p.x - mn);
+      m = mn;
+      if (!(p.y >= 0.0f)) S = (double)p.y;  // NaN
+    }
+  }
+  sm[sl][lane] = m;
+  ss[sl][lane] = S;
+  __syncthreads();
+  if (sl != 0 || t >= M) return;
+  for (int i = 1; i < 8; ++i) {
+    const float mi = sm[i][lane];
+    const float mn = fmaxf(m, mi);
+    if (mn > -INFINITY) S = S * exp2((double)m - mn) + ss[i][lane] * exp2((double)mi - mn);
+    else S += ss[i][lane];
+    m = mn;
+  }
+  const int y = labels[t];
+  const bool bad = y >= V;
+  if (bad) atomicExch(status, kBadTokenCode);
+  float out = 0.0f;
+  float ly = 0.0f;
+  if (y >= 0 && !bad) {
+    ly = stats[2 * (size_t)M + t];
+    const double z = S == 0.0 ? -INFINITY : ((double)m + log2(S)) * kLn2 - (double)ly;
+    out = (float)(z > 0.0 ? z + log1p(exp(-z)) : log1p(exp(z)));
+  }
+  stats[t] = m;
+  stats[(size_t)M + t] = (float)S;
+  stats[2 * (size_t)M + t] = ly;
+  loss[t] = out;
+}
+
+// ------------------------------------------------------------------------------------ gradient
+
+// Per-token factors of the gradient, and the largest |s_row| (bits) with a flag for negative scales.
+struct TokenFactors {
+  float4* tok;    // [M] {m, s log2 e, f s, w_y s}: f = g p_max, w_y = -g (1 - p_y)
+  double2* fac;   // [M] {f, w_y}
+  uint32_t* srow; // {bits of max |s_row|, any negative}: zero before the launch
+};
+__global__ void __launch_bounds__(256) grad_prepare_kernel(const float* __restrict__ stats,
+                                                           const int32_t* __restrict__ labels,
+                                                           const float* __restrict__ dloss,
+                                                           const double* __restrict__ s_tok, int M, int V,
+                                                           const float* __restrict__ s_row, TokenFactors o) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int i = blockIdx.x * 256 + threadIdx.x, n = gridDim.x * 256;
+  uint32_t mb = 0u, neg = 0u;
+  for (int v = i; v < V; v += n) {
+    const float s = __ldg(s_row + v);
+    mb = max(mb, __float_as_uint(s) & 0x7FFFFFFFu);  // orders like |s|, a NaN above all
+    neg |= s < 0.0f ? 1u : 0u;
+  }
+  mb = __reduce_max_sync(0xffffffffu, mb);
+  neg = __reduce_or_sync(0xffffffffu, neg);
+  if ((threadIdx.x & 31) == 0) {
+    if (mb) atomicMax(o.srow, mb);
+    if (neg) atomicOr(o.srow + 1, 1u);
+  }
+  for (int t = i; t < M; t += n) {
+    const int y = labels[t];
+    float m = stats[t];
+    const double S = (double)stats[(size_t)M + t];
+    const double ly = (double)stats[2 * (size_t)M + t];
+    double f = 0.0, wy = 0.0;
+    if (y >= 0 && y < V && S != 0.0) {
+      const double g = (double)dloss[t];
+      const double z = ((double)m + log2(S)) * kLn2 - ly;
+      const double rest = 1.0 / (1.0 + exp(-z));  // 1 - p_y
+      f = g * rest / S;
+      wy = -g * rest;
+    }
+    if (m == -INFINITY) m = 0.0f;  // no other row
+    const double s = s_tok[t];
+    // an ignored token keeps its zeros whatever its values are
+    o.tok[t] = make_float4(m, (float)s * kLog2e, f == 0.0 ? 0.0f : (float)(f * s), wy == 0.0 ? 0.0f : (float)(wy * s));
+    o.fac[t] = make_double2(f, wy);
+  }
+}
+
+// Largest coefficient in fixed point: 24 bits, one of them for the sign when a row scale is negative.  The
+// margin of 64 steps takes up the rounding of exp(l - m) just above 1.
+struct FixedPoint {
+  float unit;    // steps per unit of exp(l - m) s_row
+  float offset;  // of the stored number: 0, or 2^23 with negative scales
+  double step;   // what one step stands for
+};
+__device__ __forceinline__ FixedPoint fixed_point(const uint32_t* srow) {
+  const float smax = __uint_as_float(srow[0]);
+  const bool neg = srow[1] != 0u;
+  const float k = neg ? 8388544.0f : 16777152.0f;
+  FixedPoint p;
+  p.unit = smax == 0.0f ? 0.0f : k / smax;
+  p.offset = neg ? 8388608.0f : 0.0f;
+  p.step = p.unit == 0.0f ? 0.0 : 1.0 / (double)p.unit;
+  return p;
+}
+
+// W's piece [nv rows from v0] as K-major operand of the second product, [d / 128][Vp / 16][128][16] bytes
+// (zero past the vocabulary and past d), and the column sums of W.  A thread turns 16 rows x 4 columns.
+constexpr int TR_ROWS = 16 * 8;  // vocabulary rows per warp
+__global__ void __launch_bounds__(256) transpose_kernel(const int8_t* __restrict__ W, int V, int d, int v0, int Vp,
+                                                        int8_t* __restrict__ wt, int32_t* __restrict__ colsum) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int db = blockIdx.y, col = db * 128 + 4 * lane;
+  const int chunk0 = (blockIdx.x * 8 + warp) * (TR_ROWS / 16);
+  int sums[4] = {0, 0, 0, 0};
+  for (int i = 0; i < TR_ROWS / 16; ++i) {
+    const int chunk = chunk0 + i;
+    if (chunk * 16 >= Vp) break;
+    uint32_t w[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int v = v0 + chunk * 16 + r;
+      w[r] = (v < V && col < d) ? __ldg(reinterpret_cast<const uint32_t*>(W + (size_t)v * d + col)) : 0u;
+    }
+    uint4 o[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {  // 4 x 4 byte transpose of rows 4 g .. 4 g + 3
+      const uint32_t a = __byte_perm(w[4 * g], w[4 * g + 1], 0x5140), b = __byte_perm(w[4 * g], w[4 * g + 1], 0x7362);
+      const uint32_t e = __byte_perm(w[4 * g + 2], w[4 * g + 3], 0x5140),
+                     f = __byte_perm(w[4 * g + 2], w[4 * g + 3], 0x7362);
+      const uint32_t t[4] = {__byte_perm(a, e, 0x5410), __byte_perm(a, e, 0x7632), __byte_perm(b, f, 0x5410),
+                             __byte_perm(b, f, 0x7632)};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sums[k] = dp4a_ss(t[k], 0x01010101u, sums[k]);
+        (g == 0 ? o[k].x : g == 1 ? o[k].y : g == 2 ? o[k].z : o[k].w) = t[k];
+      }
+    }
+    uint4* dst = reinterpret_cast<uint4*>(wt + ((size_t)db * (Vp / 16) + chunk) * 2048) + 4 * lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dst[k] = o[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (col < d && sums[k]) atomicAdd(colsum + col + k, sums[k]);
+}
+
+// The first product of the gradient: digits of a piece, and the row scales' gradient per 32 tokens.
+template <bool DS>
+struct DigitPolicy {
+  struct Args {
+    CUtensorMap map_a, map_b;  // codes, W
+    RowArgs r;
+    Common c;
+    const float4* tok;      // [M]
+    const int32_t* labels;  // [M]
+    const float* s_row;     // [V]
+    const uint32_t* srow;
+    unsigned char* digits;  // [3][M / tb][Vp / 16][tb][16]
+    float* colpart;         // [ceil(M / 32)][Vp]
+    int M, v0, Vp, tb;
+    size_t plane;           // bytes of one digit's plane
+  };
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile(a.r, 0, j, t); }
+  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int kb, unsigned char* sa,
+                                              unsigned char* sb, uint64_t* bar) {
+    row_load(a.r, &a.map_a, &a.map_b, t, kb, sa, sb, bar);
+  }
+  static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
+    return umma_desc_k_sw128(addr + kk * UMMA_K);
+  }
+  static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr, int kk) {
+    return umma_desc_k_sw128(addr + kk * UMMA_K);
+  }
+  static constexpr int EPI_SMEM = EPI_WARPS * 32 * 4;
+  struct Epilogue {
+    int q, half, lane;
+    float* sr;
+    FixedPoint fp;
+    __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int half_, int lane_)
+        : q(q_), half(half_), lane(lane_), sr(reinterpret_cast<float*>(sm) + (half_ * 4 + q_) * 32),
+          fp(fixed_point(a.srow)) {}
+    __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
+      const int tk = t.a0 + q * 32 + lane;
+      const bool valid = tk < a.M;
+      const float4 tf = valid ? a.tok[tk] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const int label = valid ? a.labels[tk] - a.v0 : -1;
+      unsigned char* dst = a.digits + (size_t)(tk / a.tb) * a.tb * a.Vp + (size_t)(tk % a.tb) * 16;
+      for (int c = half * 32; c < t.nb; c += 64) {
+        uint32_t v[32];
+        tmem_ld32(taddr + (uint32_t)c, v);
+        const int v0 = t.b0 + c;  // within the piece
+        __syncwarp();
+        sr[lane] = c + lane < t.nb ? __ldg(a.s_row + a.v0 + v0 + lane) : 0.0f;
+        __syncwarp();
+        const uint32_t lc = (uint32_t)(label - v0);
+        const bool any = __any_sync(0xffffffffu, lc < 32u);
+        tmem_wait();
+        float h[32];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 w = reinterpret_cast<const float4*>(sr)[j / 4];
+          const float wv[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float av = (float)(int)v[j + k];
+            float e = ex2(fmaf(av * tf.y, wv[k], -tf.x));
+            if (DS) h[j + k] = tf.z == 0.0f ? 0.0f : tf.z * e * av;
+            if (any && (int)lc == j + k) {
+              e = 0.0f;
+              if (DS) h[j + k] = tf.w * av;
+            }
+            // rounded half to even to whole steps, kept within 24 bits
+            const float n = fminf(fmaf(e, wv[k] * fp.unit, fp.offset), 16777215.0f);
+            v[j + k] = __float2uint_rn(n);
+          }
+        }
+        if (valid) {
+          unsigned char* dp = dst + (size_t)(v0 >> 4) * a.tb * 16;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint32_t o[3][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t* x = v + 16 * g + 4 * i;
+              const uint32_t p = __byte_perm(x[0], x[1], 0x5140), r = __byte_perm(x[2], x[3], 0x5140);
+              const uint32_t u = __byte_perm(x[0], x[1], 0x0062), w = __byte_perm(x[2], x[3], 0x0062);
+              o[0][i] = __byte_perm(p, r, 0x5410) ^ 0x80808080u;
+              o[1][i] = __byte_perm(p, r, 0x7632) ^ 0x80808080u;
+              o[2][i] = __byte_perm(u, w, 0x5410) ^ 0x80808080u;
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              *reinterpret_cast<uint4*>(dp + k * a.plane + (size_t)g * a.tb * 16) =
+                  make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+          }
+        }
+        if (DS) {
+          // column sums over the warp's 32 tokens: halves exchanged at every step, lane j ends with column j
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const bool up = (lane & o) != 0;
+#pragma unroll
+            for (int j = 0; j < o; ++j) {
+              const float give = up ? h[j] : h[j + o], keep = up ? h[j + o] : h[j];
+              h[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+          }
+          if (c + lane < t.nb) a.colpart[(size_t)(t.a0 / 32 + q) * a.Vp + v0 + lane] = h[0];
+        }
+      }
+    }
+    __device__ __forceinline__ void finish(const Args&) {}
+  };
+};
+
+// The second product: accumulators [set][3][M][d] += digits x transposed W of a piece.  Lanes are columns of W
+// (128 of them), columns are tokens; the (token tile, digit, column tile, K) space is cut into one even
+// contiguous range per CTA.
+struct GradPolicy {
+  struct Args {
+    Common c;
+    const unsigned char* digits;
+    const int8_t* wt;
+    int32_t* acc;  // this piece's set: [3][M][d]
+    size_t plane;
+    int M, d, Vp, tb, kblocks;
+  };
+  static __device__ __forceinline__ void unit(const Args& a, int u, int& dt, int& dg, int& mt) {
+    const int nd = (a.d + 127) / 128;
+    dt = u % nd;
+    dg = (u / nd) % 3;
+    mt = u / (3 * nd);
+  }
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) {
+    const int nd = (a.d + 127) / 128, nt = (a.M + a.tb - 1) / a.tb;
+    const long long total = (long long)3 * nd * nt * a.kblocks;
+    const long long s0 = total * blockIdx.x / gridDim.x, s1 = total * (blockIdx.x + 1) / gridDim.x;
+    const long long u = s0 / a.kblocks + j, first = u * a.kblocks;
+    if (first >= s1 || s0 >= s1) return false;
+    t.kb0 = (int)((s0 > first ? s0 : first) - first);
+    t.kb1 = (int)((s1 < first + a.kblocks ? s1 : first + a.kblocks) - first);
+    int dt, dg, mt;
+    unit(a, (int)u, dt, dg, mt);
+    t.a0 = dt;
+    t.na = dg;
+    t.b0 = mt * a.tb;
+    t.nb = min(a.tb, a.M - t.b0);
+    return true;
+  }
+  // both operands were laid out as the product reads them: eight 16-byte K columns of all rows are contiguous
+  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int kb, unsigned char* sa,
+                                              unsigned char* sb, uint64_t* bar) {
+    const uint32_t bb = (uint32_t)a.tb * BK;
+    mbar_expect_tx(bar, A_BYTES + bb);
+    bulk_g2s(sa, a.wt + (size_t)t.a0 * 128 * a.Vp + (size_t)kb * A_BYTES, A_BYTES, bar);
+    bulk_g2s(sb, a.digits + (size_t)t.na * a.plane + (size_t)t.b0 * a.Vp + (size_t)kb * bb, bb, bar);
+  }
+  static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
+    return umma_desc_k_plain(addr + kk * 2 * (BM * 16), BM * 16);
+  }
+  static __device__ __forceinline__ uint64_t bdesc(const Args& a, uint32_t addr, int kk) {
+    return umma_desc_k_plain(addr + kk * 2 * (a.tb * 16), a.tb * 16);
+  }
+  struct Epilogue {
+    int q, half, lane;
+    __device__ __forceinline__ Epilogue(const Args&, unsigned char*, int q_, int half_, int lane_)
+        : q(q_), half(half_), lane(lane_) {}
+    __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
+      const int col = t.a0 * 128 + q * 32 + lane;
+      const bool cv = col < a.d;
+      int32_t* base = a.acc + ((size_t)t.na * a.M + t.b0) * a.d + col;
+      for (int c = half * 32; c < t.nb; c += 64) {
+        uint32_t v[32];
+        tmem_ld32(taddr + (uint32_t)c, v);
+        tmem_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (cv && c + j < t.nb) atomicAdd(base + (size_t)(c + j) * a.d, (int)v[j]);
+      }
+    }
+    __device__ __forceinline__ void finish(const Args&) {}
+  };
+};
+
+// ds_row of a piece: the partial column sums of every 32 tokens, added in order.
+__global__ void __launch_bounds__(256) ds_finish_kernel(const float* __restrict__ colpart, int parts, int Vp, int nv,
+                                                        float* __restrict__ ds) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int v = blockIdx.x * 256 + threadIdx.x;
+  if (v >= nv) return;
+  double s = 0.0;
+#pragma unroll 8
+  for (int p = 0; p < parts; ++p) s += (double)colpart[(size_t)p * Vp + v];
+  ds[v] = (float)s;
+}
+
+struct GradFinishArgs {
+  const int32_t* acc;     // [sets][3][M][d]
+  const int32_t* colsum;  // [d]
+  const uint32_t* srow;
+  const double2* fac;     // [M]
+  const int32_t* labels;
+  const int8_t* W;
+  const float* s_row;
+  const void* x;
+  const float* norm_w;
+  const float* rn;
+  void* dx;
+  float* npart;           // [gridDim.x][d] or NULL
+  int64_t ldx, lddx;
+  int M, V, d, sets;
+};
+
+// Joins the digits of a token: du = f step (sum of digits base 256 + offsets) + w_y s_row_y W_y in fp64, rounded
+// to fp32; then the norm's backward, dx = r (du w) - x r^3 / d sum(du w x).  One CTA per token at a time;
+// the norm weight's gradient is summed over the CTA's tokens in registers.
+template <typename T, int CH>
+__global__ void __launch_bounds__(256) grad_finish_kernel(GradFinishArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ double red[2][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const FixedPoint fp = fixed_point(a.srow);
+  // stored bytes are digit - 128 and the number itself is offset: both come back through W's column sums
+  const long long back = 0x808080LL - (long long)fp.offset;
+  float dn[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dn[c][k] = 0.0f;
+  int turn = 0;
+  for (int t = blockIdx.x; t < a.M; t += gridDim.x, turn ^= 1) {
+    const double2 fac = a.fac[t];
+    const int y = a.labels[t];
+    const bool kept = y >= 0 && y < a.V;
+    const double f = fac.x * fp.step, wy = kept ? fac.y * (double)__ldg(a.s_row + y) : 0.0;
+    float du[CH][8], xv[CH][8];
+    double dot = 0.0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (threadIdx.x + 256 * c) * 8;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) du[c][k] = xv[c][k] = 0.0f;
+      if (i >= a.d) continue;
+      long long sum[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] = back * (long long)a.colsum[i + k];
+      for (int s = 0; s < a.sets; ++s)
+#pragma unroll
+        for (int g = 0; g < 3; ++g) {
+          const int4* p = reinterpret_cast<const int4*>(a.acc + (((size_t)s * 3 + g) * a.M + t) * a.d + i);
+          const int4 u = p[0], w = p[1];
+          const int n[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum[k] += (long long)n[k] << (8 * g);
+        }
+      uint2 wr = make_uint2(0u, 0u);
+      if (kept) wr = __ldg(reinterpret_cast<const uint2*>(a.W + (size_t)y * a.d + i));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int w = (int)(int8_t)((k < 4 ? wr.x : wr.y) >> (8 * (k & 3)));
+        du[c][k] = kept ? (float)(f * (double)sum[k] + wy * (double)w) : 0.0f;
+      }
+      if (a.norm_w) {
+        float nw[8];
+        load8<float>(a.norm_w + i, nw);
+        load8<T>(reinterpret_cast<const T*>(a.x) + (size_t)t * a.ldx + i, xv[c]);
+        const float r = a.rn[t];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          dn[c][k] += kept ? du[c][k] * (xv[c][k] * r) : 0.0f;
+          du[c][k] *= nw[k];
+          dot += (double)du[c][k] * (double)xv[c][k];
+        }
+      }
+    }
+    if (a.norm_w) {
+      dot = warp_sum(dot);
+      if (lane == 0) red[turn][warp] = dot;
+      __syncthreads();
+      dot = 0.0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) dot += red[turn][w];
+      const float r = a.rn[t];
+      const float k3 = kept ? (float)((double)r * r * r * dot / (double)a.d) : 0.0f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) du[c][k] = kept ? fmaf(r, du[c][k], -xv[c][k] * k3) : 0.0f;
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (threadIdx.x + 256 * c) * 8;
+      if (i < a.d) store8<T>(reinterpret_cast<T*>(a.dx) + (size_t)t * a.lddx + i, du[c]);
+    }
+  }
+  if (a.npart) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (threadIdx.x + 256 * c) * 8;
+      if (i < a.d) store8<float>(a.npart + (size_t)blockIdx.x * a.d + i, dn[c]);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) dnorm_finish_kernel(const float* __restrict__ npart, int parts, int d,
+                                                           float* __restrict__ dn) {
+  pdl_launch_dependents();
+  pdl_wait();
+  // 32 columns per CTA, eight slices of the partial sums, joined in order
+  __shared__ double red[8][32];
+  const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+  double s = 0.0;
+  if (i < d)
+    for (int p = sl; p < parts; p += 8) s += (double)npart[(size_t)p * d + i];
+  red[sl][lane] = s;
+  __syncthreads();
+  if (sl == 0 && i < d) {
+    for (int k = 1; k < 8; ++k) s += red[k][lane];
+    dn[i] = (float)s;
+  }
+}
+
+// ------------------------------------------------------------------------------------ host side
+
+// Forward workspace: [status word][codes M x d][scales f64 M][partials float2 slots x M]
+struct ForwardWs {
+  size_t q, s, part, total;
+};
+int forward_slots(int V) {
+  const int grid = ceil_div(V, BN_MAX), range = ceil_div(V, 32) < kMaxRangeCtas ? ceil_div(V, 32) : kMaxRangeCtas;
+  return 2 * (grid > range ? grid : range);
+}
+ForwardWs forward_ws(int M, int d, int V) {
+  ForwardWs w;
+  w.q = kStatusBytes;
+  w.s = w.q + al256((size_t)M * d);
+  w.part = w.s + al256(sizeof(double) * (size_t)M);
+  w.total = w.part + al256(sizeof(float2) * (size_t)forward_slots(V) * M);
+  return w;
+}
+
+// The vocabulary's pieces: rows per piece (a multiple of 256), and how many accumulator sets keep the int32 sums
+// in range (|digit| <= 128, |W| <= 128: 2^14 rows-worth per row, so at most 131071 rows a set).
+struct Pieces {
+  int rows, n, per_set, sets;
+};
+constexpr size_t kPieceBytes = 80u << 20;  // digits and transposed W of a piece: they stay in the 126 MB L2
+constexpr int kSms = 148;
+Pieces pieces(int M, int d, int V) {
+  const int tb = M < BN_MAX ? (M + 15) & ~15 : BN_MAX;
+  const size_t mp = (size_t)ceil_div(M, tb) * tb, dp = (size_t)ceil_div(d, 128) * 128;
+  size_t t = kPieceBytes / (3 * mp + dp + (size_t)ceil_div(M, 32) * 4) / BN_MAX;  // tiles of 256 rows
+  if (t < 8) t = 8;
+  if (t > 256) t = 256;
+  const int vt = ceil_div(V, BN_MAX), mt = ceil_div(M, BM);
+  if ((int)t < vt) {
+    // whole waves of 128 x 256 tiles where a few fit, else equal pieces
+    int g = mt, b = kSms;
+    while (b) {
+      const int r = g % b;
+      g = b, b = r;
+    }
+    const int wave = kSms / g;
+    if (wave <= (int)t) t = t / wave * wave;
+    else t = ceil_div(vt, ceil_div(vt, (int)t));
+  } else {
+    t = vt;
+  }
+  Pieces p;
+  p.rows = (int)t * BN_MAX;
+  p.n = ceil_div(V, p.rows);
+  p.per_set = 131071 / p.rows;
+  p.sets = ceil_div(p.n, p.per_set);
+  return p;
+}
+constexpr int kNormParts = 2 * kSms;
+
+struct BackwardWs {
+  size_t q, s, rn, tok, fac, zero, srow, colsum, acc, zero_end, digits, wt, colpart, npart, total;
+};
+BackwardWs backward_ws(int M, int d, int V) {
+  const Pieces p = pieces(M, d, V);
+  const int tb = M < BN_MAX ? (M + 15) & ~15 : BN_MAX;
+  const size_t mp = (size_t)ceil_div(M, tb) * tb, dp = (size_t)ceil_div(d, 128) * 128;
+  BackwardWs w;
+  w.q = kStatusBytes;
+  w.s = w.q + al256((size_t)M * d);
+  w.rn = w.s + al256(sizeof(double) * (size_t)M);
+  w.tok = w.rn + al256(sizeof(float) * (size_t)M);
+  w.fac = w.tok + al256(sizeof(float4) * (size_t)M);
+  w.zero = w.fac + al256(sizeof(double2) * (size_t)M);
+  w.srow = w.zero;
+  w.colsum = w.srow + 256;
+  w.acc = w.colsum + al256(sizeof(int32_t) * (size_t)d);
+  w.zero_end = w.acc + al256(sizeof(int32_t) * 3 * (size_t)p.sets * M * d);
+  w.digits = w.zero_end;
+  w.wt = w.digits + al256(3 * mp * p.rows);
+  w.colpart = w.wt + al256(dp * p.rows);
+  w.npart = w.colpart + al256(sizeof(float) * 4 * (size_t)ceil_div(M, BM) * p.rows);
+  w.total = w.npart + al256(sizeof(float) * (size_t)(M < kNormParts ? M : kNormParts) * d);
+  return w;
+}
+
+// Token tiles on the lanes, rows of W on the columns: up to two token tiles stream W in balanced ranges
+// (memory bound), more take whole tiles.
+template <class A>
+int row_args(A& a, int M, int rows, int first, int d, const int8_t* W, int V, const int8_t* q, int* err) {
+  a.r.rows_a = M;
+  a.r.rows_b = rows;
+  a.r.b_first = first;
+  a.r.kblocks = ceil_div(d, BK);
+  a.r.mode = M <= 2 * BM ? kRangeB : kGrid;
+  a.r.box_a = BM;
+  a.r.box_b = a.r.mode == kRangeB ? 32 : BN_MAX;
+  a.c.b_tile = BN_MAX;
+  a.c.stages = ring_stages(BN_MAX, EPI_WARPS * 32 * 4);
+  a.c.err = err;
+  a.r.c = a.c;
+  if (!encode_u8_map_sw128(&a.map_a, q, M, d, a.r.box_a) || !encode_u8_map_sw128(&a.map_b, W, V, d, a.r.box_b))
+    return DFSSM_EUNSUPPORTED;
+  return DFSSM_OK;
+}
+int row_grid(const RowArgs& r) {
+  const long long sms = num_sms() < kMaxRangeCtas ? num_sms() : kMaxRangeCtas;
+  const long long units = r.mode == kGrid ? (long long)ceil_div(r.rows_a, BM) * ceil_div(r.rows_b, BN_MAX)
+                                          : ceil_div(r.rows_b, 32);
+  return (int)(units < sms ? units : sms);
+}
+template <class P>
+cudaError_t launch_gemm(const typename P::Args& a, int grid, int epi_smem, cudaStream_t st) {
+  const auto k = kernel<P>;
+  const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(k), SMEM_LIMIT);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, dim3(grid), dim3(THREADS), smem_bytes(a.c, epi_smem), st, a);
+}
+
+int forward(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, const double* s, int M,
+            const int32_t* labels, float* loss, float* stats, float2* part, int* err, cudaStream_t st) {
+  ForwardPolicy::Args a{};
+  const int rc = row_args(a, M, V, 0, d, W, V, q, err);
+  if (rc) return rc;
+  a.s_tok = s;
+  a.s_row = s_row;
+  a.labels = labels;
+  a.label_logit = stats + 2 * (size_t)M;
+  a.part = part;
+  a.M = M;
+  a.V = V;
+  const int grid = row_grid(a.r);
+  cudaError_t e = launch_gemm<ForwardPolicy>(a, grid, ForwardPolicy::EPI_SMEM, st);
+  const int slots = 2 * (a.r.mode == kGrid ? ceil_div(V, BN_MAX) : grid);
+  if (e == cudaSuccess)
+    e = launch_pdl(loss_finish_kernel, dim3(ceil_div(M, 32)), dim3(256), 0, st, (const float2*)part, slots, M, V,
+                   labels, stats, loss, err);
+  return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
+}
+
+template <bool DS>
+cudaError_t launch_digits(const RowArgs& r, const Common& c, const CUtensorMap& ma, const CUtensorMap& mb,
+                          const float4* tok, const int32_t* labels, const float* s_row, const uint32_t* srow,
+                          unsigned char* digits, float* colpart, int M, int v0, int Vp, int tb, size_t plane,
+                          cudaStream_t st) {
+  typename DigitPolicy<DS>::Args a{};
+  a.map_a = ma;
+  a.map_b = mb;
+  a.r = r;
+  a.c = c;
+  a.tok = tok;
+  a.labels = labels;
+  a.s_row = s_row;
+  a.srow = srow;
+  a.digits = digits;
+  a.colpart = colpart;
+  a.M = M;
+  a.v0 = v0;
+  a.Vp = Vp;
+  a.tb = tb;
+  a.plane = plane;
+  return launch_gemm<DigitPolicy<DS>>(a, row_grid(r), DigitPolicy<DS>::EPI_SMEM, st);
+}
+
+template <typename T>
+cudaError_t launch_grad_finish(const GradFinishArgs& a, int grid, cudaStream_t st) {
+  if (a.d <= 2048) return launch_pdl(grad_finish_kernel<T, 1>, dim3(grid), dim3(256), 0, st, a);
+  if (a.d <= 4096) return launch_pdl(grad_finish_kernel<T, 2>, dim3(grid), dim3(256), 0, st, a);
+  return launch_pdl(grad_finish_kernel<T, 4>, dim3(grid), dim3(256), 0, st, a);
+}
+
+inline bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+RowsQuantArgs quant_args(const void* x, int x_type, int64_t ldx, int M, int d, const float* norm_w, char* base,
+                         size_t q, size_t s) {
+  RowsQuantArgs a{};
+  a.x = x;
+  a.x_type = x_type;
+  a.ldx = ldx;
+  a.M = M;
+  a.d = d;
+  a.norm_w = norm_w;
+  a.q = reinterpret_cast<int8_t*>(base + q);
+  a.s = reinterpret_cast<double*>(base + s);
+  return a;
+}
+
+}  // namespace
+
+size_t head_loss_workspace_bytes(int M, int d, int V) { return forward_ws(M, d, V).total; }
+size_t head_loss_backward_workspace_bytes(int M, int d, int V) { return backward_ws(M, d, V).total; }
+
+}  // namespace dfssm
+
+extern "C" int dfssm_head_loss(const int8_t* W, const float* s_row, int V, int d, const void* x, int x_type,
+                               int64_t ldx, int M, const float* norm_w, const int32_t* labels, float* loss,
+                               float* stats, void* workspace, size_t ws_bytes, void* stream) {
+  using namespace dfssm;
+  int st = check_int8_matrix(W, V, d);
+  if (st) return st;
+  if (!s_row || M < 0) return DFSSM_EINVAL;
+  if (M == 0) return DFSSM_OK;
+  st = check_rows(x, x_type, ldx, d);
+  if (st) return st;
+  if (!labels || !loss || !stats) return DFSSM_EINVAL;
+  if (!al(s_row, 4) || !al(norm_w, 16) || !al(labels, 4) || !al(loss, 4) || !al(stats, 4)) return DFSSM_EALIGN;
+  const ForwardWs w = forward_ws(M, d, V);
+  if (!workspace || !al(workspace, 256) || ws_bytes < w.total) return DFSSM_EWORKSPACE;
+  if (!device_ok()) return DFSSM_EDEVICE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* base = static_cast<char*>(workspace);
+  const RowsQuantArgs qa = quant_args(x, x_type, ldx, M, d, norm_w, base, w.q, w.s);
+  const cudaError_t e = launch_rows_quant(qa, s);
+  if (e != cudaSuccess) return record_cuda_failure(e);
+  return forward(W, s_row, V, d, qa.q, qa.s, M, labels, loss, stats, reinterpret_cast<float2*>(base + w.part),
+                 reinterpret_cast<int*>(base), s);
+}
+
+extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int V, int d, const void* x,
+                                        int x_type, int64_t ldx, int M, const float* norm_w,
+                                        const int32_t* labels, const float* stats, const float* dloss, void* dx,
+                                        int64_t lddx, float* ds_row, float* dnorm_w, void* workspace,
+                                        size_t ws_bytes, void* stream) {
+  using namespace dfssm;
+  int st = check_int8_matrix(W, V, d);
+  if (st) return st;
+  if (!s_row || M < 0 || (dnorm_w && !norm_w)) return DFSSM_EINVAL;
+  if (M == 0) {  // no tokens: the sums over them are zero
+    if (!al(ds_row, 4) || !al(dnorm_w, 4)) return DFSSM_EALIGN;
+    if ((ds_row || dnorm_w) && !device_ok()) return DFSSM_EDEVICE;
+    cudaError_t e0 = cudaSuccess;
+    if (ds_row) e0 = cudaMemsetAsync(ds_row, 0, sizeof(float) * (size_t)V, static_cast<cudaStream_t>(stream));
+    if (e0 == cudaSuccess && dnorm_w)
+      e0 = cudaMemsetAsync(dnorm_w, 0, sizeof(float) * (size_t)d, static_cast<cudaStream_t>(stream));
+    return e0 == cudaSuccess ? DFSSM_OK : record_cuda_failure(e0);
+  }
+  st = check_rows(x, x_type, ldx, d);
+  if (st) return st;
+  st = check_rows(dx, x_type, lddx, d);
+  if (st) return st;
+  if (!labels || !stats || !dloss) return DFSSM_EINVAL;
+  if (!al(s_row, 4) || !al(norm_w, 16) || !al(labels, 4) || !al(stats, 4) || !al(dloss, 4) || !al(ds_row, 4) ||
+      !al(dnorm_w, 4))
+    return DFSSM_EALIGN;
+  const BackwardWs w = backward_ws(M, d, V);
+  if (!workspace || !al(workspace, 256) || ws_bytes < w.total) return DFSSM_EWORKSPACE;
+  if (!device_ok()) return DFSSM_EDEVICE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* base = static_cast<char*>(workspace);
+  int* err = reinterpret_cast<int*>(base);
+  cudaError_t e = cudaMemsetAsync(base + w.zero, 0, w.zero_end - w.zero, s);
+  if (e != cudaSuccess) return record_cuda_failure(e);
+  RowsQuantArgs qa = quant_args(x, x_type, ldx, M, d, norm_w, base, w.q, w.s);
+  qa.rn = reinterpret_cast<float*>(base + w.rn);
+  e = launch_rows_quant(qa, s);
+  if (e != cudaSuccess) return record_cuda_failure(e);
+  TokenFactors tf{reinterpret_cast<float4*>(base + w.tok), reinterpret_cast<double2*>(base + w.fac),
+                  reinterpret_cast<uint32_t*>(base + w.srow)};
+  const int work = M > V / 4 ? M : V / 4;
+  e = launch_pdl(grad_prepare_kernel, dim3(ceil_div(work, 256) < kSms ? ceil_div(work, 256) : kSms), dim3(256), 0, s,
+                 stats, labels, dloss, (const double*)qa.s, M, V, s_row, tf);
+  if (e != cudaSuccess) return record_cuda_failure(e);
+
+  const Pieces pc = pieces(M, d, V);
+  const int tb = M < BN_MAX ? (M + 15) & ~15 : BN_MAX;
+  const size_t plane = (size_t)ceil_div(M, tb) * tb * pc.rows;
+  unsigned char* digits = reinterpret_cast<unsigned char*>(base + w.digits);
+  int8_t* wt = reinterpret_cast<int8_t*>(base + w.wt);
+  float* colpart = reinterpret_cast<float*>(base + w.colpart);
+  int32_t* colsum = reinterpret_cast<int32_t*>(base + w.colsum);
+  int32_t* acc = reinterpret_cast<int32_t*>(base + w.acc);
+  for (int i = 0; i < pc.n; ++i) {
+    const int v0 = i * pc.rows, nv = V - v0 < pc.rows ? V - v0 : pc.rows;
+    const int kblocks = ceil_div(nv, BK);
+    e = launch_pdl(transpose_kernel, dim3(ceil_div(kblocks * BK, TR_ROWS * 8), ceil_div(d, 128)), dim3(256), 0, s, W, V,
+                   d, v0, pc.rows, wt, colsum);
+    if (e != cudaSuccess) return record_cuda_failure(e);
+    ForwardPolicy::Args ra{};
+    st = row_args(ra, M, nv, v0, d, W, V, qa.q, err);
+    if (st) return st;
+    e = ds_row ? launch_digits<true>(ra.r, ra.c, ra.map_a, ra.map_b, tf.tok, labels, s_row, tf.srow, digits, colpart,
+                                     M, v0, pc.rows, tb, plane, s)
+               : launch_digits<false>(ra.r, ra.c, ra.map_a, ra.map_b, tf.tok, labels, s_row, tf.srow, digits, colpart,
+                                      M, v0, pc.rows, tb, plane, s);
+    if (e != cudaSuccess) return record_cuda_failure(e);
+    if (ds_row) {
+      e = launch_pdl(ds_finish_kernel, dim3(ceil_div(nv, 256)), dim3(256), 0, s, (const float*)colpart,
+                     ceil_div(M, 32), pc.rows, nv, ds_row + v0);
+      if (e != cudaSuccess) return record_cuda_failure(e);
+    }
+    GradPolicy::Args g{};
+    g.c.b_tile = tb;
+    g.c.stages = ring_stages(tb, 0);
+    g.c.err = err;
+    g.digits = digits;
+    g.wt = wt;
+    g.acc = acc + (size_t)(i / pc.per_set) * 3 * M * d;
+    g.plane = plane;
+    g.M = M;
+    g.d = d;
+    g.Vp = pc.rows;
+    g.tb = tb;
+    g.kblocks = kblocks;
+    e = launch_gemm<GradPolicy>(g, num_sms(), 0, s);
+    if (e != cudaSuccess) return record_cuda_failure(e);
+  }
+  GradFinishArgs fa{};
+  fa.acc = acc;
+  fa.colsum = colsum;
+  fa.srow = tf.srow;
+  fa.fac = tf.fac;
+  fa.labels = labels;
+  fa.W = W;
+  fa.s_row = s_row;
+  fa.x = x;
+  fa.norm_w = norm_w;
+  fa.rn = qa.rn;
+  fa.dx = dx;
+  fa.npart = dnorm_w ? reinterpret_cast<float*>(base + w.npart) : nullptr;
+  fa.ldx = ldx;
+  fa.lddx = lddx;
+  fa.M = M;
+  fa.V = V;
+  fa.d = d;
+  fa.sets = pc.sets;
+  const int parts = M < kNormParts ? M : kNormParts;
+  e = x_type == DFSSM_BF16 ? launch_grad_finish<__nv_bfloat16>(fa, parts, s) : launch_grad_finish<float>(fa, parts, s);
+  if (e == cudaSuccess && dnorm_w)
+    e = launch_pdl(dnorm_finish_kernel, dim3(ceil_div(d, 32)), dim3(256), 0, s, (const float*)fa.npart, parts, d,
+                   dnorm_w);
+  return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
+}

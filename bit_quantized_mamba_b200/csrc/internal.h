@@ -150,6 +150,21 @@ struct EmbedArgs {
 };
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t st);
 
+// Per-token int8 quantization of M rows (natural order), see rows_quant.cu.
+struct RowsQuantArgs {
+  const void* x;          // [M] rows of d values, ldx apart, 16-byte aligned (fp32 or bf16)
+  int x_type;             // DFSSM_F32 or DFSSM_BF16
+  int64_t ldx;
+  int M, d;               // d % 16 == 0, d <= 8192
+  const float* norm_w;    // RMSNorm weight [d] or NULL
+  int8_t* q;              // [M][d]
+  double* s;              // [M] scale (the fp32 value); NaN for a token that is not finite
+  float* rn;              // [M] RMS factor or NULL
+  int8_t* dbg_q;          // optional taps
+  float* dbg_s;
+};
+cudaError_t launch_rows_quant(const RowsQuantArgs& a, cudaStream_t st);
+
 // Density-field state representation of state rows [rows][N] (8 <= N <= 256, N % 8 == 0; rows 16-byte
 // aligned): encode to field [rows][N/8] + scale [rows] (either both or neither stored) and/or write the
 // popcount readout to `out` (may equal `in`, or be NULL); decode a field back to rows.
@@ -170,6 +185,12 @@ cudaError_t set_max_dynamic_smem(const void* func, int bytes);
 namespace dfssm {
 // Prefill (tcgen05) workspace requirement for M tokens of a d_in -> d_out linear.
 size_t prefill_workspace_bytes(int M, int d_in, int d_out);
+
+// Workspace requirements of the many-token operators on an int8 matrix W [V][d], for M (n) tokens.
+size_t linear_int8_workspace_bytes(int M, int d);
+size_t head_loss_workspace_bytes(int M, int d, int V);
+size_t head_loss_backward_workspace_bytes(int M, int d, int V);
+size_t embed_backward_workspace_bytes(int n, int d, int V);
 
 // Fused persistent decode (one cooperative launch per token through all layers).
 size_t fused_decode_workspace_bytes();
@@ -196,9 +217,16 @@ int launch_linear_stream(const dfssm_linear_t* lins, int n, const float* x, int 
 int read_status_word(int* word, cudaStream_t st, int* code);
 // The no-alloc entry point's module status word on the current device.
 int noalloc_status_word(int** out);
-// A row-major u8 matrix [rows][row_bytes] (row_bytes a multiple of 128) as a TMA tensor map with boxes of
-// 128 bytes x box_rows rows and the 128-byte swizzle (16-byte chunk c of row r lands at chunk c ^ (r & 7)).
+// A row-major u8 matrix [rows][row_bytes] (row_bytes a multiple of 16) as a TMA tensor map with boxes of
+// 128 bytes x box_rows rows and the 128-byte swizzle (16-byte chunk c of row r lands at chunk c ^ (r & 7));
+// what a box covers past a row's end or the last row reads as zero.
 bool encode_u8_map_sw128(CUtensorMap* map, const void* base, int rows, int row_bytes, int box_rows);
+// Argument checks shared by the many-token operators on an int8 matrix W [V][d] (common to the embedding,
+// the linear and the loss), and of rows of d values of type x_type, ldx apart (16-byte aligned rows).
+int check_int8_matrix(const int8_t* W, int V, int d);
+int check_rows(const void* x, int x_type, int64_t ldx, int d);
+// The current device is an sm_100 part.
+bool device_ok();
 // Argument checks shared by the linear entry points (DFSSM_OK or the status to return).
 int check_linear(const dfssm_linear_t* L);
 // Records e as the text returned by dfssm_last_cuda_error (this thread) and returns DFSSM_ECUDA.

@@ -1,0 +1,163 @@
+// Many-token int8 linear (include/dfssm.h, dfssm_linear_int8): y[t][v] = fl32(acc[t][v] s[t] s_row[v]), the
+// LM head's arithmetic (technical summary §2.B: int8 LM head with per-row scaling; §2.C: per-token int8
+// activations) for any number of tokens.
+//   1. rows_quant: codes and scale of every token (with the final RMSNorm when a weight is given);
+//   2. the tcgen05 int8 product (gemm_i8.cuh) with the rows of W on the tensor memory's lanes and the tokens on
+//      its columns: a warp's store of one token covers 32 consecutive outputs, and few tokens make a narrow
+//      product (16 columns for one token), so that the stream of W alone bounds it.
+// The outputs are the head's bit for bit: the accumulators are exact, and the epilogue evaluates the
+// definition in fp64 and rounds once to fp32 (bf16 outputs round that once more).
+
+#include "gemm_i8.cuh"
+
+#include <cuda_bf16.h>
+
+namespace dfssm {
+namespace {
+
+using namespace gemm_i8;
+
+template <typename Y>
+struct LinearPolicy {
+  struct Args {
+    CUtensorMap map_a, map_b;  // W, codes
+    RowArgs r;
+    Common c;
+    const double* s_tok;  // [M]
+    const float* s_row;   // [V]
+    Y* y;
+    int64_t ldy;
+    int32_t* acc;         // [M][V] or NULL
+    int V;
+  };
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile(a.r, 1, j, t); }
+  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int kb, unsigned char* sa,
+                                              unsigned char* sb, uint64_t* bar) {
+    row_load(a.r, &a.map_a, &a.map_b, t, kb, sa, sb, bar);
+  }
+  static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
+    return umma_desc_k_sw128(addr + kk * UMMA_K);
+  }
+  static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr, int kk) {
+    return umma_desc_k_sw128(addr + kk * UMMA_K);
+  }
+  struct Epilogue {
+    int q, half, lane;
+    __device__ __forceinline__ Epilogue(const Args&, unsigned char*, int q_, int half_, int lane_)
+        : q(q_), half(half_), lane(lane_) {}
+    __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
+      const int r = q * 32 + lane, row = t.a0 + r;
+      const bool rv = r < t.na;
+      const double sw = rv ? (double)__ldg(a.s_row + row) : 0.0;
+      // columns in chunks of 16, alternating between the quadrant's two warps
+      for (int c = half * 16; c < t.nb; c += 32) {
+        uint32_t v[16];
+        tmem_ld16(taddr + (uint32_t)c, v);
+        const int n = min(16, t.nb - c);
+        const double* st = a.s_tok + t.b0 + c;
+        Y* yp = a.y + (int64_t)(t.b0 + c) * a.ldy + row;
+        double s[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[j] = j < n ? st[j] : 0.0;
+        tmem_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float out = __double2float_rn(dmul(dmul(int_to_f64((int)v[j]), s[j]), sw));
+          if (rv && j < n) yp[(int64_t)j * a.ldy] = (Y)out;
+        }
+        if (a.acc) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (rv && j < n) a.acc[(int64_t)(t.b0 + c + j) * a.V + row] = (int)v[j];
+        }
+      }
+    }
+    __device__ __forceinline__ void finish(const Args&) {}
+  };
+};
+
+inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <typename Y>
+int launch_linear(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, const double* s, int M, Y* y,
+                  int64_t ldy, int32_t* acc, int* err, cudaStream_t st) {
+  typename LinearPolicy<Y>::Args a{};
+  const int sms = num_sms();
+  a.r.rows_a = V;
+  a.r.rows_b = M;
+  a.r.kblocks = (d + BK - 1) / BK;
+  // one tile of tokens: W streams through once, in balanced ranges of rows (memory bound).  More: whole tiles
+  // of 128 x 256, the tokens' index fastest.
+  const bool range = M <= BN_MAX;
+  a.r.mode = range ? kRangeA : kGrid;
+  const int bt = range ? (M + 15) & ~15 : BN_MAX;
+  a.r.box_a = range ? 32 : BM;
+  a.r.box_b = bt;
+  a.c.b_tile = bt;
+  a.c.stages = ring_stages(bt, 0);
+  a.c.err = err;
+  a.r.c = a.c;
+  a.s_tok = s;
+  a.s_row = s_row;
+  a.y = y;
+  a.ldy = ldy;
+  a.acc = acc;
+  a.V = V;
+  if (!encode_u8_map_sw128(&a.map_a, W, V, d, a.r.box_a) || !encode_u8_map_sw128(&a.map_b, q, M, d, bt))
+    return DFSSM_EUNSUPPORTED;
+  const long long units = range ? (V + 31) / 32 : (long long)((V + BM - 1) / BM) * ((M + BN_MAX - 1) / BN_MAX);
+  const int grid = (int)(units < sms ? units : sms);
+  const auto k = kernel<LinearPolicy<Y>>;
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(k), SMEM_LIMIT);
+  if (e == cudaSuccess) e = launch_pdl(k, dim3(grid), dim3(THREADS), smem_bytes(a.c, 0), st, a);
+  return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
+}
+
+}  // namespace
+
+// [status word][codes M x d][scales f64 M]
+size_t linear_int8_workspace_bytes(int M, int d) {
+  return kStatusBytes + al256((size_t)M * d) + al256(sizeof(double) * (size_t)M);
+}
+
+}  // namespace dfssm
+
+extern "C" int dfssm_linear_int8(const int8_t* W, const float* s_row, int V, int d, const void* x, int x_type,
+                                 int64_t ldx, int M, const float* norm_w, void* y, int y_type, int64_t ldy,
+                                 void* workspace, size_t ws_bytes, const dfssm_debug_t* dbg, void* stream) {
+  using namespace dfssm;
+  int st = check_int8_matrix(W, V, d);
+  if (st) return st;
+  if (!s_row || M < 0 || ldy < V || (y_type != DFSSM_F32 && y_type != DFSSM_BF16)) return DFSSM_EINVAL;
+  if (M == 0) return DFSSM_OK;
+  st = check_rows(x, x_type, ldx, d);
+  if (st) return st;
+  if (!y) return DFSSM_EINVAL;
+  const auto al = [](const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; };
+  if (!al(s_row, 4) || !al(norm_w, 16) || !al(y, y_type == DFSSM_F32 ? 4 : 2)) return DFSSM_EALIGN;
+  if (dbg && (!al(dbg->xq, 8) || !al(dbg->xscale, 4) || !al(dbg->acc, 4))) return DFSSM_EALIGN;
+  if (!workspace || !al(workspace, 256) || ws_bytes < linear_int8_workspace_bytes(M, d)) return DFSSM_EWORKSPACE;
+  if (!device_ok()) return DFSSM_EDEVICE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* p = static_cast<char*>(workspace);
+  RowsQuantArgs qa{};
+  qa.x = x;
+  qa.x_type = x_type;
+  qa.ldx = ldx;
+  qa.M = M;
+  qa.d = d;
+  qa.norm_w = norm_w;
+  qa.q = reinterpret_cast<int8_t*>(p + kStatusBytes);
+  qa.s = reinterpret_cast<double*>(p + kStatusBytes + al256((size_t)M * d));
+  if (dbg) {
+    qa.dbg_q = dbg->xq;
+    qa.dbg_s = dbg->xscale;
+  }
+  const cudaError_t e = launch_rows_quant(qa, s);
+  if (e != cudaSuccess) return record_cuda_failure(e);
+  int32_t* acc = dbg ? dbg->acc : nullptr;
+  int* err = reinterpret_cast<int*>(p);
+  if (y_type == DFSSM_F32)
+    return launch_linear<float>(W, s_row, V, d, qa.q, qa.s, M, static_cast<float*>(y), ldy, acc, err, s);
+  return launch_linear<__nv_bfloat16>(W, s_row, V, d, qa.q, qa.s, M, static_cast<__nv_bfloat16*>(y), ldy, acc, err, s);
+}

@@ -23,6 +23,11 @@ OP_GENERATE = 6
 OP_LAYER_PREFILL = 7
 OP_LINEAR_MULTI = 8
 OP_EMBED = 9
+OP_LINEAR_INT8 = 10
+OP_EMBED_TOKENS = 11
+OP_EMBED_BACKWARD = 12
+OP_HEAD_LOSS = 13
+OP_HEAD_LOSS_BACKWARD = 14
 MAX_RANK = 16
 MAX_BATCH = 16
 MAX_LAYERS = 64
@@ -65,7 +70,7 @@ class LayerT(C.Structure):
 _lib = None
 
 # name -> (restype, argtypes); every function that include/dfssm.h declares.
-_P, _I, _Z = C.c_void_p, C.c_int, C.c_size_t
+_P, _I, _Z, _L = C.c_void_p, C.c_int, C.c_size_t, C.c_int64
 SIGNATURES = {
     "dfssm_workspace_size": (_Z, [_I, _I, _I, _I]),
     "dfssm_linear_decode": (_I, [_P, _P, _I, _P, _P, _Z, _P, _P]),
@@ -83,6 +88,12 @@ SIGNATURES = {
     "dfssm_state_field_encode": (_I, [_P, _I, _I, _P, _P, _P]),
     "dfssm_state_field_decode": (_I, [_P, _P, _I, _I, _P, _P]),
     "dfssm_state_field_roundtrip": (_I, [_P, _I, _I, _P, _P, _P]),
+    "dfssm_linear_int8": (_I, [_P, _P, _I, _I, _P, _I, _L, _I, _P, _P, _I, _L, _P, _Z, _P, _P]),
+    "dfssm_embed_tokens": (_I, [_P, _P, _I, _I, _P, _I, _P, _I, _L, _P, _Z, _P]),
+    "dfssm_embed_tokens_backward": (_I, [_P, _I, _I, _P, _I, _P, _I, _L, _P, _P, _I, _P, _Z, _P]),
+    "dfssm_head_loss": (_I, [_P, _P, _I, _I, _P, _I, _L, _I, _P, _P, _P, _P, _P, _Z, _P]),
+    "dfssm_head_loss_backward": (_I, [_P, _P, _I, _I, _P, _I, _L, _I, _P, _P, _P, _P, _P, _L, _P, _P, _P, _Z,
+                                      _P]),
     "dfssm_pack_signs": (_I, [_P, _I, _I, _P]),
     "dfssm_device_status": (_I, [_P, _P]),
     "dfssm_selftest_timeout": (_I, [_P, _Z, _P]),
@@ -456,6 +467,175 @@ def generate(stack: "LayerStack", W, s_row, final_norm_w, tokens, hidden_taps=No
         _ptr(tokens), n, stack.c()[1], stack.c()[2], _ptr(hidden_taps), _ptr(logits), _ptr(ws),
         ws.numel(), _stream(stream)))
     return tokens
+
+
+# ------------------------------------------------------- many tokens on the int8 matrix (embedding / LM head)
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _on(stream, *tensors):
+    """The handle of the call's stream, after checking that every tensor lives on the current device (the
+    library takes plain pointers and launches there)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}" if t.is_cuda
+                             else "expected a CUDA tensor")
+    return _stream(stream)
+
+
+def _new(stream, shape, dtype, device, zero=False):
+    """A tensor allocated on the call's stream, so that its memory is not reused while the call still runs."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _ws(ws, stream, op, a, b, c, device):
+    if ws is not None:
+        return ws
+    return _new(stream, max(workspace_size(op, a, b, c), 256), torch.uint8, device, zero=True)
+
+
+def _rows(t, shape, what):
+    """Pointer, type code and row stride of a 2-D tensor of rows (unit stride within a row)."""
+    if t.dtype not in _TYPES:
+        raise ValueError(f"{what} must be float32 or bfloat16, not {t.dtype}")
+    if t.dim() != 2 or tuple(t.shape) != shape:
+        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have unit stride within a row")
+    return t.data_ptr(), _TYPES[t.dtype], t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _vector(t, n, dtype, what):
+    """Pointer of a contiguous vector (or None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _matrix(W):
+    if W.dtype != torch.int8 or W.dim() != 2 or not W.is_contiguous():
+        raise ValueError("W must be a contiguous int8 matrix")
+    return W.shape
+
+
+def linear_int8(W, s_row, x, y=None, norm_w=None, out_dtype=torch.float32, ws=None, debug=None, stream=None):
+    """y [M][V] = the int8 head's product for every row of x [M][d] (dfssm_linear_int8); x f32 or bf16, rows may
+    be strided.  debug: dict of optional taps acc [M][V], xq [M][d], xscale [M]."""
+    V, d = _matrix(W)
+    M = x.shape[0]
+    st = _on(stream, W, s_row, x, y, norm_w, ws)
+    if y is None:
+        y = _new(stream, (M, V), out_dtype, x.device)
+    ws = _ws(ws, stream, OP_LINEAR_INT8, M, d, V, x.device)
+    dbg = None
+    if debug is not None:
+        dbg = DebugT(_vector(debug.get("acc"), M * V, torch.int32, "acc"), None,
+                     _vector(debug.get("xq"), M * d, torch.int8, "xq"),
+                     _vector(debug.get("xscale"), M, torch.float32, "xscale"))
+    px, tx, lx = _rows(x, (M, d), "x")
+    py, ty, ly = _rows(y, (M, V), "y")
+    _check("dfssm_linear_int8", lib().dfssm_linear_int8(
+        W.data_ptr(), _vector(s_row, V, torch.float32, "s_row"), V, d, px, tx, lx, M,
+        _vector(norm_w, d, torch.float32, "norm_w"), py, ty, ly, ws.data_ptr(), ws.numel(),
+        C.byref(dbg) if dbg is not None else None, st))
+    return y
+
+
+def embed_tokens(W, s_row, tokens, h=None, dtype=torch.float32, ws=None, stream=None):
+    """Rows tokens [n] (device int32) of the tied int8 embedding, dequantised (dfssm_embed_tokens).  ws (optional)
+    holds the call's status word (an out-of-range id is reported there)."""
+    V, d = _matrix(W)
+    n = tokens.numel()
+    st = _on(stream, W, s_row, tokens, h, ws)
+    if h is None:
+        h = _new(stream, (n, d), dtype, W.device)
+    ws = _ws(ws, stream, OP_EMBED_TOKENS, 0, 0, 0, W.device)
+    ph, th, lh = _rows(h, (n, d), "h")
+    _check("dfssm_embed_tokens", lib().dfssm_embed_tokens(
+        W.data_ptr(), _vector(s_row, V, torch.float32, "s_row"), V, d, _vector(tokens, n, torch.int32, "tokens"),
+        n, ph, th, lh, ws.data_ptr(), ws.numel(), st))
+    return h
+
+
+def embed_tokens_backward(W, tokens, dh, dE=None, ds_row=None, accumulate=False, ws=None, stream=None):
+    """Gradients of embed_tokens for dh [n][d]: (dE [V][d], ds_row [V]) (dfssm_embed_tokens_backward).  With
+    accumulate the sums are added to the tensors given (either may be left out); otherwise both are written,
+    into new tensors where none are given."""
+    V, d = _matrix(W)
+    n = tokens.numel()
+    st = _on(stream, W, tokens, dh, dE, ds_row, ws)
+    if accumulate:
+        if dE is None and ds_row is None:
+            raise ValueError("accumulate needs dE or ds_row")
+    else:
+        if dE is None:
+            dE = _new(stream, (V, d), torch.float32, W.device)
+        if ds_row is None:
+            ds_row = _new(stream, (V,), torch.float32, W.device)
+    ws = _ws(ws, stream, OP_EMBED_BACKWARD, n, d, V, W.device)
+    pd, td, ld = _rows(dh, (n, d), "dh")
+    _check("dfssm_embed_tokens_backward", lib().dfssm_embed_tokens_backward(
+        W.data_ptr(), V, d, _vector(tokens, n, torch.int32, "tokens"), n, pd, td, ld,
+        _vector(dE, V * d, torch.float32, "dE"), _vector(ds_row, V, torch.float32, "ds_row"), int(accumulate),
+        ws.data_ptr(), ws.numel(), st))
+    return dE, ds_row
+
+
+def head_loss(W, s_row, x, labels, norm_w=None, loss=None, stats=None, ws=None, stream=None):
+    """Cross entropy of the int8 head's logits for every row of x [M][d] (dfssm_head_loss); labels device int32
+    [M], negative = ignored.  Returns (loss [M], stats [3][M]); stats is what head_loss_backward needs."""
+    V, d = _matrix(W)
+    M = x.shape[0]
+    st = _on(stream, W, s_row, x, labels, norm_w, loss, stats, ws)
+    if loss is None:
+        loss = _new(stream, (M,), torch.float32, x.device)
+    if stats is None:
+        stats = _new(stream, (3, M), torch.float32, x.device)
+    ws = _ws(ws, stream, OP_HEAD_LOSS, M, d, V, x.device)
+    px, tx, lx = _rows(x, (M, d), "x")
+    _check("dfssm_head_loss", lib().dfssm_head_loss(
+        W.data_ptr(), _vector(s_row, V, torch.float32, "s_row"), V, d, px, tx, lx, M,
+        _vector(norm_w, d, torch.float32, "norm_w"), _vector(labels, M, torch.int32, "labels"),
+        _vector(loss, M, torch.float32, "loss"), _vector(stats, 3 * M, torch.float32, "stats"),
+        ws.data_ptr(), ws.numel(), st))
+    return loss, stats
+
+
+def head_loss_backward(W, s_row, x, labels, stats, dloss, norm_w=None, dx=None, ds_row=None, dnorm_w=None,
+                       scales=True, ws=None, stream=None):
+    """Gradients of sum(dloss * loss) (dfssm_head_loss_backward): (dx [M][d] of x's type, ds_row [V],
+    dnorm_w [d]).  scales=False leaves out ds_row (None unless a tensor is given); dnorm_w is None without
+    norm_w."""
+    V, d = _matrix(W)
+    M = x.shape[0]
+    st = _on(stream, W, s_row, x, labels, stats, dloss, norm_w, dx, ds_row, dnorm_w, ws)
+    if dx is None:
+        dx = _new(stream, (M, d), x.dtype, x.device)
+    if ds_row is None and scales:
+        ds_row = _new(stream, (V,), torch.float32, x.device)
+    if dnorm_w is None and norm_w is not None:
+        dnorm_w = _new(stream, (d,), torch.float32, x.device)
+    ws = _ws(ws, stream, OP_HEAD_LOSS_BACKWARD, M, d, V, x.device)
+    px, tx, lx = _rows(x, (M, d), "x")
+    pd, td, ld = _rows(dx, (M, d), "dx")
+    if td != tx:
+        raise ValueError("dx must have x's type")
+    _check("dfssm_head_loss_backward", lib().dfssm_head_loss_backward(
+        W.data_ptr(), _vector(s_row, V, torch.float32, "s_row"), V, d, px, tx, lx, M,
+        _vector(norm_w, d, torch.float32, "norm_w"), _vector(labels, M, torch.int32, "labels"),
+        _vector(stats, 3 * M, torch.float32, "stats"), _vector(dloss, M, torch.float32, "dloss"), pd, ld,
+        _vector(ds_row, V, torch.float32, "ds_row"), _vector(dnorm_w, d, torch.float32, "dnorm_w"),
+        ws.data_ptr(), ws.numel(), st))
+    return dx, ds_row, dnorm_w
 
 
 def pack_signs(signs: np.ndarray) -> np.ndarray:

@@ -18,7 +18,8 @@
  *   - Device-side errors (a wait that ran out of its clock budget, an embedding id out of range) are
  *     recorded in a status word at the start of the call's workspace (for dfssm_linear_decode,
  *     dfssm_linear_decode_multi, dfssm_linear_prefill, dfssm_embed, dfssm_layer_decode,
- *     dfssm_layer_prefill and dfssm_generate), read and cleared by dfssm_device_status.
+ *     dfssm_layer_prefill, dfssm_generate and the many-token calls on the int8 matrix), read and cleared by
+ *     dfssm_device_status.
  *   - Every call is asynchronous on `stream` (a cudaStream_t; NULL = legacy default stream).  Inputs
  *     must not be modified, and outputs not read, until the stream reaches the call.  Weights and
  *     parameters must be fully written before the call is enqueued (kernels may read them before they
@@ -106,7 +107,12 @@ enum {
   DFSSM_OP_GENERATE = 6,       /* a = V,  b = d_model, c = d_inner                     */
   DFSSM_OP_LAYER_PREFILL = 7,  /* a = M,  b = d_model, c = d_inner                     */
   DFSSM_OP_LINEAR_MULTI = 8,   /* (no size arguments): the status word only             */
-  DFSSM_OP_EMBED = 9           /* (no size arguments): the status word only             */
+  DFSSM_OP_EMBED = 9,          /* (no size arguments): the status word only             */
+  DFSSM_OP_LINEAR_INT8 = 10,   /* a = M,  b = d,     c = V                             */
+  DFSSM_OP_EMBED_TOKENS = 11,  /* (no size arguments): the status word only             */
+  DFSSM_OP_EMBED_BACKWARD = 12, /* a = n, b = d,     c = V                             */
+  DFSSM_OP_HEAD_LOSS = 13,     /* a = M,  b = d,     c = V                             */
+  DFSSM_OP_HEAD_LOSS_BACKWARD = 14 /* a = M, b = d,  c = V                             */
 };
 size_t dfssm_workspace_size(int op, int a, int b, int c);
 
@@ -333,6 +339,90 @@ int dfssm_generate(const dfssm_layer_t* layers, int n_layers, const dfssm_dims_t
                    const int8_t* W, const float* s_row, int V, const float* final_norm_w,
                    int32_t* tokens, int n_tokens, float* const* conv_states, float* const* ssm_states,
                    float* hidden_taps, float* logits, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Many tokens on the int8 matrix W [V][d] (the tied embedding / LM head, technical summary §2.B, or any int8
+ * matrix with a scale per row): the lookup, the product, the loss over the vocabulary, and the gradients.
+ * Common to these calls:
+ *   W device i8 [V][d] (16-byte aligned), s_row device f32 [V]; d % 16 == 0, d >= 16 (otherwise DFSSM_EINVAL),
+ *   d <= 8192 (otherwise DFSSM_EUNSUPPORTED).
+ *   Activations are rows of d values of type DFSSM_F32 or DFSSM_BF16, ld* elements apart (ld* >= d, else
+ *   DFSSM_EINVAL), every row 16-byte aligned (else DFSSM_EALIGN); values between rows are neither read nor
+ *   written.  Outputs must not overlap inputs or each other.
+ *   Zero tokens are valid: nothing is read or launched, pointers to the tokens' data may be NULL; sums over
+ *   the tokens (dE, ds_row, dnorm_w) are then written zero.
+ *   Results do not depend on the run: every sum is taken in a fixed order or in integers.
+ *   Calls are stream-ordered and can be captured in a CUDA graph (after one call outside a capture on the
+ *   device); every call needs a workspace of its own kind and size that no other call uses at the same time.
+ */
+enum { DFSSM_F32 = 0, DFSSM_BF16 = 1 };
+
+/*
+ * Int8 linear of M tokens: y[t][v] = fl32(acc[t][v] s[t] s_row[v]) (fp64, this order), acc = W q (int32, exact),
+ * with (q, s) the per-token absmax int8 quantization of x, as dfssm_lm_head for one token, bit for bit.
+ *   norm_w device f32 [d] (16-byte aligned) or NULL: the tokens are first RMS-normalised as in
+ *   dfssm_head_greedy.  y [M][V] of type y_type, rows ldy >= V elements apart (element alignment); bf16
+ *   outputs are the fp32 result rounded once more.  A token that holds an infinity or a NaN gives NaN outputs.
+ *   dbg (may be NULL): acc [M][V], xq [M][d] (8-byte aligned) and xscale [M] are written; lora_t is not.
+ *   M = 1 is a stream of W; M in the hundreds is bound by the tensor cores.
+ *   workspace: dfssm_workspace_size(DFSSM_OP_LINEAR_INT8, M, d, V).
+ */
+int dfssm_linear_int8(const int8_t* W, const float* s_row, int V, int d, const void* x, int x_type, int64_t ldx,
+                      int M, const float* norm_w, void* y, int y_type, int64_t ldy, void* workspace,
+                      size_t ws_bytes, const dfssm_debug_t* dbg, void* stream);
+
+/*
+ * Embedding of n tokens: h[t][i] = fl32(W[tokens[t]][i] s_row[tokens[t]]) (as dfssm_embed for one), rounded once
+ * more for h_type DFSSM_BF16.  tokens device i32 [n].  A token outside [0, V) gives a zero row and
+ * DFSSM_EINVAL from dfssm_device_status.  workspace: dfssm_workspace_size(DFSSM_OP_EMBED_TOKENS, 0, 0, 0).
+ */
+int dfssm_embed_tokens(const int8_t* W, const float* s_row, int V, int d, const int32_t* tokens, int n, void* h,
+                       int h_type, int64_t ldh, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of dfssm_embed_tokens:
+ *   dE[v][i] = sum_{t: tokens[t] = v} dh[t][i]   (of the dequantised table; device f32 [V][d], 16-byte aligned)
+ *   ds_row[v] = sum_i W[v][i] dE[v][i]           (of the row scales; device f32 [V])
+ * Either output may be NULL, not both.  accumulate = 0: every element of the outputs is written (zero for
+ * tokens that do not occur).  accumulate != 0: the sums are added to the outputs, and rows of tokens that do not
+ * occur are not touched.  A token outside [0, V) contributes nothing and gives DFSSM_EINVAL from
+ * dfssm_device_status.  Sums are fp32, by increasing t within fixed groups of equal tokens.
+ * workspace: dfssm_workspace_size(DFSSM_OP_EMBED_BACKWARD, n, d, V).
+ */
+int dfssm_embed_tokens_backward(const int8_t* W, int V, int d, const int32_t* tokens, int n, const void* dh,
+                                int dh_type, int64_t lddh, float* dE, float* ds_row, int accumulate,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Softmax cross entropy of the int8 head's logits l[t][v] = acc[t][v] s[t] s_row[v] (dfssm_linear_int8, the final
+ * norm included when norm_w is given), without storing them:
+ *   loss[t] = log sum_v exp l[t][v] - l[t][labels[t]]     device f32 [M]
+ * labels device i32 [M]; a negative label is ignored (loss 0, no gradient), one >= V is ignored too and gives
+ * DFSSM_EINVAL from dfssm_device_status.  A token that holds an infinity or a NaN has loss NaN.
+ * stats device f32 [3][M] receives what dfssm_head_loss_backward needs (opaque).
+ * workspace: dfssm_workspace_size(DFSSM_OP_HEAD_LOSS, M, d, V).
+ */
+int dfssm_head_loss(const int8_t* W, const float* s_row, int V, int d, const void* x, int x_type, int64_t ldx,
+                    int M, const float* norm_w, const int32_t* labels, float* loss, float* stats,
+                    void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of sum_t dloss[t] loss[t] (dloss device f32 [M]) for the same W, s_row, x, norm_w and labels, with
+ * stats from dfssm_head_loss.  With G[t][v] = dloss[t] (softmax(l[t])[v] - [v = labels[t]]):
+ *   du[t] = sum_v G[t][v] s_row[v] W[v]; the int8 rounding of the activations counts as the identity
+ *   (straight-through), so without norm_w dx = du; with it, r = 1 / rms(x) as in the forward call,
+ *   dx = r (du norm_w) - x r^3 / d sum_i(du norm_w x).   dx rows of x's type, lddx apart.
+ *   ds_row[v] = sum_t G[t][v] acc[t][v] s[t]     device f32 [V] or NULL (not computed)
+ *   dnorm_w[i] = sum_t du[t][i] x[t][i] r[t]     device f32 [d] or NULL (not computed; needs norm_w)
+ * W's codes are frozen integers and get no gradient.  Within du the coefficients softmax s_row are rounded to 24
+ * bits of their largest possible value in the token (23 and a sign when a row scale is negative), and
+ * everything after that is exact up to the final rounding.
+ * workspace: dfssm_workspace_size(DFSSM_OP_HEAD_LOSS_BACKWARD, M, d, V).
+ */
+int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int V, int d, const void* x, int x_type,
+                             int64_t ldx, int M, const float* norm_w, const int32_t* labels, const float* stats,
+                             const float* dloss, void* dx, int64_t lddx, float* ds_row, float* dnorm_w,
+                             void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Device-side failure detection.  The fused decode kernel of dfssm_layer_decode (batch 1, Mamba-2-1.3B
