@@ -12,17 +12,18 @@
 // token, tile and column half; a second kernel joins them.
 //
 // Gradient with respect to the (dequantised) normalised token:  du = g [sum_{v != y} p_v s_row_v W_v -
-// (1 - p_y) s_row_y W_y].  The coefficients c_v = exp(l_v - m) s_row_v / max|s_row| lie in [0, 1] (or [-1, 1]
-// with negative scales) whatever the token, so they are rounded to 24-bit fixed point (half a step: 2^-25 of
-// the largest possible coefficient) and split into three base-256 digits: the sum over v becomes three exact
-// int8 products with W, twice the rate of one bf16 product each and free of the bf16 rounding and of the
-// order of summation.  The vocabulary is taken in pieces whose digits stay in L2:
+// (1 - p_y) s_row_y W_y].  The coefficients c_v = exp(l_v - m) s_row_v / max|s_row| lie in [0, 1] (or [-1, 1] with
+// negative scales) whatever the token.  They are written in fixed point, in steps of 2^-24 tau with
+// tau = 2^-k ~ min(1, S / 16): below tau a coefficient is three base-256 digits, and at most 16 of a token's can
+// be above it (they sum to at most S), whose further bits go into a list.  The sum over v is then three exact
+// int8 products of digits with W, each at twice the rate of a bf16 product, free of bf16's rounding and of any
+// order of summation, and a few listed rows of W.  The vocabulary is taken in pieces whose digits stay in L2:
 //   1. transpose: the piece's W as K-major operand of the second product, and W's column sums;
 //   2. the first product again, its epilogue turning logits into digits (and the row scales' gradient
 //      into partial column sums);
 //   3. the second product: digits x transposed W, added to int32 accumulators in memory by integer
 //      atomics (any order gives the same sum), the (tile, digit, K) space split evenly over the CTAs.
-// At the end one kernel joins the digits and the label's row in fp64 and applies the norm's backward.
+// At the end one kernel joins the digits, the listed rows and the label's row and applies the norm's backward.
 // The digits are stored as signed bytes (digit - 128); the column sums of W give the 128s back.
 
 #include "gemm_i8.cuh"
@@ -33,7 +34,7 @@ namespace {
 
 using namespace gemm_i8;
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLog2e = 1.4426950408889634074;
 constexpr double kLn2 = 0.69314718055994530942;
 constexpr int kMaxRangeCtas = 160;  // partial slots are sized without asking the device
 
@@ -45,6 +46,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// Row scale in units of log 2: the logits' base-2 exponents are then acc s scale2, and the one rounding that
+// log2 e brings differs from row to row (in the token's scale it would be one factor on all its logits: losses
+// 4.0e-8 off instead of 3.4e-8).
+__device__ __forceinline__ float scale2(float s_row) { return __double2float_rn((double)s_row * kLog2e); }
 
 // ------------------------------------------------------------------------------------ forward
 
@@ -74,7 +80,7 @@ struct ForwardPolicy {
   static constexpr int EPI_SMEM = EPI_WARPS * 32 * 4;
   struct Epilogue {
     int q, half, lane;
-    float* sr;        // this warp's 32 row scales of a chunk
+    float* sr;        // this warp's 32 row scales of a chunk, in units of log 2
     int tok = -1;     // the token whose running (m, S) this thread holds
     int slot = 0;
     float m = -INFINITY, S = 0.0f;
@@ -94,14 +100,14 @@ struct ForwardPolicy {
         slot = sl;
       }
       const bool valid = tk < a.M;
-      const float s2 = valid ? (float)a.s_tok[tk] * kLog2e : 0.0f;
+      const float st = valid ? (float)a.s_tok[tk] : 0.0f;
       const int label = valid ? a.labels[tk] : -1;
       for (int c = half * 32; c < t.nb; c += 64) {
         uint32_t v[32];
         tmem_ld32(taddr + (uint32_t)c, v);
         const int v0 = t.b0 + c;
         __syncwarp();
-        sr[lane] = c + lane < t.nb ? __ldg(a.s_row + v0 + lane) : 0.0f;
+        sr[lane] = c + lane < t.nb ? scale2(__ldg(a.s_row + v0 + lane)) : 0.0f;
         __syncwarp();
         // columns that do not count: past the tile's end, and the token's own label
         uint32_t skip = c + 32 > t.nb ? 0xFFFFFFFFu << (t.nb - c) : 0u;
@@ -110,13 +116,13 @@ struct ForwardPolicy {
         tmem_wait();
         float x[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = (float)(int)v[j] * s2;
+        for (int j = 0; j < 32; ++j) x[j] = (float)(int)v[j] * st;
         if (lc < 32u && c + (int)lc < t.nb) {
           int al = 0;
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (j == (int)lc) al = (int)v[j];
-          a.label_logit[tk] = __double2float_rn(dmul(dmul(int_to_f64(al), a.s_tok[tk]), (double)sr[lc]));
+          a.label_logit[tk] = __double2float_rn(dmul(dmul(int_to_f64(al), a.s_tok[tk]), (double)__ldg(a.s_row + label)));
         }
         float mx = m;
         const float4* sr4 = reinterpret_cast<const float4*>(sr);
@@ -203,9 +209,12 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const float2* __restri
 
 // ------------------------------------------------------------------------------------ gradient
 
+constexpr int kListed = 16;  // coefficients of a token that may need more than 24 bits
+
 // Per-token factors of the gradient, and the largest |s_row| (bits) with a flag for negative scales.
 struct TokenFactors {
-  float4* tok;    // [M] {m, s log2 e, f s, w_y s}: f = g p_max, w_y = -g (1 - p_y)
+  float4* tok;    // [M] {m', s, f s, w_y s}: m' = m - k, f = g p_max 2^-k, w_y = -g (1 - p_y)
+  int* shift;     // [M] k
   double2* fac;   // [M] {f, w_y}
   uint32_t* srow; // {bits of max |s_row|, any negative}: zero before the launch
 };
@@ -235,37 +244,53 @@ __global__ void __launch_bounds__(256) grad_prepare_kernel(const float* __restri
     const double S = (double)stats[(size_t)M + t];
     const double ly = (double)stats[2 * (size_t)M + t];
     double f = 0.0, wy = 0.0;
+    int k = 0;
     if (y >= 0 && y < V && S != 0.0) {
       const double g = (double)dloss[t];
       const double z = ((double)m + log2(S)) * kLn2 - ly;
       const double rest = 1.0 / (1.0 + exp(-z));  // 1 - p_y
       f = g * rest / S;
       wy = -g * rest;
+      while (k < 4 && S * (double)(2 << k) <= (double)kListed) ++k;  // S 2^k <= 16
+      const float mk = m - (float)k;
+      f *= exp2((double)mk - (double)m);
+      m = mk;
     }
     if (m == -INFINITY) m = 0.0f;  // no other row
+    o.shift[t] = k;
     const double s = s_tok[t];
     // an ignored token keeps its zeros whatever its values are
-    o.tok[t] = make_float4(m, (float)s * kLog2e, f == 0.0 ? 0.0f : (float)(f * s), wy == 0.0 ? 0.0f : (float)(wy * s));
+    o.tok[t] = make_float4(m, (float)s, f == 0.0 ? 0.0f : (float)(f * s), wy == 0.0 ? 0.0f : (float)(wy * s));
     o.fac[t] = make_double2(f, wy);
   }
 }
 
-// Largest coefficient in fixed point: 24 bits, one of them for the sign when a row scale is negative.  The
-// margin of 64 steps takes up the rounding of exp(l - m) just above 1.
+// Fixed point: steps per unit of coefficient.  A number n is stored as n + offset, its low 24 bits as digits;
+// numbers up to 2^24 tau need no more (2^23 with negative scales, which take the sign's bit).  The margin of 64
+// steps takes up the rounding of exp(l - m) just above 1.
 struct FixedPoint {
-  float unit;    // steps per unit of exp(l - m) s_row
-  float offset;  // of the stored number: 0, or 2^23 with negative scales
-  double step;   // what one step stands for
+  float unit;    // steps per unit of exp(l - m') scale2(s_row)
+  int offset;    // 0, or 2^23 with negative scales
+  int range;     // 2^24, or 2^23
+  double step;   // what one step stands for, of exp(l - m') s_row
 };
 __device__ __forceinline__ FixedPoint fixed_point(const uint32_t* srow) {
   const float smax = __uint_as_float(srow[0]);
   const bool neg = srow[1] != 0u;
-  const float k = neg ? 8388544.0f : 16777152.0f;
   FixedPoint p;
-  p.unit = smax == 0.0f ? 0.0f : k / smax;
-  p.offset = neg ? 8388608.0f : 0.0f;
-  p.step = p.unit == 0.0f ? 0.0 : 1.0 / (double)p.unit;
+  p.range = neg ? 1 << 23 : 1 << 24;
+  p.unit = smax == 0.0f ? 0.0f : (float)(p.range - 64) / scale2(smax);
+  p.offset = neg ? 1 << 23 : 0;
+  p.step = p.unit == 0.0f ? 0.0 : 1.0 / ((double)p.unit * kLog2e);
   return p;
+}
+
+// Pseudo-random number in [-1/2, 1/2) of an accumulator, added before the coefficient is rounded to whole steps:
+// the rounding is then right on average for coefficients of any size.  (Rounded to nearest, the thousands of
+// coefficients below half a step all become zero, which sums over tokens show: 4e-6 of the norm weight's
+// gradient at 2048 tokens x 50288 rows.)
+__device__ __forceinline__ float dither(uint32_t acc) {
+  return __uint_as_float(((acc * 0x9E3779B1u) & 0x7FFFFFu) | 0x3F800000u) - 1.5f;
 }
 
 // W's piece [nv rows from v0] as K-major operand of the second product, [d / 128][Vp / 16][128][16] bytes
@@ -322,6 +347,9 @@ struct DigitPolicy {
     const int32_t* labels;  // [M]
     const float* s_row;     // [V]
     const uint32_t* srow;
+    const int* shift;       // [M]
+    int* listed;            // [M] entries of a token's list, zero before the first piece
+    int2* list;             // [M][kListed] {row of W, number / 2^24}
     unsigned char* digits;  // [3][M / tb][Vp / 16][tb][16]
     float* colpart;         // [ceil(M / 32)][Vp]
     int M, v0, Vp, tb;
@@ -351,18 +379,20 @@ struct DigitPolicy {
       const bool valid = tk < a.M;
       const float4 tf = valid ? a.tok[tk] : make_float4(0.f, 0.f, 0.f, 0.f);
       const int label = valid ? a.labels[tk] - a.v0 : -1;
+      const int most = (fp.range << (valid ? a.shift[tk] : 0)) - 1;
       unsigned char* dst = a.digits + (size_t)(tk / a.tb) * a.tb * a.Vp + (size_t)(tk % a.tb) * 16;
       for (int c = half * 32; c < t.nb; c += 64) {
         uint32_t v[32];
         tmem_ld32(taddr + (uint32_t)c, v);
         const int v0 = t.b0 + c;  // within the piece
         __syncwarp();
-        sr[lane] = c + lane < t.nb ? __ldg(a.s_row + a.v0 + v0 + lane) : 0.0f;
+        sr[lane] = c + lane < t.nb ? scale2(__ldg(a.s_row + a.v0 + v0 + lane)) : 0.0f;
         __syncwarp();
         const uint32_t lc = (uint32_t)(label - v0);
         const bool any = __any_sync(0xffffffffu, lc < 32u);
         tmem_wait();
         float h[32];
+        uint32_t high = 0u;
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
           const float4 w = reinterpret_cast<const float4*>(sr)[j / 4];
@@ -376,9 +406,22 @@ struct DigitPolicy {
               e = 0.0f;
               if (DS) h[j + k] = tf.w * av;
             }
-            // rounded half to even to whole steps, kept within 24 bits
-            const float n = fminf(fmaf(e, wv[k] * fp.unit, fp.offset), 16777215.0f);
-            v[j + k] = __float2uint_rn(n);
+            const float n = fmaf(e, wv[k] * fp.unit, dither(v[j + k]));
+            v[j + k] = (uint32_t)(min(__float2int_rn(n), most) + fp.offset);
+            high |= v[j + k];
+          }
+        }
+        if (valid && (high >> 24)) {
+          // few: the order of a list does not matter, its sum is taken in integers
+          for (int j = 0; j < 32; ++j) {
+            uint32_t n = 0u;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (k == j) n = v[k];
+            if ((n >> 24) && c + j < t.nb) {
+              const int i = atomicAdd(a.listed + tk, 1);
+              if (i < kListed) a.list[(size_t)tk * kListed + i] = make_int2(a.v0 + v0 + j, (int)n >> 24);
+            }
           }
         }
         if (valid) {
@@ -507,6 +550,8 @@ struct GradFinishArgs {
   const int32_t* colsum;  // [d]
   const uint32_t* srow;
   const double2* fac;     // [M]
+  const int* listed;      // [M]
+  const int2* list;       // [M][kListed]
   const int32_t* labels;
   const int8_t* W;
   const float* s_row;
@@ -519,8 +564,8 @@ struct GradFinishArgs {
   int M, V, d, sets;
 };
 
-// Joins the digits of a token: du = f step (sum of digits base 256 + offsets) + w_y s_row_y W_y in fp64, rounded
-// to fp32; then the norm's backward, dx = r (du w) - x r^3 / d sum(du w x).  One CTA per token at a time;
+// Joins the digits of a token and the listed rows: du = f step (sum of digits base 256 + offsets + 2^24 listed) +
+// w_y s_row_y W_y, integers and then fp64, rounded to fp32; then the norm's backward, dx = r (du w) - x r^3 / d sum(du w x).  One CTA per token at a time;
 // the norm weight's gradient is summed over the CTA's tokens in registers.
 template <typename T, int CH>
 __global__ void __launch_bounds__(256) grad_finish_kernel(GradFinishArgs a) {
@@ -541,6 +586,7 @@ __global__ void __launch_bounds__(256) grad_finish_kernel(GradFinishArgs a) {
     const double2 fac = a.fac[t];
     const int y = a.labels[t];
     const bool kept = y >= 0 && y < a.V;
+    const int nl = min(a.listed[t], kListed);
     const double f = fac.x * fp.step, wy = kept ? fac.y * (double)__ldg(a.s_row + y) : 0.0;
     float du[CH][8], xv[CH][8];
     double dot = 0.0;
@@ -562,6 +608,13 @@ __global__ void __launch_bounds__(256) grad_finish_kernel(GradFinishArgs a) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) sum[k] += (long long)n[k] << (8 * g);
         }
+      for (int l = 0; l < nl; ++l) {
+        const int2 e = __ldg(a.list + (size_t)t * kListed + l);
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.W + (size_t)e.x * a.d + i));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          sum[k] += (long long)(e.y * (int)(int8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3)))) << 24;
+      }
       uint2 wr = make_uint2(0u, 0u);
       if (kept) wr = __ldg(reinterpret_cast<const uint2*>(a.W + (size_t)y * a.d + i));
 #pragma unroll
@@ -685,7 +738,7 @@ Pieces pieces(int M, int d, int V) {
 constexpr int kNormParts = 2 * kSms;
 
 struct BackwardWs {
-  size_t q, s, rn, tok, fac, zero, srow, colsum, acc, zero_end, digits, wt, colpart, npart, total;
+  size_t q, s, rn, tok, fac, shift, list, zero, srow, listed, colsum, acc, zero_end, digits, wt, colpart, npart, total;
 };
 BackwardWs backward_ws(int M, int d, int V) {
   const Pieces p = pieces(M, d, V);
@@ -697,9 +750,12 @@ BackwardWs backward_ws(int M, int d, int V) {
   w.rn = w.s + al256(sizeof(double) * (size_t)M);
   w.tok = w.rn + al256(sizeof(float) * (size_t)M);
   w.fac = w.tok + al256(sizeof(float4) * (size_t)M);
-  w.zero = w.fac + al256(sizeof(double2) * (size_t)M);
+  w.shift = w.fac + al256(sizeof(double2) * (size_t)M);
+  w.list = w.shift + al256(sizeof(int) * (size_t)M);
+  w.zero = w.list + al256(sizeof(int2) * kListed * (size_t)M);
   w.srow = w.zero;
-  w.colsum = w.srow + 256;
+  w.listed = w.srow + 256;
+  w.colsum = w.listed + al256(sizeof(int) * (size_t)M);
   w.acc = w.colsum + al256(sizeof(int32_t) * (size_t)d);
   w.zero_end = w.acc + al256(sizeof(int32_t) * 3 * (size_t)p.sets * M * d);
   w.digits = w.zero_end;
@@ -766,18 +822,21 @@ int forward(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, 
 
 template <bool DS>
 cudaError_t launch_digits(const RowArgs& r, const Common& c, const CUtensorMap& ma, const CUtensorMap& mb,
-                          const float4* tok, const int32_t* labels, const float* s_row, const uint32_t* srow,
-                          unsigned char* digits, float* colpart, int M, int v0, int Vp, int tb, size_t plane,
+                          const TokenFactors& tf, int* listed, int2* list, const int32_t* labels,
+                          const float* s_row, unsigned char* digits, float* colpart, int M, int v0, int Vp, int tb, size_t plane,
                           cudaStream_t st) {
   typename DigitPolicy<DS>::Args a{};
   a.map_a = ma;
   a.map_b = mb;
   a.r = r;
   a.c = c;
-  a.tok = tok;
+  a.tok = tf.tok;
+  a.shift = tf.shift;
+  a.listed = listed;
+  a.list = list;
   a.labels = labels;
   a.s_row = s_row;
-  a.srow = srow;
+  a.srow = tf.srow;
   a.digits = digits;
   a.colpart = colpart;
   a.M = M;
@@ -880,7 +939,8 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   qa.rn = reinterpret_cast<float*>(base + w.rn);
   e = launch_rows_quant(qa, s);
   if (e != cudaSuccess) return record_cuda_failure(e);
-  TokenFactors tf{reinterpret_cast<float4*>(base + w.tok), reinterpret_cast<double2*>(base + w.fac),
+  TokenFactors tf{reinterpret_cast<float4*>(base + w.tok), reinterpret_cast<int*>(base + w.shift),
+                  reinterpret_cast<double2*>(base + w.fac),
                   reinterpret_cast<uint32_t*>(base + w.srow)};
   const int work = M > V / 4 ? M : V / 4;
   e = launch_pdl(grad_prepare_kernel, dim3(ceil_div(work, 256) < kSms ? ceil_div(work, 256) : kSms), dim3(256), 0, s,
@@ -895,6 +955,8 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   float* colpart = reinterpret_cast<float*>(base + w.colpart);
   int32_t* colsum = reinterpret_cast<int32_t*>(base + w.colsum);
   int32_t* acc = reinterpret_cast<int32_t*>(base + w.acc);
+  int* listed = reinterpret_cast<int*>(base + w.listed);
+  int2* list = reinterpret_cast<int2*>(base + w.list);
   for (int i = 0; i < pc.n; ++i) {
     const int v0 = i * pc.rows, nv = V - v0 < pc.rows ? V - v0 : pc.rows;
     const int kblocks = ceil_div(nv, BK);
@@ -904,10 +966,9 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
     ForwardPolicy::Args ra{};
     st = row_args(ra, M, nv, v0, d, W, V, qa.q, err);
     if (st) return st;
-    e = ds_row ? launch_digits<true>(ra.r, ra.c, ra.map_a, ra.map_b, tf.tok, labels, s_row, tf.srow, digits, colpart,
-                                     M, v0, pc.rows, tb, plane, s)
-               : launch_digits<false>(ra.r, ra.c, ra.map_a, ra.map_b, tf.tok, labels, s_row, tf.srow, digits, colpart,
-                                      M, v0, pc.rows, tb, plane, s);
+    const auto digit_product = ds_row ? launch_digits<true> : launch_digits<false>;
+    e = digit_product(ra.r, ra.c, ra.map_a, ra.map_b, tf, listed, list, labels, s_row, digits, colpart, M, v0, pc.rows, tb,
+                      plane, s);
     if (e != cudaSuccess) return record_cuda_failure(e);
     if (ds_row) {
       e = launch_pdl(ds_finish_kernel, dim3(ceil_div(nv, 256)), dim3(256), 0, s, (const float*)colpart,
@@ -935,6 +996,8 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   fa.colsum = colsum;
   fa.srow = tf.srow;
   fa.fac = tf.fac;
+  fa.listed = listed;
+  fa.list = list;
   fa.labels = labels;
   fa.W = W;
   fa.s_row = s_row;
