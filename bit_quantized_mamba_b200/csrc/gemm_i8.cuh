@@ -2,11 +2,14 @@
 // persistent, warp-specialised main loop (TMA producer, MMA issuer, eight epilogue warps) around a policy P
 // that says which tiles a CTA works on, how a K step is loaded and what becomes of the accumulators.
 //
-//   D[128 lanes][n columns] (int32, exact) = sum over K of A[lane][k] B[column][k]   (int8, both K-major)
+//   D[lanes][n columns] (int32, exact) = sum over K of A[lane][k] B[column][k]   (int8, both K-major)
 //
-// One CTA per SM, 128 x up to 256 tiles, K steps of 128 bytes through a ring of shared-memory stages, two
-// accumulators of 256 tensor-memory columns, so that a tile's epilogue runs while the next tile's products
-// accumulate.
+// P::CG CTAs (1 or 2) work on a tile of 128 CG lanes x up to 256 columns: K steps of 128 bytes through a ring
+// of shared-memory stages, two accumulators of 256 tensor-memory columns, so that a tile's epilogue runs while
+// the next tile's products accumulate.  A pair (CG = 2, a cluster) splits both operands: each CTA loads and
+// holds 128 lanes of A and half of B's columns, and one cta_group::2 product reads both halves.  What the
+// product waits for at these sizes is the stream from L2: one CTA's 128 x 256 tile moves 48 KB a K step, at
+// which it ran at 1350 TOPS (2048 x 50288 x 2048); a pair moves 32 KB per CTA.
 //
 // Every wait on an mbarrier is bounded: a wait that runs out of budget sets the status word, the CTA stops
 // issuing work, waits (bounded) for its copies and products in flight, frees its tensor memory and returns.
@@ -20,7 +23,7 @@
 namespace dfssm {
 namespace gemm_i8 {
 
-constexpr int BM = 128;      // lanes of a tile (the MMA's M)
+constexpr int BM = 128;      // lanes of a tile per CTA
 constexpr int BN_MAX = 256;  // columns of a tile at most (the MMA's N)
 constexpr int BK = 128;      // K bytes of a stage
 constexpr int UMMA_K = 32;   // K bytes of one kind::i8 MMA
@@ -32,24 +35,81 @@ constexpr int SMEM_LIMIT = 232448;  // 227 KB: the shared memory a CTA may have,
 constexpr int BAR_BYTES = 256;
 constexpr int TMEM_COLS = 2 * BN_MAX;
 
-// One output tile of a CTA: lanes a0 .. a0 + na, columns b0 .. b0 + nb, K steps kb0 .. kb1.
+// One output tile: lanes a0 .. a0 + na, columns b0 .. b0 + nb, K steps kb0 .. kb1.  Policies give the whole
+// tile (128 CG lanes); loads and epilogues see the CTA's own 128 lanes of it.
 struct Tile {
   int a0, na, b0, nb;
   int kb0, kb1;
+  int aux;  // the policy's own
 };
 
-// kind::i8 instruction descriptor: D s32, A and B s8, both K-major, M = 128, N = n (a multiple of 16).
+// Columns of the product: nb rounded up to what the instruction (16) and an even split over a pair (2 x 16) need.
+template <int CG>
+__device__ __forceinline__ int mma_n(int nb) { return (nb + 16 * CG - 1) & ~(16 * CG - 1); }
+
+// kind::i8 instruction descriptor: D s32, A and B s8, both K-major, M = 128 CG, N = n.
+template <int CG>
 __device__ __forceinline__ uint32_t idesc(int n) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)((BM * CG) >> 4) << 24);
 }
+template <int CG>
 __device__ __forceinline__ void umma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t id,
                                      uint32_t accum) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(id), "r"(accum)
-      : "memory");
+  if (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(id), "r"(accum)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(id), "r"(accum)
+        : "memory");
+}
+// Arrival on the barrier (of both CTAs of a pair) when the products issued so far are complete.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (CG == 1)
+    umma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// The shared::cluster address of a barrier in the pair's first CTA.
+template <int CG>
+__device__ __forceinline__ uint32_t leader_bar(uint64_t* bar) {
+  if (CG == 1) return smem_u32(bar);
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(bar)), "r"(0));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Copies into this CTA's shared memory, counted on the barrier at the shared::cluster address `bar` (of the pair's
+// first CTA).
+template <int CG>
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
 }
 // 32 lanes x 16 / 32 columns of tensor memory, one lane per thread (to be awaited with tmem_wait).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -75,7 +135,7 @@ __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.syn
 
 // What every policy's arguments start with.
 struct Common {
-  int b_tile;   // columns a stage has room for
+  int b_tile;   // columns a stage of one CTA has room for
   int stages;
   int* err;     // status word: kDeviceTimeout after a wait ran out of budget
 };
@@ -89,8 +149,19 @@ inline size_t smem_bytes(const Common& c, int epi_bytes) {
   return 1024 + (size_t)c.stages * stage_bytes(c) + BAR_BYTES + epi_bytes;
 }
 
+// What a pair of a tile belongs to this CTA of it.
+template <int CG>
+__device__ __forceinline__ Tile own_tile(Tile t, int rank) {
+  if (CG == 2) {
+    t.a0 += rank * BM;
+    t.na = max(0, min(BM, t.na - rank * BM));
+  }
+  return t;
+}
+
 template <class P>
-__global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ typename P::Args ar) {
+__global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_constant__ typename P::Args ar) {
+  constexpr int CG = P::CG;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // aligned by an offset from the array itself, so that every access stays a shared-memory access
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -98,13 +169,14 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ typ
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)stages * sbytes);  // [stages] TMA -> MMA
   uint64_t* empty = full + MAX_STAGES;      // [stages] MMA -> producer
   uint64_t* acc_full = empty + MAX_STAGES;  // [2] MMA -> epilogue
-  uint64_t* acc_empty = acc_full + 2;       // [2] epilogue -> MMA
+  uint64_t* acc_empty = acc_full + 2;       // [2] epilogue (of both CTAs) -> MMA
   uint64_t* mma_done = acc_empty + 2;       // every MMA of this CTA complete
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int& abort_flag = *reinterpret_cast<volatile int*>(tmem_holder + 1);
   unsigned char* epi_smem = smem + (size_t)stages * sbytes + BAR_BYTES;
   static_assert((2 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? (int)(blockIdx.x & 1u) : 0;  // within the pair (a cluster of two consecutive CTAs)
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
@@ -114,20 +186,27 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ typ
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], EPI_WARPS);
+      mbar_init(&acc_empty[b], EPI_WARPS * CG);
     }
     mbar_init(mma_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(tmem_holder)),
-                 "r"(TMEM_COLS)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (CG == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                   "r"(TMEM_COLS)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                   "r"(TMEM_COLS)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if (CG == 2) cluster_sync();  // the other CTA's barriers are ready
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem_base = *tmem_holder;
   if (threadIdx.x == 0) pdl_launch_dependents();
@@ -137,8 +216,10 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ typ
     pdl_wait();
     int it = 0;
     bool ok = true;
-    Tile t;
-    for (int j = 0; ok && P::tile(ar, j, t); ++j) {
+    Tile pt;
+    for (int j = 0; ok && P::tile(ar, j, pt); ++j) {
+      const Tile t = own_tile<CG>(pt, rank);
+      const uint32_t bytes = P::bytes(ar, pt);  // of the whole tile's K step, both CTAs'
       for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
         const int s = it % stages;
         if (it >= stages && !mbar_wait(&empty[s], ((it / stages) - 1) & 1, &abort_flag)) {
@@ -147,12 +228,21 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ typ
           break;
         }
         unsigned char* st = smem + (size_t)s * sbytes;
-        P::load(ar, t, kb, st, st + A_BYTES, &full[s]);
+        if (rank == 0) mbar_expect_tx(&full[s], bytes);
+        P::load(ar, t, rank, kb, st, st + A_BYTES, leader_bar<CG>(&full[s]));
       }
     }
-    // the last copies land before this CTA may exit
-    for (int j = (it > stages ? it - stages : 0); j < it; ++j) mbar_wait_drain(&full[j % stages], (j / stages) & 1);
-  } else if (warp == 1 && lane == 0) {
+    // the last copies land before this CTA may exit (those of a pair's second CTA are counted by the first, which
+    // the cluster barrier at the end waits for; after an abort they get a millisecond)
+    if (rank == 0) {
+      for (int j = (it > stages ? it - stages : 0); j < it; ++j)
+        mbar_wait_drain(&full[j % stages], (j / stages) & 1);
+    } else if (!ok) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < 2000000LL) {
+      }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---- MMA issuer
     int it = 0, local = 0;
     bool ok = true, issued = false;
@@ -165,7 +255,7 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ typ
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN_MAX);
-      const uint32_t id = idesc((t.nb + 15) & ~15);
+      const uint32_t id = idesc<CG>(mma_n<CG>(t.nb));
       for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
         const int s = it % stages;
         if (!mbar_wait(&full[s], (it / stages) & 1, &abort_flag)) {
@@ -177,17 +267,17 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ typ
         const uint32_t a_addr = smem_u32(smem + (size_t)s * sbytes);
 #pragma unroll
         for (int kk = 0; kk < BK / UMMA_K; ++kk)
-          umma(d_tmem, P::adesc(a_addr, kk), P::bdesc(ar, a_addr + A_BYTES, kk), id,
-               (kb > t.kb0 || kk > 0) ? 1u : 0u);
-        umma_commit(&empty[s]);
+          umma<CG>(d_tmem, P::adesc(a_addr, kk), P::bdesc(ar, a_addr + A_BYTES, kk), id,
+                   (kb > t.kb0 || kk > 0) ? 1u : 0u);
+        commit<CG>(&empty[s]);
         issued = true;
       }
       if (!ok) break;
-      umma_commit(&acc_full[buf]);
+      commit<CG>(&acc_full[buf]);
     }
     // every MMA this thread issued completes before the tensor memory is released
     if (issued) {
-      umma_commit(mma_done);
+      commit<CG>(mma_done);
       mbar_wait_drain(mma_done, 0);
     }
   } else if (warp >= 2) {
@@ -204,90 +294,121 @@ __global__ void __launch_bounds__(THREADS, 1) kernel(const __grid_constant__ typ
       }
       __syncwarp();
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      epi.tile(ar, t, tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(buf * BN_MAX));
+      epi.tile(ar, own_tile<CG>(t, rank), tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(buf * BN_MAX));
       // this warp's reads of the accumulator are complete
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0)
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&acc_empty[buf])) : "memory");
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         leader_bar<CG>(&acc_empty[buf]))
+                     : "memory");
     }
     __syncwarp();
     epi.finish(ar);
   }
+  __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if (CG == 2) cluster_sync();  // neither CTA's shared or tensor memory goes while the other may reach it
   if (abort_flag && threadIdx.x == 0) atomicExch(ar.c.err, kDeviceTimeout);
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
-                 : "memory");
+    if (CG == 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS) : "memory");
   }
 }
+
+// Launch of `groups` CTAs or pairs.
+template <class P>
+cudaError_t launch(const typename P::Args& a, int groups, int epi_smem, cudaStream_t st) {
+  const auto k = gemm_i8_kernel<P>;
+  const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(k), SMEM_LIMIT);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_cluster(P::CG, k, dim3(groups * P::CG), dim3(THREADS), smem_bytes(a.c, epi_smem), st, a);
+}
+// Groups that run at a time: one CTA per SM.
+template <class P>
+int max_groups() { return num_sms() / P::CG; }
 
 // ------------------------------------------------------------------ row-major operands through TMA
 // Both operands are row-major int8 matrices with K contiguous, loaded as 128-byte-swizzled boxes of 128 bytes
 // of K (bytes past a row's end and rows past the last read as zero).  The rows of one operand are the
 // tokens, of the other the matrix W.
 enum Mode {
-  kGrid = 0,    // tiles of tile_a x b_tile, strided over the CTAs, the token index fastest (W read once)
-  kRangeA = 1,  // every CTA takes a balanced range of A rows (W) in groups of 32, and all columns (one tile)
-  kRangeB = 2   // every CTA takes a balanced range of B rows (W), and for it all tiles of A rows (tokens)
+  kGrid = 0,    // whole tiles, strided over the groups, the token index fastest (W read once)
+  kRangeA = 1,  // every group takes a balanced range of A rows (W) in units of 32, and all columns (one tile)
+  kRangeB = 2   // every group takes a balanced range of B rows (W), and for it all tiles of A rows (tokens)
 };
 struct RowArgs {
-  Common c;
   int mode;
   int rows_a, rows_b;
+  int tile_b;        // columns of a whole tile
   int kblocks;
   int box_a, box_b;  // rows of one TMA box of each operand
   int b_first;       // first B row of the product (a piece of the vocabulary); rows_b counts from there
 };
 
+template <int CG>
 __device__ __forceinline__ bool row_tile(const RowArgs& r, int w_is_a, int j, Tile& t) {
+  constexpr int TA = BM * CG;
+  const int group = blockIdx.x / CG, groups = gridDim.x / CG;
   t.kb0 = 0;
   t.kb1 = r.kblocks;
+  const int ta = (r.rows_a + TA - 1) / TA;
   if (r.mode == kGrid) {
-    const int ta = (r.rows_a + BM - 1) / BM, tb = (r.rows_b + r.c.b_tile - 1) / r.c.b_tile;
-    const long long i = blockIdx.x + (long long)j * gridDim.x;
+    const int tb = (r.rows_b + r.tile_b - 1) / r.tile_b;
+    const long long i = group + (long long)j * groups;
     if (i >= (long long)ta * tb) return false;
     const int ia = w_is_a ? (int)(i / tb) : (int)(i % ta);
     const int ib = w_is_a ? (int)(i % tb) : (int)(i / ta);
-    t.a0 = ia * BM;
-    t.b0 = ib * r.c.b_tile;
-    t.na = min(BM, r.rows_a - t.a0);
-    t.nb = min(r.c.b_tile, r.rows_b - t.b0);
+    t.a0 = ia * TA;
+    t.b0 = ib * r.tile_b;
+    t.na = min(TA, r.rows_a - t.a0);
+    t.nb = min(r.tile_b, r.rows_b - t.b0);
     return true;
   }
   const int rows_w = r.mode == kRangeA ? r.rows_a : r.rows_b;
-  const long long groups = (rows_w + 31) / 32;
-  const int w0 = (int)(groups * blockIdx.x / gridDim.x) * 32;
-  const int w1 = min((int)(groups * (blockIdx.x + 1) / gridDim.x) * 32, rows_w);
+  const long long units = (rows_w + 31) / 32;
+  const int w0 = (int)(units * group / groups) * 32;
+  const int w1 = min((int)(units * (group + 1) / groups) * 32, rows_w);
   if (r.mode == kRangeA) {
-    t.a0 = w0 + BM * j;
+    t.a0 = w0 + TA * j;
     if (t.a0 >= w1) return false;
-    t.na = min(BM, w1 - t.a0);
+    t.na = min(TA, w1 - t.a0);
     t.b0 = 0;
     t.nb = r.rows_b;
     return true;
   }
-  const int nt = (w1 - w0 + r.c.b_tile - 1) / r.c.b_tile;
-  const int ta = (r.rows_a + BM - 1) / BM;
+  const int nt = (w1 - w0 + r.tile_b - 1) / r.tile_b;
   if (nt == 0 || j >= nt * ta) return false;
-  t.a0 = (j / nt) * BM;
-  t.na = min(BM, r.rows_a - t.a0);
-  t.b0 = w0 + (j % nt) * r.c.b_tile;
-  t.nb = min(r.c.b_tile, w1 - t.b0);
+  t.a0 = (j / nt) * TA;
+  t.na = min(TA, r.rows_a - t.a0);
+  t.b0 = w0 + (j % nt) * r.tile_b;
+  t.nb = min(r.tile_b, w1 - t.b0);
   return true;
 }
 
-// One K step of both operands: whole boxes up to the tile's last row.
+// One K step: whole boxes of A up to the tile's last lane, and B's columns (half of them each in a pair).
+template <int CG>
+__device__ __forceinline__ uint32_t row_bytes(const RowArgs& r, const Tile& t) {
+  int n = mma_n<CG>(t.nb) / CG;
+  n = (n + r.box_b - 1) / r.box_b * r.box_b * CG;
+#pragma unroll
+  for (int i = 0; i < CG; ++i) {
+    const int na = max(0, min(BM, t.na - i * BM));
+    n += (na + r.box_a - 1) / r.box_a * r.box_a;
+  }
+  return (uint32_t)n * BK;
+}
+template <int CG>
 __device__ __forceinline__ void row_load(const RowArgs& r, const CUtensorMap* ma, const CUtensorMap* mb,
-                                         const Tile& t, int kb, unsigned char* sa, unsigned char* sb,
-                                         uint64_t* bar) {
-  const int n_a = (t.na + r.box_a - 1) / r.box_a, n_b = (t.nb + r.box_b - 1) / r.box_b;
-  mbar_expect_tx(bar, (uint32_t)(n_a * r.box_a + n_b * r.box_b) * BK);
-  for (int i = 0; i < n_a; ++i) tma_load_2d(sa + i * r.box_a * BK, ma, kb * BK, t.a0 + i * r.box_a, bar);
-  for (int i = 0; i < n_b; ++i)
-    tma_load_2d(sb + i * r.box_b * BK, mb, kb * BK, r.b_first + t.b0 + i * r.box_b, bar);
+                                         const Tile& t, int rank, int kb, unsigned char* sa, unsigned char* sb,
+                                         uint32_t bar) {
+  const int half = mma_n<CG>(t.nb) / CG, b0 = r.b_first + t.b0 + rank * half;
+  for (int i = 0; i < t.na; i += r.box_a) tma_load<CG>(sa + i * BK, ma, kb * BK, t.a0 + i, bar);
+  for (int i = 0; i < half; i += r.box_b) tma_load<CG>(sb + i * BK, mb, kb * BK, b0 + i, bar);
 }
 
 }  // namespace gemm_i8

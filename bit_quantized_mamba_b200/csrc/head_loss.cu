@@ -54,7 +54,9 @@ __device__ __forceinline__ float scale2(float s_row) { return __double2float_rn(
 
 // ------------------------------------------------------------------------------------ forward
 
+template <int CG_>
 struct ForwardPolicy {
+  static constexpr int CG = CG_;
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
     RowArgs r;
@@ -66,10 +68,11 @@ struct ForwardPolicy {
     float2* part;           // [slots][M] (max, sum) in units of log 2
     int M, V;
   };
-  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile(a.r, 0, j, t); }
-  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int kb, unsigned char* sa,
-                                              unsigned char* sb, uint64_t* bar) {
-    row_load(a.r, &a.map_a, &a.map_b, t, kb, sa, sb, bar);
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 0, j, t); }
+  static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
+  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int rank, int kb, unsigned char* sa,
+                                              unsigned char* sb, uint32_t bar) {
+    row_load<CG>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
     return umma_desc_k_sw128(addr + kk * UMMA_K);
@@ -93,7 +96,7 @@ struct ForwardPolicy {
     }
     __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
       const int tk = t.a0 + q * 32 + lane;
-      const int sl = (a.r.mode == kGrid ? t.b0 / a.r.c.b_tile : (int)blockIdx.x) * 2 + half;
+      const int sl = (a.r.mode == kGrid ? t.b0 / a.r.tile_b : (int)blockIdx.x / CG) * 2 + half;
       if (tk != tok || sl != slot) {
         flush(a);
         tok = tk;
@@ -337,8 +340,9 @@ __global__ void __launch_bounds__(256) transpose_kernel(const int8_t* __restrict
 }
 
 // The first product of the gradient: digits of a piece, and the row scales' gradient per 32 tokens.
-template <bool DS>
+template <int CG_, bool DS>
 struct DigitPolicy {
+  static constexpr int CG = CG_;
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
     RowArgs r;
@@ -355,10 +359,11 @@ struct DigitPolicy {
     int M, v0, Vp, tb;
     size_t plane;           // bytes of one digit's plane
   };
-  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile(a.r, 0, j, t); }
-  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int kb, unsigned char* sa,
-                                              unsigned char* sb, uint64_t* bar) {
-    row_load(a.r, &a.map_a, &a.map_b, t, kb, sa, sb, bar);
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 0, j, t); }
+  static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
+  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int rank, int kb, unsigned char* sa,
+                                              unsigned char* sb, uint32_t bar) {
+    row_load<CG>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
     return umma_desc_k_sw128(addr + kk * UMMA_K);
@@ -464,46 +469,46 @@ struct DigitPolicy {
 };
 
 // The second product: accumulators [set][3][M][d] += digits x transposed W of a piece.  Lanes are columns of W
-// (128 of them), columns are tokens; the (token tile, digit, column tile, K) space is cut into one even
-// contiguous range per CTA.
+// (128 a CTA), columns are tokens (tb a CTA); the (token tile, digit, column tile, K) space is cut into one even
+// contiguous range per CTA or pair.
+template <int CG_>
 struct GradPolicy {
+  static constexpr int CG = CG_;
   struct Args {
+    CUtensorMap map_a, map_b;  // transposed W, digits: blocks of 128 bytes
     Common c;
-    const unsigned char* digits;
-    const int8_t* wt;
     int32_t* acc;  // this piece's set: [3][M][d]
     size_t plane;
     int M, d, Vp, tb, kblocks;
   };
-  static __device__ __forceinline__ void unit(const Args& a, int u, int& dt, int& dg, int& mt) {
-    const int nd = (a.d + 127) / 128;
-    dt = u % nd;
-    dg = (u / nd) % 3;
-    mt = u / (3 * nd);
+  static __host__ __device__ __forceinline__ long long steps(const Args& a) {
+    const int nd = (a.d + BM * CG - 1) / (BM * CG), nt = (a.M + a.tb * CG - 1) / (a.tb * CG);
+    return (long long)3 * nd * nt * a.kblocks;
   }
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) {
-    const int nd = (a.d + 127) / 128, nt = (a.M + a.tb - 1) / a.tb;
-    const long long total = (long long)3 * nd * nt * a.kblocks;
-    const long long s0 = total * blockIdx.x / gridDim.x, s1 = total * (blockIdx.x + 1) / gridDim.x;
+    const int group = blockIdx.x / CG, groups = gridDim.x / CG;
+    const long long total = steps(a);
+    const long long s0 = total * group / groups, s1 = total * (group + 1) / groups;
     const long long u = s0 / a.kblocks + j, first = u * a.kblocks;
     if (first >= s1 || s0 >= s1) return false;
     t.kb0 = (int)((s0 > first ? s0 : first) - first);
     t.kb1 = (int)((s1 < first + a.kblocks ? s1 : first + a.kblocks) - first);
-    int dt, dg, mt;
-    unit(a, (int)u, dt, dg, mt);
-    t.a0 = dt;
-    t.na = dg;
-    t.b0 = mt * a.tb;
-    t.nb = min(a.tb, a.M - t.b0);
+    const int nd = (a.d + BM * CG - 1) / (BM * CG), ui = (int)u;
+    t.a0 = ui % nd * BM * CG;
+    t.na = BM * CG;
+    t.aux = ui / nd % 3;  // digit
+    t.b0 = ui / nd / 3 * a.tb * CG;
+    t.nb = a.tb * CG;
     return true;
   }
+  static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile&) {
+    return CG * (A_BYTES + (uint32_t)a.tb * BK);
+  }
   // both operands were laid out as the product reads them: eight 16-byte K columns of all rows are contiguous
-  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int kb, unsigned char* sa,
-                                              unsigned char* sb, uint64_t* bar) {
-    const uint32_t bb = (uint32_t)a.tb * BK;
-    mbar_expect_tx(bar, A_BYTES + bb);
-    bulk_g2s(sa, a.wt + (size_t)t.a0 * 128 * a.Vp + (size_t)kb * A_BYTES, A_BYTES, bar);
-    bulk_g2s(sb, a.digits + (size_t)t.na * a.plane + (size_t)t.b0 * a.Vp + (size_t)kb * bb, bb, bar);
+  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int rank, int kb, unsigned char* sa,
+                                              unsigned char* sb, uint32_t bar) {
+    tma_load<CG>(sa, &a.map_a, 0, (int)((size_t)t.a0 * a.Vp / 128) + kb * BM, bar);
+    tma_load<CG>(sb, &a.map_b, 0, (int)((t.aux * a.plane + (size_t)(t.b0 + rank * a.tb) * a.Vp) / 128) + kb * a.tb, bar);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
     return umma_desc_k_plain(addr + kk * 2 * (BM * 16), BM * 16);
@@ -516,16 +521,16 @@ struct GradPolicy {
     __device__ __forceinline__ Epilogue(const Args&, unsigned char*, int q_, int half_, int lane_)
         : q(q_), half(half_), lane(lane_) {}
     __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
-      const int col = t.a0 * 128 + q * 32 + lane;
+      const int col = t.a0 + q * 32 + lane, n = min(t.nb, a.M - t.b0);
       const bool cv = col < a.d;
-      int32_t* base = a.acc + ((size_t)t.na * a.M + t.b0) * a.d + col;
-      for (int c = half * 32; c < t.nb; c += 64) {
+      int32_t* base = a.acc + ((size_t)t.aux * a.M + t.b0) * a.d + col;
+      for (int c = half * 32; c < n; c += 64) {
         uint32_t v[32];
         tmem_ld32(taddr + (uint32_t)c, v);
         tmem_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (cv && c + j < t.nb) atomicAdd(base + (size_t)(c + j) * a.d, (int)v[j]);
+          if (cv && c + j < n) atomicAdd(base + (size_t)(c + j) * a.d, (int)v[j]);
       }
     }
     __device__ __forceinline__ void finish(const Args&) {}
@@ -701,6 +706,21 @@ ForwardWs forward_ws(int M, int d, int V) {
   return w;
 }
 
+// How tokens and columns are tiled: up to 128 tokens by single CTAs (the stream of W bounds the products), above
+// by pairs.
+struct Layout {
+  int cg, tb;      // CTAs per tile; tokens of a block of digits
+  size_t mp, dp;   // tokens and columns of W, padded to whole tiles
+};
+Layout layout(int M, int d) {
+  Layout l;
+  l.cg = M <= BM ? 1 : 2;
+  l.tb = M <= BM ? (M + 15) & ~15 : BM;
+  l.mp = (size_t)ceil_div(M, l.tb * l.cg) * l.tb * l.cg;
+  l.dp = (size_t)ceil_div(d, BM * l.cg) * BM * l.cg;
+  return l;
+}
+
 // The vocabulary's pieces: rows per piece (a multiple of 256), and how many accumulator sets keep the int32 sums
 // in range (|digit| <= 128, |W| <= 128: 2^14 rows-worth per row, so at most 131071 rows a set).
 struct Pieces {
@@ -709,20 +729,19 @@ struct Pieces {
 constexpr size_t kPieceBytes = 80u << 20;  // digits and transposed W of a piece: they stay in the 126 MB L2
 constexpr int kSms = 148;
 Pieces pieces(int M, int d, int V) {
-  const int tb = M < BN_MAX ? (M + 15) & ~15 : BN_MAX;
-  const size_t mp = (size_t)ceil_div(M, tb) * tb, dp = (size_t)ceil_div(d, 128) * 128;
-  size_t t = kPieceBytes / (3 * mp + dp + (size_t)ceil_div(M, 32) * 4) / BN_MAX;  // tiles of 256 rows
+  const Layout l = layout(M, d);
+  size_t t = kPieceBytes / (3 * l.mp + l.dp + l.mp / 8) / BN_MAX;  // tiles of 256 rows
   if (t < 8) t = 8;
   if (t > 256) t = 256;
-  const int vt = ceil_div(V, BN_MAX), mt = ceil_div(M, BM);
+  const int vt = ceil_div(V, BN_MAX), mt = ceil_div(M, BM * l.cg);
   if ((int)t < vt) {
-    // whole waves of 128 x 256 tiles where a few fit, else equal pieces
-    int g = mt, b = kSms;
+    // whole waves of tiles where a few fit, else equal pieces
+    int g = mt, b = kSms / l.cg;
     while (b) {
       const int r = g % b;
       g = b, b = r;
     }
-    const int wave = kSms / g;
+    const int wave = kSms / l.cg / g;
     if (wave <= (int)t) t = t / wave * wave;
     else t = ceil_div(vt, ceil_div(vt, (int)t));
   } else {
@@ -742,8 +761,7 @@ struct BackwardWs {
 };
 BackwardWs backward_ws(int M, int d, int V) {
   const Pieces p = pieces(M, d, V);
-  const int tb = M < BN_MAX ? (M + 15) & ~15 : BN_MAX;
-  const size_t mp = (size_t)ceil_div(M, tb) * tb, dp = (size_t)ceil_div(d, 128) * 128;
+  const Layout l = layout(M, d);
   BackwardWs w;
   w.q = kStatusBytes;
   w.s = w.q + al256((size_t)M * d);
@@ -759,50 +777,47 @@ BackwardWs backward_ws(int M, int d, int V) {
   w.acc = w.colsum + al256(sizeof(int32_t) * (size_t)d);
   w.zero_end = w.acc + al256(sizeof(int32_t) * 3 * (size_t)p.sets * M * d);
   w.digits = w.zero_end;
-  w.wt = w.digits + al256(3 * mp * p.rows);
-  w.colpart = w.wt + al256(dp * p.rows);
-  w.npart = w.colpart + al256(sizeof(float) * 4 * (size_t)ceil_div(M, BM) * p.rows);
+  w.wt = w.digits + al256(3 * l.mp * p.rows);
+  w.colpart = w.wt + al256(l.dp * p.rows);
+  w.npart = w.colpart + al256(sizeof(float) * 4 * l.cg * (size_t)ceil_div(M, BM * l.cg) * p.rows);
   w.total = w.npart + al256(sizeof(float) * (size_t)(M < kNormParts ? M : kNormParts) * d);
   return w;
 }
 
-// Token tiles on the lanes, rows of W on the columns: up to two token tiles stream W in balanced ranges
-// (memory bound), more take whole tiles.
-template <class A>
-int row_args(A& a, int M, int rows, int first, int d, const int8_t* W, int V, const int8_t* q, int* err) {
+// Token tiles on the lanes, rows of W on the columns: one tile of tokens streams W in balanced ranges, more take
+// whole tiles.
+template <class P>
+int row_args(typename P::Args& a, int M, int rows, int first, int d, const int8_t* W, int V, const int8_t* q, int* err) {
+  constexpr int CG = P::CG;
   a.r.rows_a = M;
   a.r.rows_b = rows;
   a.r.b_first = first;
+  a.r.tile_b = BN_MAX;
   a.r.kblocks = ceil_div(d, BK);
-  a.r.mode = M <= 2 * BM ? kRangeB : kGrid;
+  a.r.mode = M <= BM * CG ? kRangeB : kGrid;
   a.r.box_a = BM;
-  a.r.box_b = a.r.mode == kRangeB ? 32 : BN_MAX;
-  a.c.b_tile = BN_MAX;
-  a.c.stages = ring_stages(BN_MAX, EPI_WARPS * 32 * 4);
+  a.r.box_b = a.r.mode == kRangeB ? 32 / CG : BN_MAX / CG;
+  a.c.b_tile = BN_MAX / CG;
+  a.c.stages = ring_stages(BN_MAX / CG, P::EPI_SMEM);
   a.c.err = err;
-  a.r.c = a.c;
   if (!encode_u8_map_sw128(&a.map_a, q, M, d, a.r.box_a) || !encode_u8_map_sw128(&a.map_b, W, V, d, a.r.box_b))
     return DFSSM_EUNSUPPORTED;
   return DFSSM_OK;
 }
-int row_grid(const RowArgs& r) {
-  const long long sms = num_sms() < kMaxRangeCtas ? num_sms() : kMaxRangeCtas;
-  const long long units = r.mode == kGrid ? (long long)ceil_div(r.rows_a, BM) * ceil_div(r.rows_b, BN_MAX)
-                                          : ceil_div(r.rows_b, 32);
-  return (int)(units < sms ? units : sms);
-}
 template <class P>
-cudaError_t launch_gemm(const typename P::Args& a, int grid, int epi_smem, cudaStream_t st) {
-  const auto k = kernel<P>;
-  const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(k), SMEM_LIMIT);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(grid), dim3(THREADS), smem_bytes(a.c, epi_smem), st, a);
+int row_groups(const RowArgs& r) {
+  const long long most = max_groups<P>() < kMaxRangeCtas ? max_groups<P>() : kMaxRangeCtas;
+  const long long units = r.mode == kGrid ? (long long)ceil_div(r.rows_a, BM * P::CG) * ceil_div(r.rows_b, BN_MAX)
+                                          : ceil_div(r.rows_b, 32);
+  return (int)(units < most ? units : most);
 }
 
+template <int CG>
 int forward(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, const double* s, int M,
             const int32_t* labels, float* loss, float* stats, float2* part, int* err, cudaStream_t st) {
-  ForwardPolicy::Args a{};
-  const int rc = row_args(a, M, V, 0, d, W, V, q, err);
+  using P = ForwardPolicy<CG>;
+  typename P::Args a{};
+  const int rc = row_args<P>(a, M, V, 0, d, W, V, q, err);
   if (rc) return rc;
   a.s_tok = s;
   a.s_row = s_row;
@@ -811,40 +826,78 @@ int forward(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, 
   a.part = part;
   a.M = M;
   a.V = V;
-  const int grid = row_grid(a.r);
-  cudaError_t e = launch_gemm<ForwardPolicy>(a, grid, ForwardPolicy::EPI_SMEM, st);
-  const int slots = 2 * (a.r.mode == kGrid ? ceil_div(V, BN_MAX) : grid);
+  const int groups = row_groups<P>(a.r);
+  cudaError_t e = launch<P>(a, groups, P::EPI_SMEM, st);
+  const int slots = 2 * (a.r.mode == kGrid ? ceil_div(V, BN_MAX) : groups);
   if (e == cudaSuccess)
     e = launch_pdl(loss_finish_kernel, dim3(ceil_div(M, 32)), dim3(256), 0, st, (const float2*)part, slots, M, V,
                    labels, stats, loss, err);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
 }
 
-template <bool DS>
-cudaError_t launch_digits(const RowArgs& r, const Common& c, const CUtensorMap& ma, const CUtensorMap& mb,
-                          const TokenFactors& tf, int* listed, int2* list, const int32_t* labels,
-                          const float* s_row, unsigned char* digits, float* colpart, int M, int v0, int Vp, int tb, size_t plane,
-                          cudaStream_t st) {
-  typename DigitPolicy<DS>::Args a{};
-  a.map_a = ma;
-  a.map_b = mb;
-  a.r = r;
-  a.c = c;
-  a.tok = tf.tok;
-  a.shift = tf.shift;
-  a.listed = listed;
-  a.list = list;
-  a.labels = labels;
-  a.s_row = s_row;
-  a.srow = tf.srow;
-  a.digits = digits;
-  a.colpart = colpart;
-  a.M = M;
-  a.v0 = v0;
-  a.Vp = Vp;
-  a.tb = tb;
+// One piece of the vocabulary, rows [v0, v0 + nv): digits, the row scales' gradient, and their product with W.
+struct Piece {
+  const int8_t* W;
+  const float* s_row;
+  const int8_t* q;
+  const int32_t* labels;
+  TokenFactors tf;
+  int* listed;
+  int2* list;
+  unsigned char* digits;
+  int8_t* wt;
+  float* colpart;
+  int32_t* acc;     // the piece's set
+  float* ds_row;    // [V] or NULL
+  int* err;
+  int V, d, M, v0, nv, Vp;
+  Layout l;
+};
+template <int CG, bool DS>
+int piece_products(const Piece& p, cudaStream_t st) {
+  using P = DigitPolicy<CG, DS>;
+  const size_t plane = p.l.mp * p.Vp;
+  typename P::Args a{};
+  const int rc = row_args<P>(a, p.M, p.nv, p.v0, p.d, p.W, p.V, p.q, p.err);
+  if (rc) return rc;
+  a.tok = p.tf.tok;
+  a.shift = p.tf.shift;
+  a.listed = p.listed;
+  a.list = p.list;
+  a.labels = p.labels;
+  a.s_row = p.s_row;
+  a.srow = p.tf.srow;
+  a.digits = p.digits;
+  a.colpart = p.colpart;
+  a.M = p.M;
+  a.v0 = p.v0;
+  a.Vp = p.Vp;
+  a.tb = p.l.tb;
   a.plane = plane;
-  return launch_gemm<DigitPolicy<DS>>(a, row_grid(r), DigitPolicy<DS>::EPI_SMEM, st);
+  cudaError_t e = launch<P>(a, row_groups<P>(a.r), P::EPI_SMEM, st);
+  if (DS && e == cudaSuccess)
+    e = launch_pdl(ds_finish_kernel, dim3(ceil_div(p.nv, 256)), dim3(256), 0, st, (const float*)p.colpart,
+                   ceil_div(p.M, 32), p.Vp, p.nv, p.ds_row + p.v0);
+  if (e != cudaSuccess) return record_cuda_failure(e);
+  using G = GradPolicy<CG>;
+  typename G::Args g{};
+  g.c.b_tile = p.l.tb;
+  g.c.stages = ring_stages(p.l.tb, 0);
+  g.c.err = p.err;
+  if (!encode_blocks_map(&g.map_a, p.wt, (int64_t)(p.l.dp * p.Vp / 128), BM) ||
+      !encode_blocks_map(&g.map_b, p.digits, (int64_t)(3 * plane / 128), p.l.tb))
+    return DFSSM_EUNSUPPORTED;
+  g.acc = p.acc;
+  g.plane = plane;
+  g.M = p.M;
+  g.d = p.d;
+  g.Vp = p.Vp;
+  g.tb = p.l.tb;
+  g.kblocks = ceil_div(p.nv, BK);
+  const long long steps = G::steps(g);
+  const int most = max_groups<G>();
+  e = launch<G>(g, (int)(steps < most ? steps : most), 0, st);
+  return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
 }
 
 template <typename T>
@@ -897,8 +950,9 @@ extern "C" int dfssm_head_loss(const int8_t* W, const float* s_row, int V, int d
   const RowsQuantArgs qa = quant_args(x, x_type, ldx, M, d, norm_w, base, w.q, w.s);
   const cudaError_t e = launch_rows_quant(qa, s);
   if (e != cudaSuccess) return record_cuda_failure(e);
-  return forward(W, s_row, V, d, qa.q, qa.s, M, labels, loss, stats, reinterpret_cast<float2*>(base + w.part),
-                 reinterpret_cast<int*>(base), s);
+  const auto f = layout(M, d).cg == 1 ? forward<1> : forward<2>;
+  return f(W, s_row, V, d, qa.q, qa.s, M, labels, loss, stats, reinterpret_cast<float2*>(base + w.part),
+           reinterpret_cast<int*>(base), s);
 }
 
 extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int V, int d, const void* x,
@@ -932,7 +986,6 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   if (!device_ok()) return DFSSM_EDEVICE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(workspace);
-  int* err = reinterpret_cast<int*>(base);
   cudaError_t e = cudaMemsetAsync(base + w.zero, 0, w.zero_end - w.zero, s);
   if (e != cudaSuccess) return record_cuda_failure(e);
   RowsQuantArgs qa = quant_args(x, x_type, ldx, M, d, norm_w, base, w.q, w.s);
@@ -948,56 +1001,45 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   if (e != cudaSuccess) return record_cuda_failure(e);
 
   const Pieces pc = pieces(M, d, V);
-  const int tb = M < BN_MAX ? (M + 15) & ~15 : BN_MAX;
-  const size_t plane = (size_t)ceil_div(M, tb) * tb * pc.rows;
-  unsigned char* digits = reinterpret_cast<unsigned char*>(base + w.digits);
-  int8_t* wt = reinterpret_cast<int8_t*>(base + w.wt);
-  float* colpart = reinterpret_cast<float*>(base + w.colpart);
   int32_t* colsum = reinterpret_cast<int32_t*>(base + w.colsum);
   int32_t* acc = reinterpret_cast<int32_t*>(base + w.acc);
-  int* listed = reinterpret_cast<int*>(base + w.listed);
-  int2* list = reinterpret_cast<int2*>(base + w.list);
+  Piece p{};
+  p.W = W;
+  p.s_row = s_row;
+  p.q = qa.q;
+  p.labels = labels;
+  p.tf = tf;
+  p.listed = reinterpret_cast<int*>(base + w.listed);
+  p.list = reinterpret_cast<int2*>(base + w.list);
+  p.digits = reinterpret_cast<unsigned char*>(base + w.digits);
+  p.wt = reinterpret_cast<int8_t*>(base + w.wt);
+  p.colpart = reinterpret_cast<float*>(base + w.colpart);
+  p.ds_row = ds_row;
+  p.err = reinterpret_cast<int*>(base);
+  p.V = V;
+  p.d = d;
+  p.M = M;
+  p.Vp = pc.rows;
+  p.l = layout(M, d);
+  const auto products = p.l.cg == 1 ? (ds_row ? piece_products<1, true> : piece_products<1, false>)
+                                    : (ds_row ? piece_products<2, true> : piece_products<2, false>);
   for (int i = 0; i < pc.n; ++i) {
-    const int v0 = i * pc.rows, nv = V - v0 < pc.rows ? V - v0 : pc.rows;
-    const int kblocks = ceil_div(nv, BK);
-    e = launch_pdl(transpose_kernel, dim3(ceil_div(kblocks * BK, TR_ROWS * 8), ceil_div(d, 128)), dim3(256), 0, s, W, V,
-                   d, v0, pc.rows, wt, colsum);
+    p.v0 = i * pc.rows;
+    p.nv = V - p.v0 < pc.rows ? V - p.v0 : pc.rows;
+    p.acc = acc + (size_t)(i / pc.per_set) * 3 * M * d;
+    e = launch_pdl(transpose_kernel, dim3(ceil_div(ceil_div(p.nv, BK) * BK, TR_ROWS * 8), (int)(p.l.dp / 128)),
+                   dim3(256), 0, s, W, V, d, p.v0, pc.rows, p.wt, colsum);
     if (e != cudaSuccess) return record_cuda_failure(e);
-    ForwardPolicy::Args ra{};
-    st = row_args(ra, M, nv, v0, d, W, V, qa.q, err);
+    st = products(p, s);
     if (st) return st;
-    const auto digit_product = ds_row ? launch_digits<true> : launch_digits<false>;
-    e = digit_product(ra.r, ra.c, ra.map_a, ra.map_b, tf, listed, list, labels, s_row, digits, colpart, M, v0, pc.rows, tb,
-                      plane, s);
-    if (e != cudaSuccess) return record_cuda_failure(e);
-    if (ds_row) {
-      e = launch_pdl(ds_finish_kernel, dim3(ceil_div(nv, 256)), dim3(256), 0, s, (const float*)colpart,
-                     ceil_div(M, 32), pc.rows, nv, ds_row + v0);
-      if (e != cudaSuccess) return record_cuda_failure(e);
-    }
-    GradPolicy::Args g{};
-    g.c.b_tile = tb;
-    g.c.stages = ring_stages(tb, 0);
-    g.c.err = err;
-    g.digits = digits;
-    g.wt = wt;
-    g.acc = acc + (size_t)(i / pc.per_set) * 3 * M * d;
-    g.plane = plane;
-    g.M = M;
-    g.d = d;
-    g.Vp = pc.rows;
-    g.tb = tb;
-    g.kblocks = kblocks;
-    e = launch_gemm<GradPolicy>(g, num_sms(), 0, s);
-    if (e != cudaSuccess) return record_cuda_failure(e);
   }
   GradFinishArgs fa{};
   fa.acc = acc;
   fa.colsum = colsum;
   fa.srow = tf.srow;
   fa.fac = tf.fac;
-  fa.listed = listed;
-  fa.list = list;
+  fa.listed = p.listed;
+  fa.list = p.list;
   fa.labels = labels;
   fa.W = W;
   fa.s_row = s_row;

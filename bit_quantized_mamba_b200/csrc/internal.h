@@ -221,6 +221,8 @@ int noalloc_status_word(int** out);
 // 128 bytes x box_rows rows and the 128-byte swizzle (16-byte chunk c of row r lands at chunk c ^ (r & 7));
 // what a box covers past a row's end or the last row reads as zero.
 bool encode_u8_map_sw128(CUtensorMap* map, const void* base, int rows, int row_bytes, int box_rows);
+// Memory as blocks of 128 contiguous bytes, copied unchanged in boxes of box_blocks blocks.
+bool encode_blocks_map(CUtensorMap* map, const void* base, int64_t blocks, int box_blocks);
 // Argument checks shared by the many-token operators on an int8 matrix W [V][d] (common to the embedding,
 // the linear and the loss), and of rows of d values of type x_type, ldx apart (16-byte aligned rows).
 int check_int8_matrix(const int8_t* W, int V, int d);

@@ -2,6 +2,8 @@
 // of the stream still runs, and waits for it in pdl_wait() (common.cuh).
 #pragma once
 
+#include <cstddef>
+
 #include <cuda_runtime.h>
 
 namespace dfssm {
@@ -19,6 +21,27 @@ static cudaError_t launch_pdl(Kern k, dim3 grid, dim3 block, size_t smem, cudaSt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+// The same in clusters of `cluster` CTAs.
+template <typename Kern, typename... Args>
+static cudaError_t launch_pdl_cluster(int cluster, Kern k, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                                      Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 

@@ -17,8 +17,9 @@ namespace {
 
 using namespace gemm_i8;
 
-template <typename Y>
+template <typename Y, int CG_>
 struct LinearPolicy {
+  static constexpr int CG = CG_;
   struct Args {
     CUtensorMap map_a, map_b;  // W, codes
     RowArgs r;
@@ -30,10 +31,11 @@ struct LinearPolicy {
     int32_t* acc;         // [M][V] or NULL
     int V;
   };
-  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile(a.r, 1, j, t); }
-  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int kb, unsigned char* sa,
-                                              unsigned char* sb, uint64_t* bar) {
-    row_load(a.r, &a.map_a, &a.map_b, t, kb, sa, sb, bar);
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 1, j, t); }
+  static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
+  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int rank, int kb, unsigned char* sa,
+                                              unsigned char* sb, uint32_t bar) {
+    row_load<CG>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
     return umma_desc_k_sw128(addr + kk * UMMA_K);
@@ -78,25 +80,25 @@ struct LinearPolicy {
 
 inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-template <typename Y>
+template <typename Y, int CG>
 int launch_linear(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, const double* s, int M, Y* y,
                   int64_t ldy, int32_t* acc, int* err, cudaStream_t st) {
-  typename LinearPolicy<Y>::Args a{};
-  const int sms = num_sms();
+  using P = LinearPolicy<Y, CG>;
+  typename P::Args a{};
   a.r.rows_a = V;
   a.r.rows_b = M;
   a.r.kblocks = (d + BK - 1) / BK;
-  // one tile of tokens: W streams through once, in balanced ranges of rows (memory bound).  More: whole tiles
-  // of 128 x 256, the tokens' index fastest.
+  // one tile of tokens: W streams through once, in balanced ranges of rows.  More: whole tiles, the tokens' index
+  // fastest.
   const bool range = M <= BN_MAX;
   a.r.mode = range ? kRangeA : kGrid;
-  const int bt = range ? (M + 15) & ~15 : BN_MAX;
+  a.r.tile_b = BN_MAX;
   a.r.box_a = range ? 32 : BM;
+  const int bt = range ? (M + 16 * CG - 1) / (16 * CG) * 16 : BN_MAX / CG;  // a CTA's columns
   a.r.box_b = bt;
   a.c.b_tile = bt;
   a.c.stages = ring_stages(bt, 0);
   a.c.err = err;
-  a.r.c = a.c;
   a.s_tok = s;
   a.s_row = s_row;
   a.y = y;
@@ -105,12 +107,20 @@ int launch_linear(const int8_t* W, const float* s_row, int V, int d, const int8_
   a.V = V;
   if (!encode_u8_map_sw128(&a.map_a, W, V, d, a.r.box_a) || !encode_u8_map_sw128(&a.map_b, q, M, d, bt))
     return DFSSM_EUNSUPPORTED;
-  const long long units = range ? (V + 31) / 32 : (long long)((V + BM - 1) / BM) * ((M + BN_MAX - 1) / BN_MAX);
-  const int grid = (int)(units < sms ? units : sms);
-  const auto k = kernel<LinearPolicy<Y>>;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(k), SMEM_LIMIT);
-  if (e == cudaSuccess) e = launch_pdl(k, dim3(grid), dim3(THREADS), smem_bytes(a.c, 0), st, a);
+  const long long units = range ? (V + 31) / 32
+                                : (long long)((V + BM * CG - 1) / (BM * CG)) * ((M + BN_MAX - 1) / BN_MAX);
+  const int most = max_groups<P>();
+  const cudaError_t e = launch<P>(a, (int)(units < most ? units : most), 0, st);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
+}
+
+// Up to 128 tokens the stream of W bounds the product and single CTAs keep more of it in flight; above, pairs halve
+// the traffic of the tokens' codes.
+template <typename Y>
+int launch_linear(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, const double* s, int M, void* y,
+                  int64_t ldy, int32_t* acc, int* err, cudaStream_t st) {
+  const auto f = M <= 128 ? launch_linear<Y, 1> : launch_linear<Y, 2>;
+  return f(W, s_row, V, d, q, s, M, static_cast<Y*>(y), ldy, acc, err, st);
 }
 
 }  // namespace
@@ -155,9 +165,6 @@ extern "C" int dfssm_linear_int8(const int8_t* W, const float* s_row, int V, int
   }
   const cudaError_t e = launch_rows_quant(qa, s);
   if (e != cudaSuccess) return record_cuda_failure(e);
-  int32_t* acc = dbg ? dbg->acc : nullptr;
-  int* err = reinterpret_cast<int*>(p);
-  if (y_type == DFSSM_F32)
-    return launch_linear<float>(W, s_row, V, d, qa.q, qa.s, M, static_cast<float*>(y), ldy, acc, err, s);
-  return launch_linear<__nv_bfloat16>(W, s_row, V, d, qa.q, qa.s, M, static_cast<__nv_bfloat16*>(y), ldy, acc, err, s);
+  const auto f = y_type == DFSSM_F32 ? launch_linear<float> : launch_linear<__nv_bfloat16>;
+  return f(W, s_row, V, d, qa.q, qa.s, M, y, ldy, dbg ? dbg->acc : nullptr, reinterpret_cast<int*>(p), s);
 }
