@@ -149,7 +149,21 @@ inline size_t smem_bytes(const Common& c, int epi_bytes) {
   return 1024 + (size_t)c.stages * stage_bytes(c) + BAR_BYTES + epi_bytes;
 }
 
-// What a pair of a tile belongs to this CTA of it.
+// Position in the ring of stages: the stage, the parity of its phase, and how often the ring went round.
+struct Ring {
+  int s, stages, round;
+  uint32_t phase;
+  __device__ __forceinline__ explicit Ring(int n) : s(0), stages(n), round(0), phase(0u) {}
+  __device__ __forceinline__ void next() {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1u;
+      round = 1;
+    }
+  }
+};
+
+// What of a pair's tile belongs to this CTA of it.
 template <int CG>
 __device__ __forceinline__ Tile own_tile(Tile t, int rank) {
   if (CG == 2) {
@@ -214,15 +228,15 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
   if (warp == 0 && lane == 0) {
     // ---- producer: each tile's K steps through the stage ring
     pdl_wait();
-    int it = 0;
+    Ring ring(stages);
     bool ok = true;
     Tile pt;
     for (int j = 0; ok && P::tile(ar, j, pt); ++j) {
       const Tile t = own_tile<CG>(pt, rank);
       const uint32_t bytes = P::bytes(ar, pt);  // of the whole tile's K step, both CTAs'
-      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-        const int s = it % stages;
-        if (it >= stages && !mbar_wait(&empty[s], ((it / stages) - 1) & 1, &abort_flag)) {
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next()) {
+        const int s = ring.s;
+        if (ring.round > 0 && !mbar_wait(&empty[s], ring.phase ^ 1u, &abort_flag)) {
           abort_flag = 1;
           ok = false;
           break;
@@ -235,18 +249,26 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
     // the last copies land before this CTA may exit (those of a pair's second CTA are counted by the first, which
     // the cluster barrier at the end waits for; after an abort they get a millisecond)
     if (rank == 0) {
-      for (int j = (it > stages ? it - stages : 0); j < it; ++j)
-        mbar_wait_drain(&full[j % stages], (j / stages) & 1);
+      // the stage's last copy has the phase of the ring's current round, or of the one before
+      for (int i = 0; i < stages; ++i) {
+        if (i < ring.s) mbar_wait_drain(&full[i], ring.phase);
+        else if (ring.round > 0) mbar_wait_drain(&full[i], ring.phase ^ 1u);
+      }
     } else if (!ok) {
       const long long t0 = clock64();
       while (clock64() - t0 < 2000000LL) {
       }
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
-    // ---- MMA issuer
-    int it = 0, local = 0;
+    // ---- MMA issuer: one thread, so what it does per K step is kept short (descriptors by addition, no divisions:
+    // with them a step took 800 clocks instead of the product's 512)
+    Ring ring(stages);
+    int local = 0;
     bool ok = true, issued = false;
     Tile t;
+    const uint32_t smem0 = smem_u32(smem);
+    const uint64_t a_desc = P::adesc(smem0), b_desc = P::bdesc(ar, smem0 + A_BYTES);
+    const uint64_t a_step = P::a_step(), b_step = P::b_step(ar);  // 32 bytes of K on, in 16-byte units
     for (; ok && P::tile(ar, local, t); ++local) {
       const int buf = local & 1;
       if (local >= 2 && !mbar_wait(&acc_empty[buf], ((local >> 1) - 1) & 1, &abort_flag)) {
@@ -256,20 +278,24 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN_MAX);
       const uint32_t id = idesc<CG>(mma_n<CG>(t.nb));
-      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-        const int s = it % stages;
-        if (!mbar_wait(&full[s], (it / stages) & 1, &abort_flag)) {
+      uint32_t accum = 0u;
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next()) {
+        if (!mbar_wait(&full[ring.s], ring.phase, &abort_flag)) {
           abort_flag = 1;
           ok = false;
           break;
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t a_addr = smem_u32(smem + (size_t)s * sbytes);
+        const uint64_t off = (uint64_t)((uint32_t)(ring.s * sbytes) >> 4);
+        uint64_t ad = a_desc + off, bd = b_desc + off;
 #pragma unroll
-        for (int kk = 0; kk < BK / UMMA_K; ++kk)
-          umma<CG>(d_tmem, P::adesc(a_addr, kk), P::bdesc(ar, a_addr + A_BYTES, kk), id,
-                   (kb > t.kb0 || kk > 0) ? 1u : 0u);
-        commit<CG>(&empty[s]);
+        for (int kk = 0; kk < BK / UMMA_K; ++kk) {
+          umma<CG>(d_tmem, ad, bd, id, accum);
+          accum = 1u;
+          ad += a_step;
+          bd += b_step;
+        }
+        commit<CG>(&empty[ring.s]);
         issued = true;
       }
       if (!ok) break;

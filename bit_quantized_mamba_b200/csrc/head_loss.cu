@@ -74,12 +74,10 @@ struct ForwardPolicy {
                                               unsigned char* sb, uint32_t bar) {
     row_load<CG>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar);
   }
-  static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
-    return umma_desc_k_sw128(addr + kk * UMMA_K);
-  }
-  static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr, int kk) {
-    return umma_desc_k_sw128(addr + kk * UMMA_K);
-  }
+  static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
+  static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
+  static __device__ __forceinline__ uint64_t a_step() { return UMMA_K >> 4; }
+  static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
   static constexpr int EPI_SMEM = EPI_WARPS * 32 * 4;
   struct Epilogue {
     int q, half, lane;
@@ -365,12 +363,10 @@ struct DigitPolicy {
                                               unsigned char* sb, uint32_t bar) {
     row_load<CG>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar);
   }
-  static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
-    return umma_desc_k_sw128(addr + kk * UMMA_K);
-  }
-  static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr, int kk) {
-    return umma_desc_k_sw128(addr + kk * UMMA_K);
-  }
+  static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
+  static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
+  static __device__ __forceinline__ uint64_t a_step() { return UMMA_K >> 4; }
+  static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
   static constexpr int EPI_SMEM = EPI_WARPS * 32 * 4;
   struct Epilogue {
     int q, half, lane;
@@ -510,12 +506,12 @@ struct GradPolicy {
     tma_load<CG>(sa, &a.map_a, 0, (int)((size_t)t.a0 * a.Vp / 128) + kb * BM, bar);
     tma_load<CG>(sb, &a.map_b, 0, (int)((t.aux * a.plane + (size_t)(t.b0 + rank * a.tb) * a.Vp) / 128) + kb * a.tb, bar);
   }
-  static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
-    return umma_desc_k_plain(addr + kk * 2 * (BM * 16), BM * 16);
+  static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_plain(addr, BM * 16); }
+  static __device__ __forceinline__ uint64_t bdesc(const Args& a, uint32_t addr) {
+    return umma_desc_k_plain(addr, a.tb * 16);
   }
-  static __device__ __forceinline__ uint64_t bdesc(const Args& a, uint32_t addr, int kk) {
-    return umma_desc_k_plain(addr + kk * 2 * (a.tb * 16), a.tb * 16);
-  }
+  static __device__ __forceinline__ uint64_t a_step() { return 2 * BM; }
+  static __device__ __forceinline__ uint64_t b_step(const Args& a) { return (uint64_t)(2 * a.tb); }
   struct Epilogue {
     int q, half, lane;
     __device__ __forceinline__ Epilogue(const Args&, unsigned char*, int q_, int half_, int lane_)

@@ -37,12 +37,10 @@ struct LinearPolicy {
                                               unsigned char* sb, uint32_t bar) {
     row_load<CG>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar);
   }
-  static __device__ __forceinline__ uint64_t adesc(uint32_t addr, int kk) {
-    return umma_desc_k_sw128(addr + kk * UMMA_K);
-  }
-  static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr, int kk) {
-    return umma_desc_k_sw128(addr + kk * UMMA_K);
-  }
+  static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
+  static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
+  static __device__ __forceinline__ uint64_t a_step() { return UMMA_K >> 4; }
+  static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
   struct Epilogue {
     int q, half, lane;
     __device__ __forceinline__ Epilogue(const Args&, unsigned char*, int q_, int half_, int lane_)
