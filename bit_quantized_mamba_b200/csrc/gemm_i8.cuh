@@ -30,6 +30,7 @@ constexpr int UMMA_K = 32;   // K bytes of one kind::i8 MMA
 constexpr int A_BYTES = BM * BK;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = (2 + EPI_WARPS) * 32;
+constexpr int EPI_COLS = BN_MAX / 2;  // columns of an epilogue warp: chunks 0, 2, 4, .. or 1, 3, 5, .. of a tile
 constexpr int MAX_STAGES = 12;
 constexpr int SMEM_LIMIT = 232448;  // 227 KB: the shared memory a CTA may have, all of it dynamic here
 constexpr int BAR_BYTES = 256;
@@ -131,7 +132,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the tensor-memory loads issued so far; the registers named are not used before.
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
 
 // What every policy's arguments start with.
 struct Common {
@@ -314,13 +321,15 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
     Tile t;
     for (; P::tile(ar, local, t); ++local) {
       const int buf = local & 1;
+      const Tile own = own_tile<CG>(t, rank);
+      epi.prepare(ar, own);  // what the tile needs from memory, fetched while its products run
       if (abort_flag || !mbar_wait(&acc_full[buf], (local >> 1) & 1, &abort_flag)) {
         abort_flag = 1;
         break;
       }
       __syncwarp();
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      epi.tile(ar, own_tile<CG>(t, rank), tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(buf * BN_MAX));
+      epi.tile(ar, own, tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(buf * BN_MAX));
       // this warp's reads of the accumulator are complete
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();

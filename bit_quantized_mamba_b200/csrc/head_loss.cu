@@ -78,43 +78,57 @@ struct ForwardPolicy {
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t a_step() { return UMMA_K >> 4; }
   static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
-  static constexpr int EPI_SMEM = EPI_WARPS * 32 * 4;
+  static constexpr int EPI_SMEM = EPI_WARPS * EPI_COLS * 4;
   struct Epilogue {
-    int q, half, lane;
-    float* sr;        // this warp's 32 row scales of a chunk, in units of log 2
-    int tok = -1;     // the token whose running (m, S) this thread holds
+    int half, lane, row;  // row: lane of the tile
+    float* sr;            // row scales of this warp's columns (chunks of 32: half, half + 2, ..), in units of log 2
+    int tok = -1;         // the token whose running (m, S) this thread holds
     int slot = 0;
     float m = -INFINITY, S = 0.0f;
-    __device__ __forceinline__ Epilogue(const Args&, unsigned char* sm, int q_, int half_, int lane_)
-        : q(q_), half(half_), lane(lane_), sr(reinterpret_cast<float*>(sm) + (half_ * 4 + q_) * 32) {}
+    float st;             // the token's scale and label
+    int label;
+    __device__ __forceinline__ Epilogue(const Args&, unsigned char* sm, int q, int half_, int lane_)
+        : half(half_), lane(lane_), row(q * 32 + lane_),
+          sr(reinterpret_cast<float*>(sm) + (half_ * 4 + q) * EPI_COLS) {}
     __device__ __forceinline__ void flush(const Args& a) {
       if (tok >= 0 && tok < a.M) a.part[(size_t)slot * a.M + tok] = make_float2(m, S);
       m = -INFINITY;
       S = 0.0f;
     }
-    __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
-      const int tk = t.a0 + q * 32 + lane;
+    __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
+      const int tk = t.a0 + row;
       const int sl = (a.r.mode == kGrid ? t.b0 / a.r.tile_b : (int)blockIdx.x / CG) * 2 + half;
       if (tk != tok || sl != slot) {
         flush(a);
         tok = tk;
         slot = sl;
       }
-      const bool valid = tk < a.M;
-      const float st = valid ? (float)a.s_tok[tk] : 0.0f;
-      const int label = valid ? a.labels[tk] : -1;
-      for (int c = half * 32; c < t.nb; c += 64) {
-        uint32_t v[32];
-        tmem_ld32(taddr + (uint32_t)c, v);
+      st = tk < a.M ? (float)a.s_tok[tk] : 0.0f;
+      label = tk < a.M ? a.labels[tk] : -1;
+#pragma unroll
+      for (int k = 0; k < EPI_COLS / 32; ++k) {
+        const int c = k * 64 + half * 32 + lane;
+        sr[k * 32 + lane] = c < t.nb ? scale2(__ldg(a.s_row + t.b0 + c)) : 0.0f;
+      }
+      __syncwarp();
+    }
+    __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
+      uint32_t vb[2][32];
+      int c = half * 32;
+      if (c < t.nb) tmem_ld32(taddr + (uint32_t)c, vb[0]);
+#pragma unroll
+      for (int k = 0; k < EPI_COLS / 32; ++k, c += 64) {
+        if (c >= t.nb) break;
+        uint32_t(&v)[32] = vb[k & 1];
+        tmem_wait(v);
+        if (c + 64 < t.nb) tmem_ld32(taddr + (uint32_t)c + 64, vb[(k + 1) & 1]);
         const int v0 = t.b0 + c;
-        __syncwarp();
-        sr[lane] = c + lane < t.nb ? scale2(__ldg(a.s_row + v0 + lane)) : 0.0f;
-        __syncwarp();
+        const float* w1 = sr + k * 32;
+        const float4* w4 = reinterpret_cast<const float4*>(w1);
         // columns that do not count: past the tile's end, and the token's own label
         uint32_t skip = c + 32 > t.nb ? 0xFFFFFFFFu << (t.nb - c) : 0u;
         const uint32_t lc = (uint32_t)(label - v0);
         if (lc < 32u) skip |= 1u << lc;
-        tmem_wait();
         float x[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[j] = (float)(int)v[j] * st;
@@ -123,75 +137,77 @@ struct ForwardPolicy {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (j == (int)lc) al = (int)v[j];
-          a.label_logit[tk] = __double2float_rn(dmul(dmul(int_to_f64(al), a.s_tok[tk]), (double)__ldg(a.s_row + label)));
+          a.label_logit[tok] = __double2float_rn(dmul(dmul(int_to_f64(al), a.s_tok[tok]), (double)__ldg(a.s_row + label)));
         }
         float mx = m;
-        const float4* sr4 = reinterpret_cast<const float4*>(sr);
         if (!__any_sync(0xffffffffu, skip != 0u)) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 w = sr4[j / 4];
+            const float4 w = w4[j / 4];
             mx = fmaxf(mx, fmaxf(fmaxf(x[j] * w.x, x[j + 1] * w.y), fmaxf(x[j + 2] * w.z, x[j + 3] * w.w)));
           }
           float s = S * ex2(m - mx);
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 w = sr4[j / 4];
-            s += ex2(fmaf(x[j], w.x, -mx)) + ex2(fmaf(x[j + 1], w.y, -mx)) + ex2(fmaf(x[j + 2], w.z, -mx)) +
-                 ex2(fmaf(x[j + 3], w.w, -mx));
+            const float4 w = w4[j / 4];
+            s += (ex2(fmaf(x[j], w.x, -mx)) + ex2(fmaf(x[j + 1], w.y, -mx))) +
+                 (ex2(fmaf(x[j + 2], w.z, -mx)) + ex2(fmaf(x[j + 3], w.w, -mx)));
           }
           S = s;
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (!((skip >> j) & 1u)) mx = fmaxf(mx, x[j] * sr[j]);
+            if (!((skip >> j) & 1u)) mx = fmaxf(mx, x[j] * w1[j]);
           const float mz = mx == -INFINITY ? 0.0f : mx;  // nothing counted yet
           float s = S * ex2(m - mz);
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (!((skip >> j) & 1u)) s += ex2(fmaf(x[j], sr[j], -mz));
+            if (!((skip >> j) & 1u)) s += ex2(fmaf(x[j], w1[j], -mz));
           S = s;
         }
         m = mx;
       }
+      __syncwarp();  // the scales are read: the next tile's may be written
     }
     __device__ __forceinline__ void finish(const Args& a) { flush(a); }
   };
 };
 
-// Joins the partial (max, sum) of a token and forms its loss.  32 tokens per CTA, eight slices of slots.
-__global__ void __launch_bounds__(256) loss_finish_kernel(const float2* __restrict__ part, int slots, int M, int V,
-                                                          const int32_t* __restrict__ labels,
-                                                          float* __restrict__ stats, float* __restrict__ loss,
-                                                          int* status) {
+// Joins the partial (max, sum) of a token and forms its loss.  32 tokens per CTA, 16 slices of slots; the second
+// pass over a slice comes from L1/L2.
+constexpr int LF_SLICES = 16;
+__global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float2* __restrict__ part, int slots, int M,
+                                                                     int V, const int32_t* __restrict__ labels,
+                                                                     float* __restrict__ stats,
+                                                                     float* __restrict__ loss, int* status) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ float sm[8][32];
-  __shared__ double ss[8][32];
+  __shared__ float sm[LF_SLICES][32];
+  __shared__ double ss[LF_SLICES][32];
   const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
   const int t = blockIdx.x * 32 + lane;
   float m = -INFINITY;
-  double S = 0.0;
   if (t < M) {
-    for (int s = sl; s < slots; s += 8) {
-      const float2 p = part[(size_t)s * M + t];
-      const float mn = fmaxf(m, p.x);
-      if (mn > -INFINITY) S = S * exp2((double)m - mn) + (double)p.y * exp2((double)p.x - mn);
-      m = mn;
-      if (!(p.y >= 0.0f)) S = (double)p.y;  // NaN
-    }
+#pragma unroll 8
+    for (int s = sl; s < slots; s += LF_SLICES) m = fmaxf(m, part[(size_t)s * M + t].x);
   }
   sm[sl][lane] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < LF_SLICES; ++i) m = fmaxf(m, sm[i][lane]);
+  const float mz = m == -INFINITY ? 0.0f : m;
+  double S = 0.0;
+  if (t < M) {
+#pragma unroll 8
+    for (int s = sl; s < slots; s += LF_SLICES) {
+      const float2 p = part[(size_t)s * M + t];
+      S += (double)(p.y * ex2(p.x - mz));  // an empty part is (-inf, 0); a NaN sum stays one
+    }
+  }
   ss[sl][lane] = S;
   __syncthreads();
   if (sl != 0 || t >= M) return;
-  for (int i = 1; i < 8; ++i) {
-    const float mi = sm[i][lane];
-    const float mn = fmaxf(m, mi);
-    if (mn > -INFINITY) S = S * exp2((double)m - mn) + ss[i][lane] * exp2((double)mi - mn);
-    else S += ss[i][lane];
-    m = mn;
-  }
+  for (int i = 1; i < LF_SLICES; ++i) S += ss[i][lane];
   const int y = labels[t];
   const bool bad = y >= V;
   if (bad) atomicExch(status, kBadTokenCode);
@@ -296,7 +312,7 @@ __device__ __forceinline__ float dither(uint32_t acc) {
 
 // W's piece [nv rows from v0] as K-major operand of the second product, [d / 128][Vp / 16][128][16] bytes
 // (zero past the vocabulary and past d), and the column sums of W.  A thread turns 16 rows x 4 columns.
-constexpr int TR_ROWS = 16 * 8;  // vocabulary rows per warp
+constexpr int TR_ROWS = 16 * 2;  // vocabulary rows per warp
 __global__ void __launch_bounds__(256) transpose_kernel(const int8_t* __restrict__ W, int V, int d, int v0, int Vp,
                                                         int8_t* __restrict__ wt, int32_t* __restrict__ colsum) {
   pdl_launch_dependents();
@@ -332,9 +348,16 @@ __global__ void __launch_bounds__(256) transpose_kernel(const int8_t* __restrict
 #pragma unroll
     for (int k = 0; k < 4; ++k) dst[k] = o[k];
   }
+  __shared__ int part[8][128];
+  *reinterpret_cast<int4*>(&part[warp][4 * lane]) = make_int4(sums[0], sums[1], sums[2], sums[3]);
+  __syncthreads();
+  const int i = threadIdx.x;
+  if (i < 128 && db * 128 + i < d) {
+    int s = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (col < d && sums[k]) atomicAdd(colsum + col + k, sums[k]);
+    for (int w = 0; w < 8; ++w) s += part[w][i];
+    if (s) atomicAdd(colsum + db * 128 + i, s);
+  }
 }
 
 // The first product of the gradient: digits of a piece, and the row scales' gradient per 32 tokens.
@@ -367,37 +390,55 @@ struct DigitPolicy {
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t a_step() { return UMMA_K >> 4; }
   static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
-  static constexpr int EPI_SMEM = EPI_WARPS * 32 * 4;
+  static constexpr int EPI_SMEM = EPI_WARPS * EPI_COLS * 8;
   struct Epilogue {
     int q, half, lane;
-    float* sr;
+    float* sr;   // row scales of this warp's columns (chunks of 32: half, half + 2, ..), in units of log 2
+    float* cu;   // the same times the steps per unit
     FixedPoint fp;
+    float4 tf;
+    int label, most;
     __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int half_, int lane_)
-        : q(q_), half(half_), lane(lane_), sr(reinterpret_cast<float*>(sm) + (half_ * 4 + q_) * 32),
-          fp(fixed_point(a.srow)) {}
+        : q(q_), half(half_), lane(lane_), sr(reinterpret_cast<float*>(sm) + (half_ * 4 + q_) * 2 * EPI_COLS),
+          cu(sr + EPI_COLS), fp(fixed_point(a.srow)) {}
+    __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
+      const int tk = t.a0 + q * 32 + lane;
+      const bool valid = tk < a.M;
+      tf = valid ? a.tok[tk] : make_float4(0.f, 0.f, 0.f, 0.f);
+      label = valid ? a.labels[tk] - a.v0 : -1;
+      most = (fp.range << (valid ? a.shift[tk] : 0)) - 1;
+#pragma unroll
+      for (int k = 0; k < EPI_COLS / 32; ++k) {
+        const int c = k * 64 + half * 32 + lane;
+        const float w = c < t.nb ? scale2(__ldg(a.s_row + a.v0 + t.b0 + c)) : 0.0f;
+        sr[k * 32 + lane] = w;
+        cu[k * 32 + lane] = w * fp.unit;
+      }
+      __syncwarp();
+    }
     __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
       const int tk = t.a0 + q * 32 + lane;
       const bool valid = tk < a.M;
-      const float4 tf = valid ? a.tok[tk] : make_float4(0.f, 0.f, 0.f, 0.f);
-      const int label = valid ? a.labels[tk] - a.v0 : -1;
-      const int most = (fp.range << (valid ? a.shift[tk] : 0)) - 1;
       unsigned char* dst = a.digits + (size_t)(tk / a.tb) * a.tb * a.Vp + (size_t)(tk % a.tb) * 16;
-      for (int c = half * 32; c < t.nb; c += 64) {
-        uint32_t v[32];
-        tmem_ld32(taddr + (uint32_t)c, v);
+      uint32_t vb[2][32];
+      int c = half * 32;
+      if (c < t.nb) tmem_ld32(taddr + (uint32_t)c, vb[0]);
+#pragma unroll
+      for (int ch = 0; ch < EPI_COLS / 32; ++ch, c += 64) {
+        if (c >= t.nb) break;
+        uint32_t(&v)[32] = vb[ch & 1];
+        tmem_wait(v);
+        if (c + 64 < t.nb) tmem_ld32(taddr + (uint32_t)c + 64, vb[(ch + 1) & 1]);
         const int v0 = t.b0 + c;  // within the piece
-        __syncwarp();
-        sr[lane] = c + lane < t.nb ? scale2(__ldg(a.s_row + a.v0 + v0 + lane)) : 0.0f;
-        __syncwarp();
         const uint32_t lc = (uint32_t)(label - v0);
         const bool any = __any_sync(0xffffffffu, lc < 32u);
-        tmem_wait();
         float h[32];
         uint32_t high = 0u;
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-          const float4 w = reinterpret_cast<const float4*>(sr)[j / 4];
-          const float wv[4] = {w.x, w.y, w.z, w.w};
+          const float4 w = reinterpret_cast<const float4*>(sr + ch * 32)[j / 4];
+          const float4 u = reinterpret_cast<const float4*>(cu + ch * 32)[j / 4];
+          const float wv[4] = {w.x, w.y, w.z, w.w}, uv[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float av = (float)(int)v[j + k];
@@ -407,23 +448,19 @@ struct DigitPolicy {
               e = 0.0f;
               if (DS) h[j + k] = tf.w * av;
             }
-            const float n = fmaf(e, wv[k] * fp.unit, dither(v[j + k]));
+            const float n = fmaf(e, uv[k], dither(v[j + k]));
             v[j + k] = (uint32_t)(min(__float2int_rn(n), most) + fp.offset);
             high |= v[j + k];
           }
         }
         if (valid && (high >> 24)) {
           // few: the order of a list does not matter, its sum is taken in integers
-          for (int j = 0; j < 32; ++j) {
-            uint32_t n = 0u;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (k == j) n = v[k];
-            if ((n >> 24) && c + j < t.nb) {
+          for (int j = 0; j < 32; ++j)
+            if ((v[j] >> 24) && c + j < t.nb) {
               const int i = atomicAdd(a.listed + tk, 1);
-              if (i < kListed) a.list[(size_t)tk * kListed + i] = make_int2(a.v0 + v0 + j, (int)n >> 24);
+              if (i < kListed) a.list[(size_t)tk * kListed + i] = make_int2(a.v0 + v0 + j, (int)v[j] >> 24);
             }
-          }
         }
         if (valid) {
           unsigned char* dp = dst + (size_t)(v0 >> 4) * a.tb * 16;
@@ -459,6 +496,7 @@ struct DigitPolicy {
           if (c + lane < t.nb) a.colpart[(size_t)(t.a0 / 32 + q) * a.Vp + v0 + lane] = h[0];
         }
       }
+      __syncwarp();  // the scales are read: the next tile's may be written
     }
     __device__ __forceinline__ void finish(const Args&) {}
   };
@@ -523,27 +561,35 @@ struct GradPolicy {
       for (int c = half * 32; c < n; c += 64) {
         uint32_t v[32];
         tmem_ld32(taddr + (uint32_t)c, v);
-        tmem_wait();
+        tmem_wait(v);
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           if (cv && c + j < n) atomicAdd(base + (size_t)(c + j) * a.d, (int)v[j]);
       }
     }
+    __device__ __forceinline__ void prepare(const Args&, const Tile&) {}
     __device__ __forceinline__ void finish(const Args&) {}
   };
 };
 
-// ds_row of a piece: the partial column sums of every 32 tokens, added in order.
+// ds_row of a piece: the partial column sums of every 32 tokens, eight slices of them, joined in order.
 __global__ void __launch_bounds__(256) ds_finish_kernel(const float* __restrict__ colpart, int parts, int Vp, int nv,
                                                         float* __restrict__ ds) {
   pdl_launch_dependents();
   pdl_wait();
-  const int v = blockIdx.x * 256 + threadIdx.x;
-  if (v >= nv) return;
+  __shared__ double red[8][32];
+  const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5, v = blockIdx.x * 32 + lane;
   double s = 0.0;
+  if (v < nv) {
 #pragma unroll 8
-  for (int p = 0; p < parts; ++p) s += (double)colpart[(size_t)p * Vp + v];
-  ds[v] = (float)s;
+    for (int p = sl; p < parts; p += 8) s += (double)colpart[(size_t)p * Vp + v];
+  }
+  red[sl][lane] = s;
+  __syncthreads();
+  if (sl == 0 && v < nv) {
+    for (int k = 1; k < 8; ++k) s += red[k][lane];
+    ds[v] = (float)s;
+  }
 }
 
 struct GradFinishArgs {
@@ -826,7 +872,7 @@ int forward(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, 
   cudaError_t e = launch<P>(a, groups, P::EPI_SMEM, st);
   const int slots = 2 * (a.r.mode == kGrid ? ceil_div(V, BN_MAX) : groups);
   if (e == cudaSuccess)
-    e = launch_pdl(loss_finish_kernel, dim3(ceil_div(M, 32)), dim3(256), 0, st, (const float2*)part, slots, M, V,
+    e = launch_pdl(loss_finish_kernel, dim3(ceil_div(M, 32)), dim3(32 * LF_SLICES), 0, st, (const float2*)part, slots, M, V,
                    labels, stats, loss, err);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
 }
@@ -872,7 +918,7 @@ int piece_products(const Piece& p, cudaStream_t st) {
   a.plane = plane;
   cudaError_t e = launch<P>(a, row_groups<P>(a.r), P::EPI_SMEM, st);
   if (DS && e == cudaSuccess)
-    e = launch_pdl(ds_finish_kernel, dim3(ceil_div(p.nv, 256)), dim3(256), 0, st, (const float*)p.colpart,
+    e = launch_pdl(ds_finish_kernel, dim3(ceil_div(p.nv, 32)), dim3(256), 0, st, (const float*)p.colpart,
                    ceil_div(p.M, 32), p.Vp, p.nv, p.ds_row + p.v0);
   if (e != cudaSuccess) return record_cuda_failure(e);
   using G = GradPolicy<CG>;

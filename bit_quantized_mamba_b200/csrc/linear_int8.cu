@@ -41,36 +41,51 @@ struct LinearPolicy {
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t a_step() { return UMMA_K >> 4; }
   static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
+  static constexpr int EPI_SMEM = EPI_WARPS * EPI_COLS * 8;
   struct Epilogue {
-    int q, half, lane;
-    __device__ __forceinline__ Epilogue(const Args&, unsigned char*, int q_, int half_, int lane_)
-        : q(q_), half(half_), lane(lane_) {}
-    __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
-      const int r = q * 32 + lane, row = t.a0 + r;
-      const bool rv = r < t.na;
-      const double sw = rv ? (double)__ldg(a.s_row + row) : 0.0;
-      // columns in chunks of 16, alternating between the quadrant's two warps
-      for (int c = half * 16; c < t.nb; c += 32) {
-        uint32_t v[16];
-        tmem_ld16(taddr + (uint32_t)c, v);
-        const int n = min(16, t.nb - c);
-        const double* st = a.s_tok + t.b0 + c;
-        Y* yp = a.y + (int64_t)(t.b0 + c) * a.ldy + row;
-        double s[16];
+    int half, lane, r;  // r: lane of the tile
+    double* s;          // scales of this warp's columns (chunks of 16: half, half + 2, ..)
+    double sw;
+    __device__ __forceinline__ Epilogue(const Args&, unsigned char* sm, int q, int half_, int lane_)
+        : half(half_), lane(lane_), r(q * 32 + lane_),
+          s(reinterpret_cast<double*>(sm) + (half_ * 4 + q) * EPI_COLS) {}
+    __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
+      sw = r < t.na ? (double)__ldg(a.s_row + t.a0 + r) : 0.0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) s[j] = j < n ? st[j] : 0.0;
-        tmem_wait();
+      for (int k = 0; k < EPI_COLS / 32; ++k) {
+        const int i = k * 32 + lane, c = (i >> 4) * 32 + half * 16 + (i & 15);
+        s[i] = c < t.nb ? a.s_tok[t.b0 + c] : 0.0;
+      }
+      __syncwarp();
+    }
+    __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
+      const int row = t.a0 + r;
+      const bool rv = r < t.na;
+      uint32_t v[2][16];
+      int c = half * 16;
+      if (c < t.nb) tmem_ld16(taddr + (uint32_t)c, v[0]);
+#pragma unroll
+      for (int k = 0; k < EPI_COLS / 16; ++k, c += 32) {
+        if (c >= t.nb) break;
+        uint32_t(&w)[16] = v[k & 1];
+        tmem_wait(w);
+        if (c + 32 < t.nb) tmem_ld16(taddr + (uint32_t)c + 32, v[(k + 1) & 1]);
+        const int n = min(16, t.nb - c);
+        const double* st = s + k * 16;
+        Y* yp = a.y + (int64_t)(t.b0 + c) * a.ldy + row;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float out = __double2float_rn(dmul(dmul(int_to_f64((int)v[j]), s[j]), sw));
-          if (rv && j < n) yp[(int64_t)j * a.ldy] = (Y)out;
+          const float out = __double2float_rn(dmul(dmul(int_to_f64((int)w[j]), st[j]), sw));
+          if (rv && j < n) *yp = (Y)out;
+          yp += a.ldy;
         }
         if (a.acc) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (rv && j < n) a.acc[(int64_t)(t.b0 + c + j) * a.V + row] = (int)v[j];
+            if (rv && j < n) a.acc[(int64_t)(t.b0 + c + j) * a.V + row] = (int)w[j];
         }
       }
+      __syncwarp();  // the scales are read: the next tile's may be written
     }
     __device__ __forceinline__ void finish(const Args&) {}
   };
@@ -95,7 +110,7 @@ int launch_linear(const int8_t* W, const float* s_row, int V, int d, const int8_
   const int bt = range ? (M + 16 * CG - 1) / (16 * CG) * 16 : BN_MAX / CG;  // a CTA's columns
   a.r.box_b = bt;
   a.c.b_tile = bt;
-  a.c.stages = ring_stages(bt, 0);
+  a.c.stages = ring_stages(bt, P::EPI_SMEM);
   a.c.err = err;
   a.s_tok = s;
   a.s_row = s_row;
@@ -108,7 +123,7 @@ int launch_linear(const int8_t* W, const float* s_row, int V, int d, const int8_
   const long long units = range ? (V + 31) / 32
                                 : (long long)((V + BM * CG - 1) / (BM * CG)) * ((M + BN_MAX - 1) / BN_MAX);
   const int most = max_groups<P>();
-  const cudaError_t e = launch<P>(a, (int)(units < most ? units : most), 0, st);
+  const cudaError_t e = launch<P>(a, (int)(units < most ? units : most), P::EPI_SMEM, st);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
 }
 
