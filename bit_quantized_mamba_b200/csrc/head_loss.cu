@@ -52,6 +52,18 @@ __device__ __forceinline__ float ex2(float x) {
 // 4.0e-8 off instead of 3.4e-8).
 __device__ __forceinline__ float scale2(float s_row) { return __double2float_rn((double)s_row * kLog2e); }
 
+// v[j] of an array in registers.
+__device__ __forceinline__ uint32_t pick(const uint32_t (&v)[32], int j) {
+  uint32_t x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = (j & 16) ? v[i + 16] : v[i];
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) x[i] = (j & n) ? x[i + n] : x[i];
+  return x[0];
+}
+
 // ------------------------------------------------------------------------------------ forward
 
 template <int CG_>
@@ -113,17 +125,13 @@ struct ForwardPolicy {
       __syncwarp();
     }
     __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
-      uint32_t vb[2][32];
-      int c = half * 32;
-      if (c < t.nb) tmem_ld32(taddr + (uint32_t)c, vb[0]);
-#pragma unroll
-      for (int k = 0; k < EPI_COLS / 32; ++k, c += 64) {
-        if (c >= t.nb) break;
-        uint32_t(&v)[32] = vb[k & 1];
+      uint32_t v[32];
+      const float* w1 = sr;
+      if (half * 32 < t.nb) tmem_ld32(taddr + (uint32_t)(half * 32), v);
+#pragma unroll 1  // four copies of the body would not stay in the instruction cache
+      for (int c = half * 32; c < t.nb; c += 64, w1 += 32) {
         tmem_wait(v);
-        if (c + 64 < t.nb) tmem_ld32(taddr + (uint32_t)c + 64, vb[(k + 1) & 1]);
         const int v0 = t.b0 + c;
-        const float* w1 = sr + k * 32;
         const float4* w4 = reinterpret_cast<const float4*>(w1);
         // columns that do not count: past the tile's end, and the token's own label
         uint32_t skip = c + 32 > t.nb ? 0xFFFFFFFFu << (t.nb - c) : 0u;
@@ -133,12 +141,10 @@ struct ForwardPolicy {
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[j] = (float)(int)v[j] * st;
         if (lc < 32u && c + (int)lc < t.nb) {
-          int al = 0;
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j == (int)lc) al = (int)v[j];
+          const int al = (int)pick(v, (int)lc);
           a.label_logit[tok] = __double2float_rn(dmul(dmul(int_to_f64(al), a.s_tok[tok]), (double)__ldg(a.s_row + label)));
         }
+        if (c + 64 < t.nb) tmem_ld32(taddr + (uint32_t)c + 64, v);  // the next chunk, while this one is summed
         float mx = m;
         if (!__any_sync(0xffffffffu, skip != 0u)) {
 #pragma unroll
@@ -420,15 +426,12 @@ struct DigitPolicy {
       const int tk = t.a0 + q * 32 + lane;
       const bool valid = tk < a.M;
       unsigned char* dst = a.digits + (size_t)(tk / a.tb) * a.tb * a.Vp + (size_t)(tk % a.tb) * 16;
-      uint32_t vb[2][32];
-      int c = half * 32;
-      if (c < t.nb) tmem_ld32(taddr + (uint32_t)c, vb[0]);
-#pragma unroll
-      for (int ch = 0; ch < EPI_COLS / 32; ++ch, c += 64) {
-        if (c >= t.nb) break;
-        uint32_t(&v)[32] = vb[ch & 1];
+      uint32_t v[32];
+      const float *w1 = sr, *u1 = cu;
+      if (half * 32 < t.nb) tmem_ld32(taddr + (uint32_t)(half * 32), v);
+#pragma unroll 1  // four copies of the body would not stay in the instruction cache
+      for (int c = half * 32; c < t.nb; c += 64, w1 += 32, u1 += 32) {
         tmem_wait(v);
-        if (c + 64 < t.nb) tmem_ld32(taddr + (uint32_t)c + 64, vb[(ch + 1) & 1]);
         const int v0 = t.b0 + c;  // within the piece
         const uint32_t lc = (uint32_t)(label - v0);
         const bool any = __any_sync(0xffffffffu, lc < 32u);
@@ -436,8 +439,8 @@ struct DigitPolicy {
         uint32_t high = 0u;
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-          const float4 w = reinterpret_cast<const float4*>(sr + ch * 32)[j / 4];
-          const float4 u = reinterpret_cast<const float4*>(cu + ch * 32)[j / 4];
+          const float4 w = reinterpret_cast<const float4*>(w1)[j / 4];
+          const float4 u = reinterpret_cast<const float4*>(u1)[j / 4];
           const float wv[4] = {w.x, w.y, w.z, w.w}, uv[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -455,12 +458,15 @@ struct DigitPolicy {
         }
         if (valid && (high >> 24)) {
           // few: the order of a list does not matter, its sum is taken in integers
+          uint32_t which = 0u;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if ((v[j] >> 24) && c + j < t.nb) {
-              const int i = atomicAdd(a.listed + tk, 1);
-              if (i < kListed) a.list[(size_t)tk * kListed + i] = make_int2(a.v0 + v0 + j, (int)v[j] >> 24);
-            }
+          for (int j = 0; j < 32; ++j) which |= (v[j] >> 24 ? 1u : 0u) << j;
+          if (c + 32 > t.nb) which &= ~(0xFFFFFFFFu << (t.nb - c));
+          while (which) {
+            const int j = __ffs(which) - 1, i = atomicAdd(a.listed + tk, 1);
+            which &= which - 1u;
+            if (i < kListed) a.list[(size_t)tk * kListed + i] = make_int2(a.v0 + v0 + j, (int)pick(v, j) >> 24);
+          }
         }
         if (valid) {
           unsigned char* dp = dst + (size_t)(v0 >> 4) * a.tb * 16;
@@ -482,6 +488,7 @@ struct DigitPolicy {
                   make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
           }
         }
+        if (c + 64 < t.nb) tmem_ld32(taddr + (uint32_t)c + 64, v);  // the next chunk
         if (DS) {
           // column sums over the warp's 32 tokens: halves exchanged at every step, lane j ends with column j
 #pragma unroll

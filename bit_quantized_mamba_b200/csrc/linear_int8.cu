@@ -61,29 +61,30 @@ struct LinearPolicy {
     __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
       const int row = t.a0 + r;
       const bool rv = r < t.na;
-      uint32_t v[2][16];
-      int c = half * 16;
-      if (c < t.nb) tmem_ld16(taddr + (uint32_t)c, v[0]);
-#pragma unroll
-      for (int k = 0; k < EPI_COLS / 16; ++k, c += 32) {
-        if (c >= t.nb) break;
-        uint32_t(&w)[16] = v[k & 1];
-        tmem_wait(w);
-        if (c + 32 < t.nb) tmem_ld16(taddr + (uint32_t)c + 32, v[(k + 1) & 1]);
+      uint32_t v[16];
+      const double* st = s;
+      Y* yp = a.y + (int64_t)(t.b0 + half * 16) * a.ldy + row;
+      if (half * 16 < t.nb) tmem_ld16(taddr + (uint32_t)(half * 16), v);
+#pragma unroll 1
+      for (int c = half * 16; c < t.nb; c += 32, st += 16) {
+        tmem_wait(v);
         const int n = min(16, t.nb - c);
-        const double* st = s + k * 16;
-        Y* yp = a.y + (int64_t)(t.b0 + c) * a.ldy + row;
+        double x[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float out = __double2float_rn(dmul(dmul(int_to_f64((int)w[j]), st[j]), sw));
-          if (rv && j < n) *yp = (Y)out;
-          yp += a.ldy;
-        }
+        for (int j = 0; j < 16; ++j) x[j] = int_to_f64((int)v[j]);
         if (a.acc) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (rv && j < n) a.acc[(int64_t)(t.b0 + c + j) * a.V + row] = (int)w[j];
+            if (rv && j < n) a.acc[(int64_t)(t.b0 + c + j) * a.V + row] = (int)v[j];
         }
+        if (c + 32 < t.nb) tmem_ld16(taddr + (uint32_t)c + 32, v);  // the next chunk, while this one is stored
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float out = __double2float_rn(dmul(dmul(x[j], st[j]), sw));
+          if (rv && j < n) *yp = (Y)out;
+          yp += a.ldy;
+        }
+        yp += 16 * a.ldy;
       }
       __syncwarp();  // the scales are read: the next tile's may be written
     }
