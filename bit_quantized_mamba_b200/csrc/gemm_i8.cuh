@@ -140,6 +140,8 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+enum Load { kLoadBoth = 0, kLoadW = 1, kLoadTokens = 2 };
+
 // What every policy's arguments start with.
 struct Common {
   int b_tile;   // columns a stage of one CTA has room for
@@ -234,13 +236,27 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
 
   if (warp == 0 && lane == 0) {
     // ---- producer: each tile's K steps through the stage ring
+    // With PDL the kernel may start while the one that writes the tokens' codes still runs: the first round of W
+    // (immutable) is requested before waiting for it.
+    int early = 0;
+    Tile pt;
+    if (P::W_EARLY) {
+      for (int j = 0; early < stages && P::tile(ar, j, pt); ++j) {
+        const Tile t = own_tile<CG>(pt, rank);
+        const uint32_t bytes = P::bytes(ar, pt);  // of the whole tile's K step, both CTAs'
+        for (int kb = t.kb0; kb < t.kb1 && early < stages; ++kb, ++early) {
+          unsigned char* st = smem + (size_t)early * sbytes;
+          if (rank == 0) mbar_expect_tx(&full[early], bytes);
+          P::load(ar, t, rank, kb, st, st + A_BYTES, leader_bar<CG>(&full[early]), kLoadW);
+        }
+      }
+    }
     pdl_wait();
     Ring ring(stages);
     bool ok = true;
-    Tile pt;
     for (int j = 0; ok && P::tile(ar, j, pt); ++j) {
       const Tile t = own_tile<CG>(pt, rank);
-      const uint32_t bytes = P::bytes(ar, pt);  // of the whole tile's K step, both CTAs'
+      const uint32_t bytes = P::bytes(ar, pt);
       for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next()) {
         const int s = ring.s;
         if (ring.round > 0 && !mbar_wait(&empty[s], ring.phase ^ 1u, &abort_flag)) {
@@ -249,8 +265,9 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
           break;
         }
         unsigned char* st = smem + (size_t)s * sbytes;
-        if (rank == 0) mbar_expect_tx(&full[s], bytes);
-        P::load(ar, t, rank, kb, st, st + A_BYTES, leader_bar<CG>(&full[s]));
+        const bool late = P::W_EARLY && ring.round == 0;  // its W is under way
+        if (rank == 0 && !late) mbar_expect_tx(&full[s], bytes);
+        P::load(ar, t, rank, kb, st, st + A_BYTES, leader_bar<CG>(&full[s]), late ? kLoadTokens : kLoadBoth);
       }
     }
     // the last copies land before this CTA may exit (those of a pair's second CTA are counted by the first, which
@@ -437,13 +454,15 @@ __device__ __forceinline__ uint32_t row_bytes(const RowArgs& r, const Tile& t) {
   }
   return (uint32_t)n * BK;
 }
-template <int CG>
+template <int CG, bool W_IS_A>
 __device__ __forceinline__ void row_load(const RowArgs& r, const CUtensorMap* ma, const CUtensorMap* mb,
                                          const Tile& t, int rank, int kb, unsigned char* sa, unsigned char* sb,
-                                         uint32_t bar) {
+                                         uint32_t bar, Load what) {
   const int half = mma_n<CG>(t.nb) / CG, b0 = r.b_first + t.b0 + rank * half;
-  for (int i = 0; i < t.na; i += r.box_a) tma_load<CG>(sa + i * BK, ma, kb * BK, t.a0 + i, bar);
-  for (int i = 0; i < half; i += r.box_b) tma_load<CG>(sb + i * BK, mb, kb * BK, b0 + i, bar);
+  if (what != (W_IS_A ? kLoadTokens : kLoadW))
+    for (int i = 0; i < t.na; i += r.box_a) tma_load<CG>(sa + i * BK, ma, kb * BK, t.a0 + i, bar);
+  if (what != (W_IS_A ? kLoadW : kLoadTokens))
+    for (int i = 0; i < half; i += r.box_b) tma_load<CG>(sb + i * BK, mb, kb * BK, b0 + i, bar);
 }
 
 }  // namespace gemm_i8

@@ -69,6 +69,7 @@ __device__ __forceinline__ uint32_t pick(const uint32_t (&v)[32], int j) {
 template <int CG_>
 struct ForwardPolicy {
   static constexpr int CG = CG_;
+  static constexpr bool W_EARLY = true;
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
     RowArgs r;
@@ -83,8 +84,8 @@ struct ForwardPolicy {
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 0, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
   static __device__ __forceinline__ void load(const Args& a, const Tile& t, int rank, int kb, unsigned char* sa,
-                                              unsigned char* sb, uint32_t bar) {
-    row_load<CG>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar);
+                                              unsigned char* sb, uint32_t bar, Load what) {
+    row_load<CG, false>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar, what);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
@@ -370,6 +371,7 @@ __global__ void __launch_bounds__(256) transpose_kernel(const int8_t* __restrict
 template <int CG_, bool DS>
 struct DigitPolicy {
   static constexpr int CG = CG_;
+  static constexpr bool W_EARLY = true;
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
     RowArgs r;
@@ -389,8 +391,8 @@ struct DigitPolicy {
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 0, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
   static __device__ __forceinline__ void load(const Args& a, const Tile& t, int rank, int kb, unsigned char* sa,
-                                              unsigned char* sb, uint32_t bar) {
-    row_load<CG>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar);
+                                              unsigned char* sb, uint32_t bar, Load what) {
+    row_load<CG, false>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar, what);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
@@ -515,6 +517,7 @@ struct DigitPolicy {
 template <int CG_>
 struct GradPolicy {
   static constexpr int CG = CG_;
+  static constexpr bool W_EARLY = false;
   struct Args {
     CUtensorMap map_a, map_b;  // transposed W, digits: blocks of 128 bytes
     Common c;
@@ -547,7 +550,7 @@ struct GradPolicy {
   }
   // both operands were laid out as the product reads them: eight 16-byte K columns of all rows are contiguous
   static __device__ __forceinline__ void load(const Args& a, const Tile& t, int rank, int kb, unsigned char* sa,
-                                              unsigned char* sb, uint32_t bar) {
+                                              unsigned char* sb, uint32_t bar, Load) {
     tma_load<CG>(sa, &a.map_a, 0, (int)((size_t)t.a0 * a.Vp / 128) + kb * BM, bar);
     tma_load<CG>(sb, &a.map_b, 0, (int)((t.aux * a.plane + (size_t)(t.b0 + rank * a.tb) * a.Vp) / 128) + kb * a.tb, bar);
   }

@@ -479,10 +479,11 @@ def _on(stream, *tensors):
     library takes plain pointers and launches there)."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}" if t.is_cuda
                              else "expected a CUDA tensor")
-    return _stream(stream)
+    # the raw handle: a torch.cuda.Stream object takes longer to make than a small call
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _new(stream, shape, dtype, device, zero=False):
@@ -501,15 +502,17 @@ def _ws(ws, stream, op, a, b, c, device):
     return _new(stream, max(workspace_size(op, a, b, c), 256), torch.uint8, device, zero=True)
 
 
-def _rows(t, shape, what):
-    """Pointer, type code and row stride of a 2-D tensor of rows (unit stride within a row)."""
-    if t.dtype not in _TYPES:
+def _rows(t, n, d, what):
+    """Pointer, type code and row stride of n rows of d values (unit stride within a row)."""
+    code = _TYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{what} must be float32 or bfloat16, not {t.dtype}")
-    if t.dim() != 2 or tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    if t.dim() != 2 or t.shape != (n, d):
+        raise ValueError(f"{what} must have shape {(n, d)}, not {tuple(t.shape)}")
+    ld, unit = t.stride()
+    if d > 1 and unit != 1:
         raise ValueError(f"{what} must have unit stride within a row")
-    return t.data_ptr(), _TYPES[t.dtype], t.stride(0) if shape[0] > 1 else shape[1]
+    return t.data_ptr(), code, ld if n > 1 else d
 
 
 def _vector(t, n, dtype, what):
@@ -541,8 +544,8 @@ def linear_int8(W, s_row, x, y=None, norm_w=None, out_dtype=torch.float32, ws=No
         dbg = DebugT(_vector(debug.get("acc"), M * V, torch.int32, "acc"), None,
                      _vector(debug.get("xq"), M * d, torch.int8, "xq"),
                      _vector(debug.get("xscale"), M, torch.float32, "xscale"))
-    px, tx, lx = _rows(x, (M, d), "x")
-    py, ty, ly = _rows(y, (M, V), "y")
+    px, tx, lx = _rows(x, M, d, "x")
+    py, ty, ly = _rows(y, M, V, "y")
     _check("dfssm_linear_int8", lib().dfssm_linear_int8(
         W.data_ptr(), _vector(s_row, V, torch.float32, "s_row"), V, d, px, tx, lx, M,
         _vector(norm_w, d, torch.float32, "norm_w"), py, ty, ly, ws.data_ptr(), ws.numel(),
@@ -559,7 +562,7 @@ def embed_tokens(W, s_row, tokens, h=None, dtype=torch.float32, ws=None, stream=
     if h is None:
         h = _new(stream, (n, d), dtype, W.device)
     ws = _ws(ws, stream, OP_EMBED_TOKENS, 0, 0, 0, W.device)
-    ph, th, lh = _rows(h, (n, d), "h")
+    ph, th, lh = _rows(h, n, d, "h")
     _check("dfssm_embed_tokens", lib().dfssm_embed_tokens(
         W.data_ptr(), _vector(s_row, V, torch.float32, "s_row"), V, d, _vector(tokens, n, torch.int32, "tokens"),
         n, ph, th, lh, ws.data_ptr(), ws.numel(), st))
@@ -582,7 +585,7 @@ def embed_tokens_backward(W, tokens, dh, dE=None, ds_row=None, accumulate=False,
         if ds_row is None:
             ds_row = _new(stream, (V,), torch.float32, W.device)
     ws = _ws(ws, stream, OP_EMBED_BACKWARD, n, d, V, W.device)
-    pd, td, ld = _rows(dh, (n, d), "dh")
+    pd, td, ld = _rows(dh, n, d, "dh")
     _check("dfssm_embed_tokens_backward", lib().dfssm_embed_tokens_backward(
         W.data_ptr(), V, d, _vector(tokens, n, torch.int32, "tokens"), n, pd, td, ld,
         _vector(dE, V * d, torch.float32, "dE"), _vector(ds_row, V, torch.float32, "ds_row"), int(accumulate),
@@ -601,7 +604,7 @@ def head_loss(W, s_row, x, labels, norm_w=None, loss=None, stats=None, ws=None, 
     if stats is None:
         stats = _new(stream, (3, M), torch.float32, x.device)
     ws = _ws(ws, stream, OP_HEAD_LOSS, M, d, V, x.device)
-    px, tx, lx = _rows(x, (M, d), "x")
+    px, tx, lx = _rows(x, M, d, "x")
     _check("dfssm_head_loss", lib().dfssm_head_loss(
         W.data_ptr(), _vector(s_row, V, torch.float32, "s_row"), V, d, px, tx, lx, M,
         _vector(norm_w, d, torch.float32, "norm_w"), _vector(labels, M, torch.int32, "labels"),
@@ -625,8 +628,8 @@ def head_loss_backward(W, s_row, x, labels, stats, dloss, norm_w=None, dx=None, 
     if dnorm_w is None and norm_w is not None:
         dnorm_w = _new(stream, (d,), torch.float32, x.device)
     ws = _ws(ws, stream, OP_HEAD_LOSS_BACKWARD, M, d, V, x.device)
-    px, tx, lx = _rows(x, (M, d), "x")
-    pd, td, ld = _rows(dx, (M, d), "dx")
+    px, tx, lx = _rows(x, M, d, "x")
+    pd, td, ld = _rows(dx, M, d, "dx")
     if td != tx:
         raise ValueError("dx must have x's type")
     _check("dfssm_head_loss_backward", lib().dfssm_head_loss_backward(

@@ -119,12 +119,12 @@ def test_binding_checks_shapes_and_types():
     with pytest.raises(ValueError):
         D._matrix(torch.zeros(4, 64, dtype=torch.int8)[:, ::2])
     x = torch.zeros(4, 32)
-    assert D._rows(x, (4, 32), "x")[1:] == (0, 32)
-    assert D._rows(torch.zeros(4, 40, dtype=torch.bfloat16)[:, :32], (4, 32), "x")[1:] == (1, 40)
-    assert D._rows(torch.zeros(1, 32).expand(1, 32), (1, 32), "x")[2] == 32
+    assert D._rows(x, 4, 32, "x")[1:] == (0, 32)
+    assert D._rows(torch.zeros(4, 40, dtype=torch.bfloat16)[:, :32], 4, 32, "x")[1:] == (1, 40)
+    assert D._rows(torch.zeros(1, 32).expand(1, 32), 1, 32, "x")[2] == 32
     for bad in (x.double(), x.t(), x[:2], torch.zeros(4, 64)[:, ::2]):
         with pytest.raises(ValueError):
-            D._rows(bad, (4, 32), "x")
+            D._rows(bad, 4, 32, "x")
     assert D._vector(None, 3, torch.float32, "v") is None
     for bad in (torch.zeros(4), torch.zeros(3, dtype=torch.int32), torch.zeros(6)[::2]):
         with pytest.raises(ValueError):
@@ -139,6 +139,11 @@ def test_binding_refuses_another_device(monkeypatch):
     class Fake:
         def __init__(self, i):
             self.device, self.is_cuda = torch.device("cuda", i), True
+
+        def get_device(self):
+            return self.device.index
+
+
     assert D._on(7, Fake(1), None) == 7
     with pytest.raises(ValueError):
         D._on(7, Fake(1), Fake(0))
