@@ -140,7 +140,13 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-enum Load { kLoadBoth = 0, kLoadW = 1, kLoadTokens = 2 };
+// One lane's TMA copy of a K step kb: box at (x + kb dx, y + kb dy) to the stage's byte `off`.
+struct Copy {
+  const CUtensorMap* map;  // NULL: this lane has none
+  int x, y, dx, dy;
+  uint32_t off;
+  bool w;                  // of the matrix W, which does not change
+};
 
 // What every policy's arguments start with.
 struct Common {
@@ -182,6 +188,31 @@ __device__ __forceinline__ Tile own_tile(Tile t, int rank) {
   return t;
 }
 
+// With PDL the kernel may start while the one that writes the tokens' codes still runs: the first round of W is
+// requested without waiting for it.  Returns the number of K steps.  (Whole warp.)
+template <class P>
+__device__ __forceinline__ int request_w(const typename P::Args& ar, unsigned char* smem, uint64_t* full, int rank,
+                                         int lane) {
+  if (!P::W_EARLY) return 0;
+  constexpr int CG = P::CG;
+  const int sbytes = stage_bytes(ar.c);
+  int n = 0;
+  Tile pt;
+  for (int j = 0; n < ar.c.stages && P::tile(ar, j, pt); ++j) {
+    const Tile t = own_tile<CG>(pt, rank);
+    const uint32_t bytes = P::bytes(ar, pt);
+    const Copy cp = P::copy(ar, t, rank, lane);
+    for (int kb = t.kb0; kb < t.kb1 && n < ar.c.stages; ++kb, ++n) {
+      if (rank == 0 && lane == 0) mbar_expect_tx(&full[n], bytes);
+      __syncwarp();
+      if (cp.map && cp.w)
+        tma_load<CG>(smem + (size_t)n * sbytes + cp.off, cp.map, cp.x + kb * cp.dx, cp.y + kb * cp.dy,
+                     leader_bar<CG>(&full[n]));
+    }
+  }
+  return n;
+}
+
 template <class P>
 __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_constant__ typename P::Args ar) {
   constexpr int CG = P::CG;
@@ -200,6 +231,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
   static_assert((2 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)(blockIdx.x & 1u) : 0;  // within the pair (a cluster of two consecutive CTAs)
+  int early = 0;  // K steps whose W was requested ahead
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
@@ -213,6 +245,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
     }
     mbar_init(mma_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    __syncwarp();
+    if (CG == 1) early = request_w<P>(ar, smem, full, 0, lane);  // while tensor memory is allocated
   }
   if (warp == 1) {
     if (CG == 1) {
@@ -234,45 +270,37 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
   const uint32_t tmem_base = *tmem_holder;
   if (threadIdx.x == 0) pdl_launch_dependents();
 
-  if (warp == 0 && lane == 0) {
-    // ---- producer: each tile's K steps through the stage ring
-    // With PDL the kernel may start while the one that writes the tokens' codes still runs: the first round of W
-    // (immutable) is requested before waiting for it.
-    int early = 0;
-    Tile pt;
-    if (P::W_EARLY) {
-      for (int j = 0; early < stages && P::tile(ar, j, pt); ++j) {
-        const Tile t = own_tile<CG>(pt, rank);
-        const uint32_t bytes = P::bytes(ar, pt);  // of the whole tile's K step, both CTAs'
-        for (int kb = t.kb0; kb < t.kb1 && early < stages; ++kb, ++early) {
-          unsigned char* st = smem + (size_t)early * sbytes;
-          if (rank == 0) mbar_expect_tx(&full[early], bytes);
-          P::load(ar, t, rank, kb, st, st + A_BYTES, leader_bar<CG>(&full[early]), kLoadW);
-        }
-      }
-    }
+  if (warp == 0) {
+    // ---- producer: each tile's K steps through the stage ring, one copy per lane
+    if (CG == 2) early = request_w<P>(ar, smem, full, rank, lane);
     pdl_wait();
     Ring ring(stages);
     bool ok = true;
+    Tile pt;
     for (int j = 0; ok && P::tile(ar, j, pt); ++j) {
       const Tile t = own_tile<CG>(pt, rank);
-      const uint32_t bytes = P::bytes(ar, pt);
+      const uint32_t bytes = P::bytes(ar, pt);  // of the whole tile's K step, both CTAs'
+      const Copy cp = P::copy(ar, t, rank, lane);
       for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next()) {
         const int s = ring.s;
-        if (ring.round > 0 && !mbar_wait(&empty[s], ring.phase ^ 1u, &abort_flag)) {
+        if (ring.round > 0 && !mbar_wait(&empty[s], ring.phase ^ 1u, &abort_flag)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
           abort_flag = 1;
-          ok = false;
           break;
         }
-        unsigned char* st = smem + (size_t)s * sbytes;
-        const bool late = P::W_EARLY && ring.round == 0;  // its W is under way
-        if (rank == 0 && !late) mbar_expect_tx(&full[s], bytes);
-        P::load(ar, t, rank, kb, st, st + A_BYTES, leader_bar<CG>(&full[s]), late ? kLoadTokens : kLoadBoth);
+        const bool late = ring.round == 0 && s < early;  // its W is under way
+        if (rank == 0 && lane == 0 && !late) mbar_expect_tx(&full[s], bytes);
+        __syncwarp();
+        if (cp.map && !(late && cp.w))
+          tma_load<CG>(smem + (size_t)s * sbytes + cp.off, cp.map, cp.x + kb * cp.dx, cp.y + kb * cp.dy,
+                       leader_bar<CG>(&full[s]));
       }
     }
     // the last copies land before this CTA may exit (those of a pair's second CTA are counted by the first, which
     // the cluster barrier at the end waits for; after an abort they get a millisecond)
-    if (rank == 0) {
+    __syncwarp();
+    if (lane == 0 && rank == 0) {
       // the stage's last copy has the phase of the ring's current round, or of the one before
       for (int i = 0; i < stages; ++i) {
         if (i < ring.s) mbar_wait_drain(&full[i], ring.phase);
@@ -454,15 +482,29 @@ __device__ __forceinline__ uint32_t row_bytes(const RowArgs& r, const Tile& t) {
   }
   return (uint32_t)n * BK;
 }
+// Lanes 0.. copy A's boxes, lanes 16.. B's (at most eight each).
 template <int CG, bool W_IS_A>
-__device__ __forceinline__ void row_load(const RowArgs& r, const CUtensorMap* ma, const CUtensorMap* mb,
-                                         const Tile& t, int rank, int kb, unsigned char* sa, unsigned char* sb,
-                                         uint32_t bar, Load what) {
-  const int half = mma_n<CG>(t.nb) / CG, b0 = r.b_first + t.b0 + rank * half;
-  if (what != (W_IS_A ? kLoadTokens : kLoadW))
-    for (int i = 0; i < t.na; i += r.box_a) tma_load<CG>(sa + i * BK, ma, kb * BK, t.a0 + i, bar);
-  if (what != (W_IS_A ? kLoadW : kLoadTokens))
-    for (int i = 0; i < half; i += r.box_b) tma_load<CG>(sb + i * BK, mb, kb * BK, b0 + i, bar);
+__device__ __forceinline__ Copy row_copy(const RowArgs& r, const CUtensorMap* ma, const CUtensorMap* mb, const Tile& t,
+                                         int rank, int lane) {
+  const int half = mma_n<CG>(t.nb) / CG;
+  Copy c;
+  c.map = nullptr;
+  c.x = 0;
+  c.dx = BK;
+  c.dy = 0;
+  c.w = (lane < 16) == W_IS_A;
+  if (lane < 16) {
+    const int i = lane * r.box_a;
+    if (i < t.na) c.map = ma;
+    c.y = t.a0 + i;
+    c.off = (uint32_t)(i * BK);
+  } else {
+    const int i = (lane - 16) * r.box_b;
+    if (i < half) c.map = mb;
+    c.y = r.b_first + t.b0 + rank * half + i;
+    c.off = (uint32_t)(A_BYTES + i * BK);
+  }
+  return c;
 }
 
 }  // namespace gemm_i8

@@ -83,9 +83,8 @@ struct ForwardPolicy {
   };
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 0, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
-  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int rank, int kb, unsigned char* sa,
-                                              unsigned char* sb, uint32_t bar, Load what) {
-    row_load<CG, false>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar, what);
+  static __device__ __forceinline__ Copy copy(const Args& a, const Tile& t, int rank, int lane) {
+    return row_copy<CG, false>(a.r, &a.map_a, &a.map_b, t, rank, lane);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
@@ -390,9 +389,8 @@ struct DigitPolicy {
   };
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 0, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
-  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int rank, int kb, unsigned char* sa,
-                                              unsigned char* sb, uint32_t bar, Load what) {
-    row_load<CG, false>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar, what);
+  static __device__ __forceinline__ Copy copy(const Args& a, const Tile& t, int rank, int lane) {
+    return row_copy<CG, false>(a.r, &a.map_a, &a.map_b, t, rank, lane);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
@@ -549,10 +547,21 @@ struct GradPolicy {
     return CG * (A_BYTES + (uint32_t)a.tb * BK);
   }
   // both operands were laid out as the product reads them: eight 16-byte K columns of all rows are contiguous
-  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int rank, int kb, unsigned char* sa,
-                                              unsigned char* sb, uint32_t bar, Load) {
-    tma_load<CG>(sa, &a.map_a, 0, (int)((size_t)t.a0 * a.Vp / 128) + kb * BM, bar);
-    tma_load<CG>(sb, &a.map_b, 0, (int)((t.aux * a.plane + (size_t)(t.b0 + rank * a.tb) * a.Vp) / 128) + kb * a.tb, bar);
+  static __device__ __forceinline__ Copy copy(const Args& a, const Tile& t, int rank, int lane) {
+    Copy c;
+    c.map = lane == 0 ? &a.map_a : lane == 16 ? &a.map_b : nullptr;
+    c.x = c.dx = 0;
+    c.w = false;
+    if (lane < 16) {
+      c.y = (int)((size_t)t.a0 * a.Vp / 128);
+      c.dy = BM;
+      c.off = 0u;
+    } else {
+      c.y = (int)((t.aux * a.plane + (size_t)(t.b0 + rank * a.tb) * a.Vp) / 128);
+      c.dy = a.tb;
+      c.off = (uint32_t)A_BYTES;
+    }
+    return c;
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_plain(addr, BM * 16); }
   static __device__ __forceinline__ uint64_t bdesc(const Args& a, uint32_t addr) {

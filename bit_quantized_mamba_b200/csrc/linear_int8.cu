@@ -34,9 +34,8 @@ struct LinearPolicy {
   };
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 1, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
-  static __device__ __forceinline__ void load(const Args& a, const Tile& t, int rank, int kb, unsigned char* sa,
-                                              unsigned char* sb, uint32_t bar, Load what) {
-    row_load<CG, true>(a.r, &a.map_a, &a.map_b, t, rank, kb, sa, sb, bar, what);
+  static __device__ __forceinline__ Copy copy(const Args& a, const Tile& t, int rank, int lane) {
+    return row_copy<CG, true>(a.r, &a.map_a, &a.map_b, t, rank, lane);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
