@@ -412,6 +412,21 @@ cudaError_t launch(const typename P::Args& a, int groups, int epi_smem, cudaStre
 template <class P>
 int max_groups() { return num_sms() / P::CG; }
 
+// Columns of a tile for `cols` columns times `rows` tile rows on `groups` groups: of the widths 128 .. 256 the one whose
+// fullest group has the fewest columns to do (with 32 for each tile's start and end), the widest of equals.
+inline int even_tile(int rows, int cols, int groups) {
+  int best = BN_MAX;
+  long long least = -1;
+  for (int w = BN_MAX; w >= 128; w -= 32) {
+    const long long tiles = (long long)rows * ((cols + w - 1) / w), cost = (tiles + groups - 1) / groups * (w + 32);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = w;
+    }
+  }
+  return best;
+}
+
 // ------------------------------------------------------------------ row-major operands through TMA
 // Both operands are row-major int8 matrices with K contiguous, loaded as 128-byte-swizzled boxes of 128 bytes
 // of K (bytes past a row's end and rows past the last read as zero).  The rows of one operand are the

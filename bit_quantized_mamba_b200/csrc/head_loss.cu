@@ -179,9 +179,9 @@ struct ForwardPolicy {
   };
 };
 
-// Joins the partial (max, sum) of a token and forms its loss.  32 tokens per CTA, 16 slices of slots; the second
+// Joins the partial (max, sum) of a token and forms its loss.  32 tokens per CTA, 32 slices of slots; the second
 // pass over a slice comes from L1/L2.
-constexpr int LF_SLICES = 16;
+constexpr int LF_SLICES = 32;
 __global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float2* __restrict__ part, int slots, int M,
                                                                      int V, const int32_t* __restrict__ labels,
                                                                      float* __restrict__ stats,
@@ -739,6 +739,7 @@ __global__ void __launch_bounds__(256) dnorm_finish_kernel(const float* __restri
   const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
   double s = 0.0;
   if (i < d)
+#pragma unroll 8
     for (int p = sl; p < parts; p += 8) s += (double)npart[(size_t)p * d + i];
   red[sl][lane] = s;
   __syncthreads();
@@ -755,7 +756,7 @@ struct ForwardWs {
   size_t q, s, part, total;
 };
 int forward_slots(int V) {
-  const int grid = ceil_div(V, BN_MAX), range = ceil_div(V, 32) < kMaxRangeCtas ? ceil_div(V, 32) : kMaxRangeCtas;
+  const int grid = ceil_div(V, BN_MAX / 2), range = ceil_div(V, 32) < kMaxRangeCtas ? ceil_div(V, 32) : kMaxRangeCtas;
   return 2 * (grid > range ? grid : range);
 }
 ForwardWs forward_ws(int M, int d, int V) {
@@ -776,7 +777,8 @@ struct Layout {
 Layout layout(int M, int d) {
   Layout l;
   l.cg = M <= BM ? 1 : 2;
-  l.tb = M <= BM ? (M + 15) & ~15 : BM;
+  const int tiles = ceil_div(M, BM * l.cg);  // blocks of equal size, a multiple of 16
+  l.tb = (ceil_div(M, tiles * l.cg) + 15) & ~15;
   l.mp = (size_t)ceil_div(M, l.tb * l.cg) * l.tb * l.cg;
   l.dp = (size_t)ceil_div(d, BM * l.cg) * BM * l.cg;
   return l;
@@ -853,13 +855,13 @@ int row_args(typename P::Args& a, int M, int rows, int first, int d, const int8_
   a.r.rows_a = M;
   a.r.rows_b = rows;
   a.r.b_first = first;
-  a.r.tile_b = BN_MAX;
   a.r.kblocks = ceil_div(d, BK);
   a.r.mode = M <= BM * CG ? kRangeB : kGrid;
+  a.r.tile_b = a.r.mode == kRangeB ? BN_MAX : even_tile(ceil_div(M, BM * CG), rows, max_groups<P>());
   a.r.box_a = BM;
-  a.r.box_b = a.r.mode == kRangeB ? 32 / CG : BN_MAX / CG;
-  a.c.b_tile = BN_MAX / CG;
-  a.c.stages = ring_stages(BN_MAX / CG, P::EPI_SMEM);
+  a.r.box_b = a.r.mode == kRangeB ? 32 / CG : a.r.tile_b / CG;
+  a.c.b_tile = a.r.tile_b / CG;
+  a.c.stages = ring_stages(a.c.b_tile, P::EPI_SMEM);
   a.c.err = err;
   if (!encode_u8_map_sw128(&a.map_a, q, M, d, a.r.box_a) || !encode_u8_map_sw128(&a.map_b, W, V, d, a.r.box_b))
     return DFSSM_EUNSUPPORTED;
@@ -868,7 +870,7 @@ int row_args(typename P::Args& a, int M, int rows, int first, int d, const int8_
 template <class P>
 int row_groups(const RowArgs& r) {
   const long long most = max_groups<P>() < kMaxRangeCtas ? max_groups<P>() : kMaxRangeCtas;
-  const long long units = r.mode == kGrid ? (long long)ceil_div(r.rows_a, BM * P::CG) * ceil_div(r.rows_b, BN_MAX)
+  const long long units = r.mode == kGrid ? (long long)ceil_div(r.rows_a, BM * P::CG) * ceil_div(r.rows_b, r.tile_b)
                                           : ceil_div(r.rows_b, 32);
   return (int)(units < most ? units : most);
 }
@@ -889,7 +891,7 @@ int forward(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, 
   a.V = V;
   const int groups = row_groups<P>(a.r);
   cudaError_t e = launch<P>(a, groups, P::EPI_SMEM, st);
-  const int slots = 2 * (a.r.mode == kGrid ? ceil_div(V, BN_MAX) : groups);
+  const int slots = 2 * (a.r.mode == kGrid ? ceil_div(V, a.r.tile_b) : groups);
   if (e == cudaSuccess)
     e = launch_pdl(loss_finish_kernel, dim3(ceil_div(M, 32)), dim3(32 * LF_SLICES), 0, st, (const float2*)part, slots, M, V,
                    labels, stats, loss, err);

@@ -5,8 +5,8 @@
 //   2. the tcgen05 int8 product (gemm_i8.cuh) with the rows of W on the tensor memory's lanes and the tokens on
 //      its columns: a warp's store of one token covers 32 consecutive outputs, and few tokens make a narrow
 //      product (16 columns for one token), so that the stream of W alone bounds it.
-// The outputs are the head's bit for bit: the accumulators are exact, and the epilogue evaluates the
-// definition in fp64 and rounds once to fp32 (bf16 outputs round that once more).
+// The outputs are the head's bit for bit: the accumulators are exact, and the epilogue gives the definition's
+// value, an fp64 product rounded once to fp32 (bf16 outputs round that once more).
 
 #include "gemm_i8.cuh"
 
@@ -16,6 +16,23 @@ namespace dfssm {
 namespace {
 
 using namespace gemm_i8;
+
+// fl32(acc s w) of the definition, its fp64 product rounded once, in fp32: with x = acc exact (|acc| <= 2^24), p = fl(x s)
+// and e = x s - p, the product is y + r, y = fl(p w), r = (p w - y) + e w, where r alone is rounded, by less than
+// 2^-47 |y|.  Where y + r rounds the same with r moved by 2^-46 |y| either way, that is the definition's value;
+// otherwise (about one in 2^20) `sure` is cleared and the caller takes fp64.  (In fp64 throughout, the fp64 and
+// conversion units bound the product: 2048 x 50288 x 2048 took 215 us of 133 us without an epilogue.)
+// s and w in [2^-40, 2^40] (ordinary) keep every term normal; s = 0 gives acc = 0.
+__device__ __forceinline__ bool ordinary(float s) { return fabsf(s) >= 0x1p-40f && fabsf(s) <= 0x1p40f; }
+__device__ __forceinline__ float scaled(uint32_t acc, float s, float w, bool& sure) {
+  const float x = (float)(int)acc;
+  const float p = fmul(x, s), e = fmaf(x, s, -p);
+  const float y = fmul(p, w), r = fmaf(e, w, fmaf(p, w, -y));
+  const float d = fabsf(y) * 0x1p-46f;
+  const float lo = fadd(y, r - d), hi = fadd(y, r + d);
+  sure = sure && lo == hi && acc + (1u << 24) <= (2u << 24);
+  return lo;
+}
 
 template <typename Y, int CG_>
 struct LinearPolicy {
@@ -41,48 +58,67 @@ struct LinearPolicy {
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t a_step() { return UMMA_K >> 4; }
   static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
-  static constexpr int EPI_SMEM = EPI_WARPS * EPI_COLS * 8;
+  static constexpr int EPI_SMEM = EPI_WARPS * EPI_COLS * 4;
   struct Epilogue {
     int half, lane, r;  // r: lane of the tile
-    double* s;          // scales of this warp's columns (chunks of 16: half, half + 2, ..)
-    double sw;
+    float* s;           // scales of this warp's columns (chunks of 16: half, half + 2, ..)
+    float sw;
+    bool plain;         // the warp's scales are of ordinary size
     __device__ __forceinline__ Epilogue(const Args&, unsigned char* sm, int q, int half_, int lane_)
         : half(half_), lane(lane_), r(q * 32 + lane_),
-          s(reinterpret_cast<double*>(sm) + (half_ * 4 + q) * EPI_COLS) {}
+          s(reinterpret_cast<float*>(sm) + (half_ * 4 + q) * EPI_COLS) {}
     __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
-      sw = r < t.na ? (double)__ldg(a.s_row + t.a0 + r) : 0.0;
+      sw = r < t.na ? __ldg(a.s_row + t.a0 + r) : 1.0f;
+      bool ok = ordinary(sw);
 #pragma unroll
       for (int k = 0; k < EPI_COLS / 32; ++k) {
         const int i = k * 32 + lane, c = (i >> 4) * 32 + half * 16 + (i & 15);
-        s[i] = c < t.nb ? a.s_tok[t.b0 + c] : 0.0;
+        const float st = c < t.nb ? (float)a.s_tok[t.b0 + c] : 1.0f;
+        s[i] = st;
+        ok = ok && (ordinary(st) || st == 0.0f);
       }
-      __syncwarp();
+      plain = __all_sync(0xffffffffu, ok);
     }
     __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
       const int row = t.a0 + r;
       const bool rv = r < t.na;
       uint32_t v[16];
-      const double* st = s;
+      const float* st = s;
       Y* yp = a.y + (int64_t)(t.b0 + half * 16) * a.ldy + row;
       if (half * 16 < t.nb) tmem_ld16(taddr + (uint32_t)(half * 16), v);
 #pragma unroll 1
       for (int c = half * 16; c < t.nb; c += 32, st += 16) {
         tmem_wait(v);
         const int n = min(16, t.nb - c);
-        double x[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = int_to_f64((int)v[j]);
         if (a.acc) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             if (rv && j < n) a.acc[(int64_t)(t.b0 + c + j) * a.V + row] = (int)v[j];
         }
-        if (c + 32 < t.nb) tmem_ld16(taddr + (uint32_t)c + 32, v);  // the next chunk, while this one is stored
+        float out[16];
+        bool sure = plain;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float out = __double2float_rn(dmul(dmul(x[j], st[j]), sw));
-          if (rv && j < n) *yp = (Y)out;
-          yp += a.ldy;
+        for (int j = 0; j < 16; j += 4) {
+          const float4 s4 = *reinterpret_cast<const float4*>(st + j);
+          out[j] = scaled(v[j], s4.x, sw, sure);
+          out[j + 1] = scaled(v[j + 1], s4.y, sw, sure);
+          out[j + 2] = scaled(v[j + 2], s4.z, sw, sure);
+          out[j + 3] = scaled(v[j + 3], s4.w, sw, sure);
+        }
+        if (!sure) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            out[j] = __double2float_rn(dmul(dmul(int_to_f64((int)v[j]), (double)st[j]), (double)sw));
+        }
+        if (c + 32 < t.nb) tmem_ld16(taddr + (uint32_t)c + 32, v);  // the next chunk, while this one is stored
+        if (n == 16) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j, yp += a.ldy)
+            if (rv) *yp = (Y)out[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j, yp += a.ldy)
+            if (rv && j < n) *yp = (Y)out[j];
         }
         yp += 16 * a.ldy;
       }
@@ -106,9 +142,9 @@ int launch_linear(const int8_t* W, const float* s_row, int V, int d, const int8_
   // fastest.
   const bool range = M <= BN_MAX;
   a.r.mode = range ? kRangeA : kGrid;
-  a.r.tile_b = BN_MAX;
+  a.r.tile_b = range ? BN_MAX : even_tile((V + BM * CG - 1) / (BM * CG), M, max_groups<P>());
   a.r.box_a = range ? 32 : BM;
-  const int bt = range ? (M + 16 * CG - 1) / (16 * CG) * 16 : BN_MAX / CG;  // a CTA's columns
+  const int bt = range ? (M + 16 * CG - 1) / (16 * CG) * 16 : a.r.tile_b / CG;  // a CTA's columns
   a.r.box_b = bt;
   a.c.b_tile = bt;
   a.c.stages = ring_stages(bt, P::EPI_SMEM);
@@ -122,7 +158,7 @@ int launch_linear(const int8_t* W, const float* s_row, int V, int d, const int8_
   if (!encode_u8_map_sw128(&a.map_a, W, V, d, a.r.box_a) || !encode_u8_map_sw128(&a.map_b, q, M, d, bt))
     return DFSSM_EUNSUPPORTED;
   const long long units = range ? (V + 31) / 32
-                                : (long long)((V + BM * CG - 1) / (BM * CG)) * ((M + BN_MAX - 1) / BN_MAX);
+                                : (long long)((V + BM * CG - 1) / (BM * CG)) * ((M + a.r.tile_b - 1) / a.r.tile_b);
   const int most = max_groups<P>();
   const cudaError_t e = launch<P>(a, (int)(units < most ? units : most), P::EPI_SMEM, st);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
