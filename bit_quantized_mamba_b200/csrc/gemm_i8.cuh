@@ -1,5 +1,5 @@
 // Int8 matrix product on the 5th-generation tensor cores, shared by the many-token operators: a
-// persistent, warp-specialised main loop (TMA producer, MMA issuer, eight epilogue warps) around a policy P
+// persistent, warp-specialised main loop (TMA producer, MMA issuer, epilogue warps) around a policy P
 // that says which tiles a CTA works on, how a K step is loaded and what becomes of the accumulators.
 //
 //   D[lanes][n columns] (int32, exact) = sum over K of A[lane][k] B[column][k]   (int8, both K-major)
@@ -28,13 +28,15 @@ constexpr int BN_MAX = 256;  // columns of a tile at most (the MMA's N)
 constexpr int BK = 128;      // K bytes of a stage
 constexpr int UMMA_K = 32;   // K bytes of one kind::i8 MMA
 constexpr int A_BYTES = BM * BK;
-constexpr int EPI_WARPS = 8;
-constexpr int THREADS = (2 + EPI_WARPS) * 32;
-constexpr int EPI_COLS = BN_MAX / 2;  // columns of an epilogue warp: chunks 0, 2, 4, .. or 1, 3, 5, .. of a tile
 constexpr int MAX_STAGES = 12;
 constexpr int SMEM_LIMIT = 232448;  // 227 KB: the shared memory a CTA may have, all of it dynamic here
 constexpr int BAR_BYTES = 256;
 constexpr int TMEM_COLS = 2 * BN_MAX;
+
+// Epilogue warps P::EPI_WARPS (8 or 16): `parts` of them share a quadrant of 32 lanes, part p taking the chunks p,
+// p + parts, .. of a tile's columns.
+template <class P>
+constexpr int threads() { return (2 + P::EPI_WARPS) * 32; }
 
 // One output tile: lanes a0 .. a0 + na, columns b0 .. b0 + nb, K steps kb0 .. kb1.  Policies give the whole
 // tile (128 CG lanes); loads and epilogues see the CTA's own 128 lanes of it.
@@ -214,7 +216,7 @@ __device__ __forceinline__ int request_w(const typename P::Args& ar, unsigned ch
 }
 
 template <class P>
-__global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_constant__ typename P::Args ar) {
+__global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_constant__ typename P::Args ar) {
   constexpr int CG = P::CG;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // aligned by an offset from the array itself, so that every access stays a shared-memory access
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], EPI_WARPS * CG);
+      mbar_init(&acc_empty[b], P::EPI_WARPS * CG);
     }
     mbar_init(mma_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
       mbar_wait_drain(mma_done, 0);
     }
   } else if (warp >= 2) {
-    // ---- epilogue: warp drains TMEM lanes [32 (warp % 4), +32); the two warps of a quadrant share its columns
+    // ---- epilogue: warp drains TMEM lanes [32 (warp % 4), +32)
     pdl_wait();
     typename P::Epilogue epi(ar, epi_smem, warp & 3, (warp - 2) >> 2, lane);
     int local = 0;
@@ -378,8 +380,9 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_i8_kernel(const __grid_consta
       // this warp's reads of the accumulator are complete
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
+      // (relaxed: the loads are complete, and a release would wait for this tile's stores as well)
       if (lane == 0)
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                          leader_bar<CG>(&acc_empty[buf]))
                      : "memory");
     }
@@ -406,7 +409,7 @@ cudaError_t launch(const typename P::Args& a, int groups, int epi_smem, cudaStre
   const auto k = gemm_i8_kernel<P>;
   const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(k), SMEM_LIMIT);
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(P::CG, k, dim3(groups * P::CG), dim3(THREADS), smem_bytes(a.c, epi_smem), st, a);
+  return launch_pdl_cluster(P::CG, k, dim3(groups * P::CG), dim3(threads<P>()), smem_bytes(a.c, epi_smem), st, a);
 }
 // Groups that run at a time: one CTA per SM.
 template <class P>

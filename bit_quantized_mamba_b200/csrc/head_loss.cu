@@ -70,6 +70,7 @@ template <int CG_>
 struct ForwardPolicy {
   static constexpr int CG = CG_;
   static constexpr bool W_EARLY = true;
+  static constexpr int EPI_WARPS = 8, EPI_COLS = BN_MAX / 2;  // columns of an epilogue warp
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
     RowArgs r;
@@ -371,6 +372,7 @@ template <int CG_, bool DS>
 struct DigitPolicy {
   static constexpr int CG = CG_;
   static constexpr bool W_EARLY = true;
+  static constexpr int EPI_WARPS = 8, EPI_COLS = BN_MAX / 2;  // columns of an epilogue warp
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
     RowArgs r;
@@ -516,6 +518,7 @@ template <int CG_>
 struct GradPolicy {
   static constexpr int CG = CG_;
   static constexpr bool W_EARLY = false;
+  static constexpr int EPI_WARPS = 8;
   struct Args {
     CUtensorMap map_a, map_b;  // transposed W, digits: blocks of 128 bytes
     Common c;

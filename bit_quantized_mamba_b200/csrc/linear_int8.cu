@@ -38,6 +38,7 @@ template <typename Y, int CG_>
 struct LinearPolicy {
   static constexpr int CG = CG_;
   static constexpr bool W_EARLY = true;
+  static constexpr int EPI_WARPS = 16, PARTS = EPI_WARPS / 4, EPI_COLS = BN_MAX / PARTS;  // columns of a warp
   struct Args {
     CUtensorMap map_a, map_b;  // W, codes
     RowArgs r;
@@ -60,19 +61,19 @@ struct LinearPolicy {
   static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
   static constexpr int EPI_SMEM = EPI_WARPS * EPI_COLS * 4;
   struct Epilogue {
-    int half, lane, r;  // r: lane of the tile
-    float* s;           // scales of this warp's columns (chunks of 16: half, half + 2, ..)
+    int part, lane, r;  // r: lane of the tile
+    float* s;           // scales of this warp's columns (chunks of 16: part, part + PARTS, ..)
     float sw;
     bool plain;         // the warp's scales are of ordinary size
-    __device__ __forceinline__ Epilogue(const Args&, unsigned char* sm, int q, int half_, int lane_)
-        : half(half_), lane(lane_), r(q * 32 + lane_),
-          s(reinterpret_cast<float*>(sm) + (half_ * 4 + q) * EPI_COLS) {}
+    __device__ __forceinline__ Epilogue(const Args&, unsigned char* sm, int q, int part_, int lane_)
+        : part(part_), lane(lane_), r(q * 32 + lane_),
+          s(reinterpret_cast<float*>(sm) + (part_ * 4 + q) * EPI_COLS) {}
     __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
       sw = r < t.na ? __ldg(a.s_row + t.a0 + r) : 1.0f;
       bool ok = ordinary(sw);
 #pragma unroll
       for (int k = 0; k < EPI_COLS / 32; ++k) {
-        const int i = k * 32 + lane, c = (i >> 4) * 32 + half * 16 + (i & 15);
+        const int i = k * 32 + lane, c = ((i >> 4) * PARTS + part) * 16 + (i & 15);
         const float st = c < t.nb ? (float)a.s_tok[t.b0 + c] : 1.0f;
         s[i] = st;
         ok = ok && (ordinary(st) || st == 0.0f);
@@ -84,10 +85,10 @@ struct LinearPolicy {
       const bool rv = r < t.na;
       uint32_t v[16];
       const float* st = s;
-      Y* yp = a.y + (int64_t)(t.b0 + half * 16) * a.ldy + row;
-      if (half * 16 < t.nb) tmem_ld16(taddr + (uint32_t)(half * 16), v);
+      Y* yp = a.y + (int64_t)(t.b0 + part * 16) * a.ldy + row;
+      if (part * 16 < t.nb) tmem_ld16(taddr + (uint32_t)(part * 16), v);
 #pragma unroll 1
-      for (int c = half * 16; c < t.nb; c += 32, st += 16) {
+      for (int c = part * 16; c < t.nb; c += 16 * PARTS, st += 16) {
         tmem_wait(v);
         const int n = min(16, t.nb - c);
         if (a.acc) {
@@ -110,7 +111,7 @@ struct LinearPolicy {
           for (int j = 0; j < 16; ++j)
             out[j] = __double2float_rn(dmul(dmul(int_to_f64((int)v[j]), (double)st[j]), (double)sw));
         }
-        if (c + 32 < t.nb) tmem_ld16(taddr + (uint32_t)c + 32, v);  // the next chunk, while this one is stored
+        if (c + 16 * PARTS < t.nb) tmem_ld16(taddr + (uint32_t)(c + 16 * PARTS), v);  // the next chunk, while this one is stored
         if (n == 16) {
 #pragma unroll
           for (int j = 0; j < 16; ++j, yp += a.ldy)
@@ -120,7 +121,7 @@ struct LinearPolicy {
           for (int j = 0; j < 16; ++j, yp += a.ldy)
             if (rv && j < n) *yp = (Y)out[j];
         }
-        yp += 16 * a.ldy;
+        yp += (16 * PARTS - 16) * a.ldy;
       }
       __syncwarp();  // the scales are read: the next tile's may be written
     }
