@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
   volatile int& abort_flag = *reinterpret_cast<volatile int*>(tmem_holder + 1);
   unsigned char* epi_smem = smem + (size_t)stages * sbytes + BAR_BYTES;
   static_assert((2 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)(blockIdx.x & 1u) : 0;  // within the pair (a cluster of two consecutive CTAs)
   int early = 0;  // K steps whose W was requested ahead
 
@@ -313,19 +313,21 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
       while (clock64() - t0 < 2000000LL) {
       }
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
-    // ---- MMA issuer: one thread, so what it does per K step is kept short (descriptors by addition, no divisions:
-    // with them a step took 800 clocks instead of the product's 512)
+  } else if (warp == 1 && rank == 0) {
+    // ---- MMA issuer: the warp stays converged and one lane issues, so that descriptors are formed in uniform
+    // registers.  What a K step takes here has to stay below the product's 512 clocks, also while the epilogue
+    // warps compete for issue slots: with divisions and per-thread operands it took up to 890.
     Ring ring(stages);
     int local = 0;
     bool ok = true, issued = false;
     Tile t;
+    const bool leader = elect_one();
     const uint32_t smem0 = smem_u32(smem);
     const uint64_t a_desc = P::adesc(smem0), b_desc = P::bdesc(ar, smem0 + A_BYTES);
     const uint64_t a_step = P::a_step(), b_step = P::b_step(ar);  // 32 bytes of K on, in 16-byte units
     for (; ok && P::tile(ar, local, t); ++local) {
       const int buf = local & 1;
-      if (local >= 2 && !mbar_wait(&acc_empty[buf], ((local >> 1) - 1) & 1, &abort_flag)) {
+      if (local >= 2 && !mbar_wait_warp(&acc_empty[buf], ((local >> 1) - 1) & 1, &abort_flag)) {
         abort_flag = 1;
         break;
       }
@@ -334,30 +336,30 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
       const uint32_t id = idesc<CG>(mma_n<CG>(t.nb));
       uint32_t accum = 0u;
       for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next()) {
-        if (!mbar_wait(&full[ring.s], ring.phase, &abort_flag)) {
+        if (!mbar_wait_warp(&full[ring.s], ring.phase, &abort_flag)) {
           abort_flag = 1;
           ok = false;
           break;
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint64_t off = (uint64_t)((uint32_t)(ring.s * sbytes) >> 4);
-        uint64_t ad = a_desc + off, bd = b_desc + off;
-#pragma unroll
-        for (int kk = 0; kk < BK / UMMA_K; ++kk) {
+        const uint64_t ad = a_desc + off, bd = b_desc + off;
+        if (leader) {
           umma<CG>(d_tmem, ad, bd, id, accum);
-          accum = 1u;
-          ad += a_step;
-          bd += b_step;
+          umma<CG>(d_tmem, ad + a_step, bd + b_step, id, 1u);
+          umma<CG>(d_tmem, ad + 2 * a_step, bd + 2 * b_step, id, 1u);
+          umma<CG>(d_tmem, ad + 3 * a_step, bd + 3 * b_step, id, 1u);
+          commit<CG>(&empty[ring.s]);
         }
-        commit<CG>(&empty[ring.s]);
+        accum = 1u;
         issued = true;
       }
       if (!ok) break;
-      commit<CG>(&acc_full[buf]);
+      if (leader) commit<CG>(&acc_full[buf]);
     }
-    // every MMA this thread issued completes before the tensor memory is released
+    // every MMA this warp issued completes before the tensor memory is released
     if (issued) {
-      commit<CG>(mma_done);
+      if (leader) commit<CG>(mma_done);
       mbar_wait_drain(mma_done, 0);
     }
   } else if (warp >= 2) {

@@ -138,9 +138,10 @@ struct ForwardPolicy {
         uint32_t skip = c + 32 > t.nb ? 0xFFFFFFFFu << (t.nb - c) : 0u;
         const uint32_t lc = (uint32_t)(label - v0);
         if (lc < 32u) skip |= 1u << lc;
-        float x[32];
+        f2 x[16];
+        const f2 st2 = pack2(st, st);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = (float)(int)v[j] * st;
+        for (int j = 0; j < 16; ++j) x[j] = mul2(pack2((float)(int)v[2 * j], (float)(int)v[2 * j + 1]), st2);
         if (lc < 32u && c + (int)lc < t.nb) {
           const int al = (int)pick(v, (int)lc);
           a.label_logit[tok] = __double2float_rn(dmul(dmul(int_to_f64(al), a.s_tok[tok]), (double)__ldg(a.s_row + label)));
@@ -149,27 +150,38 @@ struct ForwardPolicy {
         float mx = m;
         if (!__any_sync(0xffffffffu, skip != 0u)) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 w = w4[j / 4];
-            mx = fmaxf(mx, fmaxf(fmaxf(x[j] * w.x, x[j + 1] * w.y), fmaxf(x[j + 2] * w.z, x[j + 3] * w.w)));
+          for (int j = 0; j < 16; j += 2) {
+            const float4 w = w4[j / 2];
+            float l0, l1, l2, l3;
+            unpack2(mul2(x[j], pack2(w.x, w.y)), l0, l1);
+            unpack2(mul2(x[j + 1], pack2(w.z, w.w)), l2, l3);
+            mx = fmaxf(mx, fmaxf(fmaxf(l0, l1), fmaxf(l2, l3)));
           }
-          float s = S * ex2(m - mx);
+          const f2 mx2 = pack2(-mx, -mx);
+          f2 s = pack2(S * ex2(m - mx), 0.0f);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 w = w4[j / 4];
-            s += (ex2(fmaf(x[j], w.x, -mx)) + ex2(fmaf(x[j + 1], w.y, -mx))) +
-                 (ex2(fmaf(x[j + 2], w.z, -mx)) + ex2(fmaf(x[j + 3], w.w, -mx)));
+          for (int j = 0; j < 16; j += 2) {
+            const float4 w = w4[j / 2];
+            float l0, l1, l2, l3;
+            unpack2(fma2(x[j], pack2(w.x, w.y), mx2), l0, l1);
+            unpack2(fma2(x[j + 1], pack2(w.z, w.w), mx2), l2, l3);
+            s = add2(s, add2(pack2(ex2(l0), ex2(l1)), pack2(ex2(l2), ex2(l3))));
           }
-          S = s;
+          float s0, s1;
+          unpack2(s, s0, s1);
+          S = s0 + s1;
         } else {
+          float xs[32];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) unpack2(x[j], xs[2 * j], xs[2 * j + 1]);
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (!((skip >> j) & 1u)) mx = fmaxf(mx, x[j] * w1[j]);
+            if (!((skip >> j) & 1u)) mx = fmaxf(mx, xs[j] * w1[j]);
           const float mz = mx == -INFINITY ? 0.0f : mx;  // nothing counted yet
           float s = S * ex2(m - mz);
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (!((skip >> j) & 1u)) s += ex2(fmaf(x[j], w1[j], -mz));
+            if (!((skip >> j) & 1u)) s += ex2(fmaf(xs[j], w1[j], -mz));
           S = s;
         }
         m = mx;
@@ -283,8 +295,9 @@ __global__ void __launch_bounds__(256) grad_prepare_kernel(const float* __restri
     if (m == -INFINITY) m = 0.0f;  // no other row
     o.shift[t] = k;
     const double s = s_tok[t];
-    // an ignored token keeps its zeros whatever its values are
-    o.tok[t] = make_float4(m, (float)s, f == 0.0 ? 0.0f : (float)(f * s), wy == 0.0 ? 0.0f : (float)(wy * s));
+    // a token without a gradient (ignored, or dloss 0) has none whatever its values are
+    o.tok[t] = f == 0.0 && wy == 0.0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                     : make_float4(m, (float)s, (float)(f * s), (float)(wy * s));
     o.fac[t] = make_double2(f, wy);
   }
 }
@@ -309,12 +322,12 @@ __device__ __forceinline__ FixedPoint fixed_point(const uint32_t* srow) {
   return p;
 }
 
-// Pseudo-random number in [-1/2, 1/2) of an accumulator, added before the coefficient is rounded to whole steps:
+// Pseudo-random number in [1, 2) of an accumulator; less 3/2 it is added before the coefficient is rounded to whole steps:
 // the rounding is then right on average for coefficients of any size.  (Rounded to nearest, the thousands of
 // coefficients below half a step all become zero, which sums over tokens show: 4e-6 of the norm weight's
 // gradient at 2048 tokens x 50288 rows.)
 __device__ __forceinline__ float dither(uint32_t acc) {
-  return __uint_as_float(((acc * 0x9E3779B1u) & 0x7FFFFFu) | 0x3F800000u) - 1.5f;
+  return __uint_as_float(((acc * 0x9E3779B1u) & 0x7FFFFFu) | 0x3F800000u);
 }
 
 // W's piece [nv rows from v0] as K-major operand of the second product, [d / 128][Vp / 16][128][16] bytes
@@ -414,7 +427,7 @@ struct DigitPolicy {
       const bool valid = tk < a.M;
       tf = valid ? a.tok[tk] : make_float4(0.f, 0.f, 0.f, 0.f);
       label = valid ? a.labels[tk] - a.v0 : -1;
-      most = (fp.range << (valid ? a.shift[tk] : 0)) - 1;
+      most = (fp.range << (valid ? a.shift[tk] : 0)) - 1 + fp.offset;
 #pragma unroll
       for (int k = 0; k < EPI_COLS / 32; ++k) {
         const int c = k * 64 + half * 32 + lane;
@@ -430,6 +443,7 @@ struct DigitPolicy {
       unsigned char* dst = a.digits + (size_t)(tk / a.tb) * a.tb * a.Vp + (size_t)(tk % a.tb) * 16;
       uint32_t v[32];
       const float *w1 = sr, *u1 = cu;
+      const f2 s2 = pack2(tf.y, tf.y), m2 = pack2(-tf.x, -tf.x), f_s = pack2(tf.z, tf.z);
       if (half * 32 < t.nb) tmem_ld32(taddr + (uint32_t)(half * 32), v);
 #pragma unroll 1  // four copies of the body would not stay in the instruction cache
       for (int c = half * 32; c < t.nb; c += 64, w1 += 32, u1 += 32) {
@@ -437,25 +451,30 @@ struct DigitPolicy {
         const int v0 = t.b0 + c;  // within the piece
         const uint32_t lc = (uint32_t)(label - v0);
         const bool any = __any_sync(0xffffffffu, lc < 32u);
-        float h[32];
+        const float at_label = any ? (float)(int)pick(v, (int)(lc & 31u)) : 0.0f;
+        f2 h[16];
         uint32_t high = 0u;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 w = reinterpret_cast<const float4*>(w1)[j / 4];
-          const float4 u = reinterpret_cast<const float4*>(u1)[j / 4];
-          const float wv[4] = {w.x, w.y, w.z, w.w}, uv[4] = {u.x, u.y, u.z, u.w};
+        for (int j = 0; j < 16; ++j) {
+          const f2 w = *reinterpret_cast<const f2*>(w1 + 2 * j), u = *reinterpret_cast<const f2*>(u1 + 2 * j);
+          const f2 av = pack2((float)(int)v[2 * j], (float)(int)v[2 * j + 1]);
+          float e0, e1, n0, n1;
+          unpack2(fma2(mul2(av, s2), w, m2), e0, e1);
+          const f2 e = pack2(ex2(e0), ex2(e1));
+          if (DS) h[j] = mul2(mul2(e, av), f_s);
+          unpack2(fma2(e, u, add2(pack2(dither(v[2 * j]), dither(v[2 * j + 1])), pack2(-1.5f, -1.5f))), n0, n1);
+          v[2 * j] = (uint32_t)__viaddmin_s32(__float2int_rn(n0), fp.offset, most);
+          v[2 * j + 1] = (uint32_t)__viaddmin_s32(__float2int_rn(n1), fp.offset, most);
+          high |= v[2 * j] | v[2 * j + 1];
+        }
+        if (any && lc < 32u) {  // the label's own column: no digits, and its gradient of the row scale
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float av = (float)(int)v[j + k];
-            float e = ex2(fmaf(av * tf.y, wv[k], -tf.x));
-            if (DS) h[j + k] = tf.z == 0.0f ? 0.0f : tf.z * e * av;
-            if (any && (int)lc == j + k) {
-              e = 0.0f;
-              if (DS) h[j + k] = tf.w * av;
-            }
-            const float n = fmaf(e, uv[k], dither(v[j + k]));
-            v[j + k] = (uint32_t)(min(__float2int_rn(n), most) + fp.offset);
-            high |= v[j + k];
+          for (int j = 0; j < 16; ++j) {
+            float h0, h1;
+            if (DS) unpack2(h[j], h0, h1);
+            if ((int)lc == 2 * j) v[2 * j] = (uint32_t)fp.offset, h0 = tf.w * at_label;
+            if ((int)lc == 2 * j + 1) v[2 * j + 1] = (uint32_t)fp.offset, h1 = tf.w * at_label;
+            if (DS) h[j] = pack2(h0, h1);
           }
         }
         if (valid && (high >> 24)) {
@@ -494,15 +513,20 @@ struct DigitPolicy {
         if (DS) {
           // column sums over the warp's 32 tokens: halves exchanged at every step, lane j ends with column j
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            const bool up = (lane & o) != 0;
+          for (int o = 8; o > 0; o >>= 1) {
+            const bool up = (lane & (2 * o)) != 0;
 #pragma unroll
             for (int j = 0; j < o; ++j) {
-              const float give = up ? h[j] : h[j + o], keep = up ? h[j + o] : h[j];
-              h[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+              f2 give = up ? h[j] : h[j + o];
+              const f2 keep = up ? h[j + o] : h[j];
+              give.v = __shfl_xor_sync(0xffffffffu, give.v, 2 * o);
+              h[j] = add2(keep, give);
             }
           }
-          if (c + lane < t.nb) a.colpart[(size_t)(t.a0 / 32 + q) * a.Vp + v0 + lane] = h[0];
+          float h0, h1;
+          unpack2(h[0], h0, h1);
+          h0 = ((lane & 1) ? h1 : h0) + __shfl_xor_sync(0xffffffffu, (lane & 1) ? h0 : h1, 1);
+          if (c + lane < t.nb) a.colpart[(size_t)(t.a0 / 32 + q) * a.Vp + v0 + lane] = h0;
         }
       }
       __syncwarp();  // the scales are read: the next tile's may be written

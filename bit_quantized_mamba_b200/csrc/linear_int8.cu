@@ -24,14 +24,16 @@ using namespace gemm_i8;
 // conversion units bound the product: 2048 x 50288 x 2048 took 215 us of 133 us without an epilogue.)
 // s and w in [2^-40, 2^40] (ordinary) keep every term normal; s = 0 gives acc = 0.
 __device__ __forceinline__ bool ordinary(float s) { return fabsf(s) >= 0x1p-40f && fabsf(s) <= 0x1p40f; }
-__device__ __forceinline__ float scaled(uint32_t acc, float s, float w, bool& sure) {
-  const float x = (float)(int)acc;
-  const float p = fmul(x, s), e = fmaf(x, s, -p);
-  const float y = fmul(p, w), r = fmaf(e, w, fmaf(p, w, -y));
-  const float d = fabsf(y) * 0x1p-46f;
-  const float lo = fadd(y, r - d), hi = fadd(y, r + d);
-  sure = sure && lo == hi && acc + (1u << 24) <= (2u << 24);
-  return lo;
+__device__ __forceinline__ void scaled(uint32_t acc0, uint32_t acc1, f2 s, f2 w, bool& sure, float& out0, float& out1) {
+  const f2 x = pack2((float)(int)acc0, (float)(int)acc1);
+  const f2 p = mul2(x, s), e = fma2(x, s, neg2(p));
+  const f2 y = mul2(p, w), r = fma2(e, w, fma2(p, w, neg2(y)));
+  const f2 d = abs2(y), t = pack2(0x1p-46f, 0x1p-46f);
+  const f2 lo = add2(y, fma2(neg2(d), t, r)), hi = add2(y, fma2(d, t, r));
+  float hi0, hi1;
+  unpack2(lo, out0, out1);
+  unpack2(hi, hi0, hi1);
+  sure = sure && out0 == hi0 && out1 == hi1 && acc0 + (1u << 24) <= (2u << 24) && acc1 + (1u << 24) <= (2u << 24);
 }
 
 template <typename Y, int CG_>
@@ -85,6 +87,7 @@ struct LinearPolicy {
       const bool rv = r < t.na;
       uint32_t v[16];
       const float* st = s;
+      const f2 sw2 = pack2(sw, sw);
       Y* yp = a.y + (int64_t)(t.b0 + part * 16) * a.ldy + row;
       if (part * 16 < t.nb) tmem_ld16(taddr + (uint32_t)(part * 16), v);
 #pragma unroll 1
@@ -101,10 +104,8 @@ struct LinearPolicy {
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 s4 = *reinterpret_cast<const float4*>(st + j);
-          out[j] = scaled(v[j], s4.x, sw, sure);
-          out[j + 1] = scaled(v[j + 1], s4.y, sw, sure);
-          out[j + 2] = scaled(v[j + 2], s4.z, sw, sure);
-          out[j + 3] = scaled(v[j + 3], s4.w, sw, sure);
+          scaled(v[j], v[j + 1], pack2(s4.x, s4.y), sw2, sure, out[j], out[j + 1]);
+          scaled(v[j + 2], v[j + 3], pack2(s4.z, s4.w), sw2, sure, out[j + 2], out[j + 3]);
         }
         if (!sure) {
 #pragma unroll
