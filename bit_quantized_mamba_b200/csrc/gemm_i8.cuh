@@ -142,12 +142,10 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// One lane's TMA copy of a K step kb: box at (x + kb dx, y + kb dy) to the stage's byte `off`.
-struct Copy {
-  const CUtensorMap* map;  // NULL: this lane has none
-  int x, y, dx, dy;
-  uint32_t off;
-  bool w;                  // of the matrix W, which does not change
+// The TMA copies of an operand's K step kb: n boxes of `box` rows of 128 bytes at (kb dx, y + kb dy + i box).
+struct Boxes {
+  const CUtensorMap* map;
+  int n, box, y, dx, dy;
 };
 
 // What every policy's arguments start with.
@@ -190,11 +188,18 @@ __device__ __forceinline__ Tile own_tile(Tile t, int rank) {
   return t;
 }
 
+// (Converged warp; `leader` is one lane of it.)
+template <int CG>
+__device__ __forceinline__ void issue(const Boxes& o, int kb, unsigned char* dst, uint32_t bar, bool leader) {
+  for (int i = 0; i < o.n; ++i)
+    if (leader) tma_load<CG>(dst + i * o.box * BK, o.map, kb * o.dx, o.y + kb * o.dy + i * o.box, bar);
+}
+
 // With PDL the kernel may start while the one that writes the tokens' codes still runs: the first round of W is
-// requested without waiting for it.  Returns the number of K steps.  (Whole warp.)
+// requested without waiting for it.  Returns the number of K steps.  (Converged warp.)
 template <class P>
-__device__ __forceinline__ int request_w(const typename P::Args& ar, unsigned char* smem, uint64_t* full, int rank,
-                                         int lane) {
+__device__ __forceinline__ int request_w(const typename P::Args& ar, unsigned char* smem, uint64_t* full,
+                                         uint32_t full_bar, int rank, bool leader) {
   if (!P::W_EARLY) return 0;
   constexpr int CG = P::CG;
   const int sbytes = stage_bytes(ar.c);
@@ -203,13 +208,10 @@ __device__ __forceinline__ int request_w(const typename P::Args& ar, unsigned ch
   for (int j = 0; n < ar.c.stages && P::tile(ar, j, pt); ++j) {
     const Tile t = own_tile<CG>(pt, rank);
     const uint32_t bytes = P::bytes(ar, pt);
-    const Copy cp = P::copy(ar, t, rank, lane);
+    const Boxes w = P::W_IS_A ? P::boxes_a(ar, t, rank) : P::boxes_b(ar, t, rank);
     for (int kb = t.kb0; kb < t.kb1 && n < ar.c.stages; ++kb, ++n) {
-      if (rank == 0 && lane == 0) mbar_expect_tx(&full[n], bytes);
-      __syncwarp();
-      if (cp.map && cp.w)
-        tma_load<CG>(smem + (size_t)n * sbytes + cp.off, cp.map, cp.x + kb * cp.dx, cp.y + kb * cp.dy,
-                     leader_bar<CG>(&full[n]));
+      if (rank == 0 && leader) mbar_expect_tx(&full[n], bytes);
+      issue<CG>(w, kb, smem + (size_t)n * sbytes + (P::W_IS_A ? 0 : A_BYTES), full_bar + 8 * n, leader);
     }
   }
   return n;
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
   }
   if (warp == 0) {
     __syncwarp();
-    if (CG == 1) early = request_w<P>(ar, smem, full, 0, lane);  // while tensor memory is allocated
+    if (CG == 1) early = request_w<P>(ar, smem, full, smem_u32(full), 0, elect_one());  // while tensor memory is allocated
   }
   if (warp == 1) {
     if (CG == 1) {
@@ -273,8 +275,10 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
   if (threadIdx.x == 0) pdl_launch_dependents();
 
   if (warp == 0) {
-    // ---- producer: each tile's K steps through the stage ring, one copy per lane
-    if (CG == 2) early = request_w<P>(ar, smem, full, rank, lane);
+    // ---- producer: each tile's K steps through the stage ring (converged, like the MMA issuer)
+    const bool leader = elect_one();
+    const uint32_t full_bar = leader_bar<CG>(full);
+    if (CG == 2) early = request_w<P>(ar, smem, full, full_bar, rank, leader);
     pdl_wait();
     Ring ring(stages);
     bool ok = true;
@@ -282,21 +286,19 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
     for (int j = 0; ok && P::tile(ar, j, pt); ++j) {
       const Tile t = own_tile<CG>(pt, rank);
       const uint32_t bytes = P::bytes(ar, pt);  // of the whole tile's K step, both CTAs'
-      const Copy cp = P::copy(ar, t, rank, lane);
+      const Boxes a = P::boxes_a(ar, t, rank), b = P::boxes_b(ar, t, rank);
       for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next()) {
         const int s = ring.s;
-        if (ring.round > 0 && !mbar_wait(&empty[s], ring.phase ^ 1u, &abort_flag)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
+        if (ring.round > 0 && !mbar_wait_warp(&empty[s], ring.phase ^ 1u, &abort_flag)) {
           abort_flag = 1;
+          ok = false;
           break;
         }
         const bool late = ring.round == 0 && s < early;  // its W is under way
-        if (rank == 0 && lane == 0 && !late) mbar_expect_tx(&full[s], bytes);
-        __syncwarp();
-        if (cp.map && !(late && cp.w))
-          tma_load<CG>(smem + (size_t)s * sbytes + cp.off, cp.map, cp.x + kb * cp.dx, cp.y + kb * cp.dy,
-                       leader_bar<CG>(&full[s]));
+        if (rank == 0 && leader && !late) mbar_expect_tx(&full[s], bytes);
+        unsigned char* st = smem + (size_t)s * sbytes;
+        if (!(late && P::W_IS_A)) issue<CG>(a, kb, st, full_bar + 8 * s, leader);
+        if (!(late && !P::W_IS_A)) issue<CG>(b, kb, st + A_BYTES, full_bar + 8 * s, leader);
       }
     }
     // the last copies land before this CTA may exit (those of a pair's second CTA are counted by the first, which
@@ -502,29 +504,14 @@ __device__ __forceinline__ uint32_t row_bytes(const RowArgs& r, const Tile& t) {
   }
   return (uint32_t)n * BK;
 }
-// Lanes 0.. copy A's boxes, lanes 16.. B's (at most eight each).
-template <int CG, bool W_IS_A>
-__device__ __forceinline__ Copy row_copy(const RowArgs& r, const CUtensorMap* ma, const CUtensorMap* mb, const Tile& t,
-                                         int rank, int lane) {
+template <int CG>
+__device__ __forceinline__ Boxes row_boxes_a(const RowArgs& r, const CUtensorMap* map, const Tile& t) {
+  return Boxes{map, (t.na + r.box_a - 1) / r.box_a, r.box_a, t.a0, BK, 0};
+}
+template <int CG>
+__device__ __forceinline__ Boxes row_boxes_b(const RowArgs& r, const CUtensorMap* map, const Tile& t, int rank) {
   const int half = mma_n<CG>(t.nb) / CG;
-  Copy c;
-  c.map = nullptr;
-  c.x = 0;
-  c.dx = BK;
-  c.dy = 0;
-  c.w = (lane < 16) == W_IS_A;
-  if (lane < 16) {
-    const int i = lane * r.box_a;
-    if (i < t.na) c.map = ma;
-    c.y = t.a0 + i;
-    c.off = (uint32_t)(i * BK);
-  } else {
-    const int i = (lane - 16) * r.box_b;
-    if (i < half) c.map = mb;
-    c.y = r.b_first + t.b0 + rank * half + i;
-    c.off = (uint32_t)(A_BYTES + i * BK);
-  }
-  return c;
+  return Boxes{map, (half + r.box_b - 1) / r.box_b, r.box_b, r.b_first + t.b0 + rank * half, BK, 0};
 }
 
 }  // namespace gemm_i8

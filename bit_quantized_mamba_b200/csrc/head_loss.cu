@@ -69,7 +69,7 @@ __device__ __forceinline__ uint32_t pick(const uint32_t (&v)[32], int j) {
 template <int CG_>
 struct ForwardPolicy {
   static constexpr int CG = CG_;
-  static constexpr bool W_EARLY = true;
+  static constexpr bool W_EARLY = true, W_IS_A = false;
   static constexpr int EPI_WARPS = 8, EPI_COLS = BN_MAX / 2;  // columns of an epilogue warp
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
@@ -84,8 +84,11 @@ struct ForwardPolicy {
   };
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 0, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
-  static __device__ __forceinline__ Copy copy(const Args& a, const Tile& t, int rank, int lane) {
-    return row_copy<CG, false>(a.r, &a.map_a, &a.map_b, t, rank, lane);
+  static __device__ __forceinline__ Boxes boxes_a(const Args& a, const Tile& t, int) {
+    return row_boxes_a<CG>(a.r, &a.map_a, t);
+  }
+  static __device__ __forceinline__ Boxes boxes_b(const Args& a, const Tile& t, int rank) {
+    return row_boxes_b<CG>(a.r, &a.map_b, t, rank);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(256) transpose_kernel(const int8_t* __restrict
 template <int CG_, bool DS>
 struct DigitPolicy {
   static constexpr int CG = CG_;
-  static constexpr bool W_EARLY = true;
+  static constexpr bool W_EARLY = true, W_IS_A = false;
   static constexpr int EPI_WARPS = 8, EPI_COLS = BN_MAX / 2;  // columns of an epilogue warp
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
@@ -404,8 +407,11 @@ struct DigitPolicy {
   };
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 0, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
-  static __device__ __forceinline__ Copy copy(const Args& a, const Tile& t, int rank, int lane) {
-    return row_copy<CG, false>(a.r, &a.map_a, &a.map_b, t, rank, lane);
+  static __device__ __forceinline__ Boxes boxes_a(const Args& a, const Tile& t, int) {
+    return row_boxes_a<CG>(a.r, &a.map_a, t);
+  }
+  static __device__ __forceinline__ Boxes boxes_b(const Args& a, const Tile& t, int rank) {
+    return row_boxes_b<CG>(a.r, &a.map_b, t, rank);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
@@ -541,7 +547,7 @@ struct DigitPolicy {
 template <int CG_>
 struct GradPolicy {
   static constexpr int CG = CG_;
-  static constexpr bool W_EARLY = false;
+  static constexpr bool W_EARLY = false, W_IS_A = true;
   static constexpr int EPI_WARPS = 8;
   struct Args {
     CUtensorMap map_a, map_b;  // transposed W, digits: blocks of 128 bytes
@@ -574,21 +580,11 @@ struct GradPolicy {
     return CG * (A_BYTES + (uint32_t)a.tb * BK);
   }
   // both operands were laid out as the product reads them: eight 16-byte K columns of all rows are contiguous
-  static __device__ __forceinline__ Copy copy(const Args& a, const Tile& t, int rank, int lane) {
-    Copy c;
-    c.map = lane == 0 ? &a.map_a : lane == 16 ? &a.map_b : nullptr;
-    c.x = c.dx = 0;
-    c.w = false;
-    if (lane < 16) {
-      c.y = (int)((size_t)t.a0 * a.Vp / 128);
-      c.dy = BM;
-      c.off = 0u;
-    } else {
-      c.y = (int)((t.aux * a.plane + (size_t)(t.b0 + rank * a.tb) * a.Vp) / 128);
-      c.dy = a.tb;
-      c.off = (uint32_t)A_BYTES;
-    }
-    return c;
+  static __device__ __forceinline__ Boxes boxes_a(const Args& a, const Tile& t, int) {
+    return Boxes{&a.map_a, 1, BM, (int)((size_t)t.a0 * a.Vp / 128), 0, BM};
+  }
+  static __device__ __forceinline__ Boxes boxes_b(const Args& a, const Tile& t, int rank) {
+    return Boxes{&a.map_b, 1, a.tb, (int)((t.aux * a.plane + (size_t)(t.b0 + rank * a.tb) * a.Vp) / 128), 0, a.tb};
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_plain(addr, BM * 16); }
   static __device__ __forceinline__ uint64_t bdesc(const Args& a, uint32_t addr) {

@@ -39,7 +39,7 @@ __device__ __forceinline__ void scaled(uint32_t acc0, uint32_t acc1, f2 s, f2 w,
 template <typename Y, int CG_>
 struct LinearPolicy {
   static constexpr int CG = CG_;
-  static constexpr bool W_EARLY = true;
+  static constexpr bool W_EARLY = true, W_IS_A = true;
   static constexpr int EPI_WARPS = 16, PARTS = EPI_WARPS / 4, EPI_COLS = BN_MAX / PARTS;  // columns of a warp
   struct Args {
     CUtensorMap map_a, map_b;  // W, codes
@@ -54,8 +54,11 @@ struct LinearPolicy {
   };
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 1, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
-  static __device__ __forceinline__ Copy copy(const Args& a, const Tile& t, int rank, int lane) {
-    return row_copy<CG, true>(a.r, &a.map_a, &a.map_b, t, rank, lane);
+  static __device__ __forceinline__ Boxes boxes_a(const Args& a, const Tile& t, int) {
+    return row_boxes_a<CG>(a.r, &a.map_a, t);
+  }
+  static __device__ __forceinline__ Boxes boxes_b(const Args& a, const Tile& t, int rank) {
+    return row_boxes_b<CG>(a.r, &a.map_b, t, rank);
   }
   static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
