@@ -2,8 +2,8 @@
 // scaling), and its gradient (include/dfssm.h, dfssm_embed_tokens and dfssm_embed_tokens_backward).
 //
 // Forward: h[t][i] = fl32(W[tok_t][i] s_row[tok_t]) — a gather bound by memory (the output is four or two times
-// the table rows read).  One row per CTA at a time, four (fp32) or eight (bf16) values a thread, so that both
-// the loads and the stores of a warp are contiguous.
+// the table rows read).  Four (fp32) or eight (bf16) values a thread, so that both the loads and the stores of
+// a warp are contiguous.
 //
 // Gradient: dE[v][i] = sum over t with tok_t = v of dh[t][i] and ds_row[v] = sum_i W[v][i] dE[v][i], in an order
 // fixed by the tokens alone:
@@ -37,36 +37,55 @@ struct EmbedTokensArgs {
   int V, d, n;
 };
 
-template <typename T>
+// WPT warps per token (8 or 1): a CTA for a token where there are few tokens, a warp where they fill the device, with
+// the loads of four pieces of a row in flight.
+template <typename T, int WPT>
 __global__ void __launch_bounds__(256) embed_tokens_kernel(EmbedTokensArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  for (int t = blockIdx.x; t < a.n; t += gridDim.x) {
+  constexpr int N = sizeof(T) == 4 ? 4 : 8, STEP = WPT * 32 * N, U = 4;  // values a thread handles at a time
+  const int per_cta = 8 / WPT, sub = (threadIdx.x >> 5) / WPT, i0 = (threadIdx.x % (WPT * 32)) * N;
+  for (int t = blockIdx.x * per_cta + sub; t < a.n; t += gridDim.x * per_cta) {
     const int tok = __ldg(a.tokens + t);
     const bool ok = tok >= 0 && tok < a.V;
-    if (!ok && threadIdx.x == 0) atomicExch(a.status, kBadTokenCode);
+    if (!ok && i0 == 0) atomicExch(a.status, kBadTokenCode);
     const float sc = ok ? __ldg(a.s_row + tok) : 0.0f;
     const int8_t* row = a.W + (size_t)(ok ? tok : 0) * a.d;
     T* h = reinterpret_cast<T*>(a.h) + (int64_t)t * a.ldh;
-    const auto value = [&](uint32_t w, int k) { return fmul((float)(int8_t)(w >> (8 * k)), sc); };
-    if (sizeof(T) == 4) {
-      for (int i = threadIdx.x * 4; i < a.d; i += 256 * 4) {
-        const uint32_t w = ok ? __ldg(reinterpret_cast<const uint32_t*>(row + i)) : 0u;
-        st_f4(h + i, make_float4(value(w, 0), value(w, 1), value(w, 2), value(w, 3)));
+    for (int i = i0; i < a.d; i += U * STEP) {
+      uint2 w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = i + u * STEP;
+        w[u] = make_uint2(0u, 0u);
+        if (k < a.d) {
+          if (N == 8) w[u] = __ldg(reinterpret_cast<const uint2*>(row + k));
+          else w[u].x = __ldg(reinterpret_cast<const uint32_t*>(row + k));
+        }
       }
-    } else {
-      for (int i = threadIdx.x * 8; i < a.d; i += 256 * 8) {
-        const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(row + i)) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = i + u * STEP;
+        if (k >= a.d) continue;
         float v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[k] = value(w.x, k);
-          v[k + 4] = value(w.y, k);
+        for (int j = 0; j < 4; ++j) {
+          v[j] = ok ? fmul((float)(int8_t)(w[u].x >> (8 * j)), sc) : 0.0f;
+          v[j + 4] = ok ? fmul((float)(int8_t)(w[u].y >> (8 * j)), sc) : 0.0f;
         }
-        store8<T>(h + i, v);
+        if constexpr (N == 8) store8<T>(h + k, v);
+        else st_f4(h + k, make_float4(v[0], v[1], v[2], v[3]));
       }
     }
   }
+}
+
+template <typename T>
+cudaError_t launch_embed_tokens(const EmbedTokensArgs& a, cudaStream_t st) {
+  const int most = num_sms() * 8;  // CTAs resident at a time
+  if (a.n <= most) return launch_pdl(embed_tokens_kernel<T, 8>, dim3(a.n), dim3(256), 0, st, a);
+  const int ctas = a.n / 8 + (a.n % 8 != 0);
+  return launch_pdl(embed_tokens_kernel<T, 1>, dim3(ctas < most ? ctas : most), dim3(256), 0, st, a);
 }
 
 // ------------------------------------------------------------------------------------ sort
@@ -331,7 +350,7 @@ constexpr int MAX_WINDOW = 64;
 // A window of sorted positions: rows added in order, run by run.  A run is final when both its ends lie in the
 // window.
 template <typename T, int CH>
-__global__ void __launch_bounds__(256) window_kernel(SumArgs a) {
+__global__ void __launch_bounds__(256, CH == 1 ? 4 : CH == 2 ? 3 : 2) window_kernel(SumArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ int32_t id[MAX_WINDOW + 2], ps[MAX_WINDOW];
@@ -354,12 +373,17 @@ __global__ void __launch_bounds__(256) window_kernel(SumArgs a) {
   int start = 0;
   for (int r0 = 0; r0 < nk; r0 += U) {
     float x[U][CH][8];
+    uint2 wr[U][CH];  // the rows of W where runs end, requested with the gradient's
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int i = (threadIdx.x + 256 * c) * 8;
-        if (r0 + u < nk && i < a.d) {
+        const int i = (threadIdx.x + 256 * c) * 8, r = r0 + u;
+        wr[u][c] = make_uint2(0u, 0u);
+        if (r < nk && i < a.d) {
+          const int v = id[r + 1];
+          if (a.ds_row && v < a.V && !(r + 1 < nk && id[r + 2] == v))
+            wr[u][c] = __ldg(reinterpret_cast<const uint2*>(a.W + (size_t)v * a.d + i));
           load8<T>(reinterpret_cast<const T*>(a.dh) + (int64_t)ps[r0 + u] * a.lddh + i, x[u][c]);
         } else {
 #pragma unroll
@@ -385,7 +409,7 @@ __global__ void __launch_bounds__(256) window_kernel(SumArgs a) {
           const int i = (threadIdx.x + 256 * c) * 8;
           if (i >= a.d) continue;
           if (a.ds_row) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.W + (size_t)v * a.d + i));
+            const uint2 w = wr[u][c];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               dot = fmaf((float)(int8_t)(w.x >> (8 * j)), acc[c][j], dot);
@@ -437,38 +461,53 @@ __global__ void __launch_bounds__(256) window_kernel(SumArgs a) {
 __global__ void __launch_bounds__(64) join_kernel(SumArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const long long w = blockIdx.x, k1 = (w + 1) * a.window;
+  const long long w = blockIdx.x, k0 = w * a.window, k1 = k0 + a.window;
   if (k1 >= a.n) return;
-  const int v = a.ids[k1 - 1];
-  if (v >= a.V || a.ids[k1] != v) return;
-  const long long k0 = w * a.window;
-  if (k0 > 0 && a.ids[k0 - 1] == v && a.ids[k0] == v) return;  // it started earlier
-  // windows w + 1 .. we hold more of it
-  long long we = w + 1;
-  while ((we + 1) * a.window < a.n && a.ids[(we + 1) * a.window - 1] == v && a.ids[(we + 1) * a.window] == v) ++we;
+  const int v = a.ids[k1 - 1], next = a.ids[k1], first = a.ids[k0], prev = k0 > 0 ? a.ids[k0 - 1] : -1;
+  if (v >= a.V || next != v) return;
+  if (first == v && prev == v) return;  // the run started earlier
+  // windows w + 1 .. we hold more of it: window x does if x's boundary with the one before lies within the run
+  const int lane = threadIdx.x & 31;
+  long long we = w;
+  while (true) {
+    const long long k = (we + 1 + lane) * a.window;
+    const bool in = k < a.n && a.ids[k - 1] == v && a.ids[k] == v;
+    const uint32_t out = ~__ballot_sync(0xffffffffu, in);
+    we += out ? __ffs(out) - 1 : 32;
+    if (out) break;
+  }
+  if (a.ds_row && blockIdx.y == 0 && threadIdx.x < 32) {
+    float s = 0.0f;
+    for (long long x = w + 1 + lane; x <= we; x += 32) s += a.dpart[(size_t)x * 2];
+    s = warp_sum(s);
+    if (lane == 0) {
+      s += a.dpart[(size_t)w * 2 + 1];
+      a.ds_row[v] = a.accumulate ? a.ds_row[v] + s : s;
+    }
+  }
   const int i = (blockIdx.y * 64 + threadIdx.x) * 8;
-  if (a.dE && i < a.d) {
-    float acc[8];
-    load8<float>(a.part + ((size_t)w * 2 + 1) * a.d + i, acc);
-#pragma unroll 4
-    for (long long x = w + 1; x <= we; ++x) {
-      float p[8];
-      load8<float>(a.part + (size_t)x * 2 * a.d + i, p);
+  if (!a.dE || i >= a.d) return;
+  float acc[8];
+  load8<float>(a.part + ((size_t)w * 2 + 1) * a.d + i, acc);
+  constexpr int U = 8;  // partial rows in flight
+  for (long long x0 = w + 1; x0 <= we; x0 += U) {
+    float p[U][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += p[j];
-    }
-    float* e = a.dE + (size_t)v * a.d + i;
-    if (a.accumulate) {
+    for (int u = 0; u < U; ++u)
+      if (x0 + u <= we) load8<float>(a.part + (size_t)(x0 + u) * 2 * a.d + i, p[u]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += e[j];
-    }
-    store8<float>(e, acc);
+    for (int u = 0; u < U; ++u)
+      if (x0 + u <= we) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += p[u][j];
+      }
   }
-  if (a.ds_row && blockIdx.y == 0 && threadIdx.x == 0) {
-    float s = a.dpart[(size_t)w * 2 + 1];
-    for (long long x = w + 1; x <= we; ++x) s += a.dpart[(size_t)x * 2];
-    a.ds_row[v] = a.accumulate ? a.ds_row[v] + s : s;
+  float* e = a.dE + (size_t)v * a.d + i;
+  if (a.accumulate) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] += e[j];
   }
+  store8<float>(e, acc);
 }
 
 template <typename T>
@@ -524,11 +563,8 @@ extern "C" int dfssm_embed_tokens(const int8_t* W, const float* s_row, int V, in
   if (!workspace || !al(workspace, 256) || ws_bytes < kStatusBytes) return DFSSM_EWORKSPACE;
   if (!device_ok()) return DFSSM_EDEVICE;
   const EmbedTokensArgs a{W, s_row, tokens, h, ldh, static_cast<int*>(workspace), V, d, n};
-  const int most = num_sms() * 8, grid = n < most ? n : most;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = h_type == DFSSM_F32
-                            ? launch_pdl(embed_tokens_kernel<float>, dim3(grid), dim3(256), 0, s, a)
-                            : launch_pdl(embed_tokens_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, s, a);
+  const cudaError_t e = h_type == DFSSM_F32 ? launch_embed_tokens<float>(a, s) : launch_embed_tokens<__nv_bfloat16>(a, s);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
 }
 
