@@ -18,6 +18,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "rows.cuh"
 #include "umma.cuh"
 
 namespace dfssm {
@@ -151,17 +152,20 @@ struct Boxes {
 // What every policy's arguments start with.
 struct Common {
   int b_tile;   // columns a stage of one CTA has room for
+  int resident; // bytes of B kept in shared memory for all of K instead (P::RESIDENT; a multiple of 1024)
   int stages;
   int* err;     // status word: kDeviceTimeout after a wait ran out of budget
 };
-__host__ __device__ inline int stage_bytes(const Common& c) { return A_BYTES + c.b_tile * BK; }
-// Ring depth for b_tile columns beside epi_bytes of epilogue scratch, and the shared memory it takes.
-inline int ring_stages(int b_tile, int epi_bytes) {
-  const int n = (SMEM_LIMIT - 1024 - BAR_BYTES - epi_bytes) / (A_BYTES + b_tile * BK);
+__host__ __device__ inline int stage_bytes(const Common& c) {
+  return A_BYTES + (c.resident ? 0 : c.b_tile * BK);
+}
+// Ring depth beside epi_bytes of epilogue scratch, and the shared memory it takes.
+inline int ring_stages(const Common& c, int epi_bytes) {
+  const int n = (SMEM_LIMIT - 1024 - BAR_BYTES - c.resident - epi_bytes) / stage_bytes(c);
   return n < MAX_STAGES ? n : MAX_STAGES;
 }
 inline size_t smem_bytes(const Common& c, int epi_bytes) {
-  return 1024 + (size_t)c.stages * stage_bytes(c) + BAR_BYTES + epi_bytes;
+  return 1024 + (size_t)c.resident + (size_t)c.stages * stage_bytes(c) + BAR_BYTES + epi_bytes;
 }
 
 // Position in the ring of stages: the stage, the parity of its phase, and how often the ring went round.
@@ -222,17 +226,19 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
   constexpr int CG = P::CG;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // aligned by an offset from the array itself, so that every access stays a shared-memory access
-  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* resident = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* smem = resident + ar.c.resident;
   const int stages = ar.c.stages, sbytes = stage_bytes(ar.c);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)stages * sbytes);  // [stages] TMA -> MMA
   uint64_t* empty = full + MAX_STAGES;      // [stages] MMA -> producer
   uint64_t* acc_full = empty + MAX_STAGES;  // [2] MMA -> epilogue
   uint64_t* acc_empty = acc_full + 2;       // [2] epilogue (of both CTAs) -> MMA
   uint64_t* mma_done = acc_empty + 2;       // every MMA of this CTA complete
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint64_t* b_ready = mma_done + 1;         // a resident B is written: epilogue -> MMA
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(b_ready + 1);
   volatile int& abort_flag = *reinterpret_cast<volatile int*>(tmem_holder + 1);
   unsigned char* epi_smem = smem + (size_t)stages * sbytes + BAR_BYTES;
-  static_assert((2 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
+  static_assert((2 * MAX_STAGES + 6) * 8 + 8 <= BAR_BYTES, "barrier area");
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)(blockIdx.x & 1u) : 0;  // within the pair (a cluster of two consecutive CTAs)
   int early = 0;  // K steps whose W was requested ahead
@@ -248,6 +254,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
       mbar_init(&acc_empty[b], P::EPI_WARPS * CG);
     }
     mbar_init(mma_done, 1);
+    mbar_init(b_ready, P::EPI_WARPS);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -279,7 +286,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
     const bool leader = elect_one();
     const uint32_t full_bar = leader_bar<CG>(full);
     if (CG == 2) early = request_w<P>(ar, smem, full, full_bar, rank, leader);
-    pdl_wait();
+    if (!P::RESIDENT) pdl_wait();  // with a resident B it loads W alone
     Ring ring(stages);
     bool ok = true;
     Tile pt;
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
         if (rank == 0 && leader && !late) mbar_expect_tx(&full[s], bytes);
         unsigned char* st = smem + (size_t)s * sbytes;
         if (!(late && P::W_IS_A)) issue<CG>(a, kb, st, full_bar + 8 * s, leader);
-        if (!(late && !P::W_IS_A)) issue<CG>(b, kb, st + A_BYTES, full_bar + 8 * s, leader);
+        if (!P::RESIDENT && !(late && !P::W_IS_A)) issue<CG>(b, kb, st + A_BYTES, full_bar + 8 * s, leader);
       }
     }
     // the last copies land before this CTA may exit (those of a pair's second CTA are counted by the first, which
@@ -325,8 +332,12 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
     Tile t;
     const bool leader = elect_one();
     const uint32_t smem0 = smem_u32(smem);
-    const uint64_t a_desc = P::adesc(smem0), b_desc = P::bdesc(ar, smem0 + A_BYTES);
+    const uint64_t a_desc = P::adesc(smem0), b_desc = P::bdesc(ar, P::RESIDENT ? smem_u32(resident) : smem0 + A_BYTES);
     const uint64_t a_step = P::a_step(), b_step = P::b_step(ar);  // 32 bytes of K on, in 16-byte units
+    if (P::RESIDENT && !mbar_wait_warp(b_ready, 0, &abort_flag)) {
+      abort_flag = 1;
+      ok = false;
+    }
     for (; ok && P::tile(ar, local, t); ++local) {
       const int buf = local & 1;
       if (local >= 2 && !mbar_wait_warp(&acc_empty[buf], ((local >> 1) - 1) & 1, &abort_flag)) {
@@ -345,7 +356,8 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint64_t off = (uint64_t)((uint32_t)(ring.s * sbytes) >> 4);
-        const uint64_t ad = a_desc + off, bd = b_desc + off;
+        const uint64_t ad = a_desc + off;
+        const uint64_t bd = b_desc + (P::RESIDENT ? (uint64_t)((uint32_t)(kb * ar.c.b_tile * BK) >> 4) : off);
         if (leader) {
           umma<CG>(d_tmem, ad, bd, id, accum);
           umma<CG>(d_tmem, ad + a_step, bd + b_step, id, 1u);
@@ -368,6 +380,14 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
     // ---- epilogue: warp drains TMEM lanes [32 (warp % 4), +32)
     pdl_wait();
     typename P::Epilogue epi(ar, epi_smem, warp & 3, (warp - 2) >> 2, lane);
+    if (P::RESIDENT) {
+      epi.write_b(ar, resident, warp - 2);
+      // written by the generic proxy, read by the tensor core through the async one
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b_ready)) : "memory");
+      mbar_wait_warp(b_ready, 0, &abort_flag);  // every warp's part, as the epilogues read the scales
+    }
     int local = 0;
     Tile t;
     for (; P::tile(ar, local, t); ++local) {
@@ -493,10 +513,10 @@ __device__ __forceinline__ bool row_tile(const RowArgs& r, int w_is_a, int j, Ti
 }
 
 // One K step: whole boxes of A up to the tile's last lane, and B's columns (half of them each in a pair).
-template <int CG>
+template <int CG, bool RESIDENT = false>
 __device__ __forceinline__ uint32_t row_bytes(const RowArgs& r, const Tile& t) {
   int n = mma_n<CG>(t.nb) / CG;
-  n = (n + r.box_b - 1) / r.box_b * r.box_b * CG;
+  n = RESIDENT ? 0 : (n + r.box_b - 1) / r.box_b * r.box_b * CG;
 #pragma unroll
   for (int i = 0; i < CG; ++i) {
     const int na = max(0, min(BM, t.na - i * BM));
@@ -512,6 +532,108 @@ template <int CG>
 __device__ __forceinline__ Boxes row_boxes_b(const RowArgs& r, const CUtensorMap* map, const Tile& t, int rank) {
   const int half = mma_n<CG>(t.nb) / CG;
   return Boxes{map, (half + r.box_b - 1) / r.box_b, r.box_b, r.b_first + t.b0 + rank * half, BK, 0};
+}
+
+// ------------------------------------------------------------------ few tokens, quantized by every CTA
+// B is one to four tokens: every CTA quantizes them itself (as the single-token head does; codes and scales of
+// rows_quant.cu) into the 128-byte swizzled layout the product reads, [K / 128][16 rows][128] bytes, while its first
+// rows of W are on their way.  The epilogue's sixteen warps are split evenly over the tokens and keep their values in
+// registers, which bounds M d.  (With a warp per token for 16 tokens this took longer than a launch: 47 us for 28.)
+constexpr int RES_ROWS = 16, RES_TOKENS = 4, RES_WARPS = 16, RES_CHUNKS = 4;
+inline bool resident_supported(int M, int d) {
+  const int per = M == 1 ? 16 : M == 2 ? 8 : 4;  // warps per token
+  return M <= RES_TOKENS && d <= per * 256 * RES_CHUNKS;
+}
+inline int resident_bytes(int d) { return (d + BK - 1) / BK * RES_ROWS * BK; }
+struct ResidentArgs {
+  const void* x;
+  int x_type;
+  int64_t ldx;
+  int M, d;
+  const float* norm_w;
+  int8_t* dbg_q;  // optional taps, written by the first CTA
+  float* dbg_s;
+};
+struct ResidentScratch {
+  double ss[RES_WARPS];
+  uint32_t m[RES_WARPS];
+  float rn[RES_TOKENS], s[RES_TOKENS];  // s: the tokens' scales
+};
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(RES_WARPS * 32) : "memory"); }
+template <typename T>
+__device__ __forceinline__ void resident_quantize(const ResidentArgs& r, unsigned char* res, ResidentScratch* sc, int w,
+                                                  int lane) {
+  const int per = r.M == 1 ? 16 : r.M == 2 ? 8 : 4, t = w / per, first = t * per;
+  const bool on = t < r.M;
+  const T* x = reinterpret_cast<const T*>(r.x) + (on ? t : 0) * r.ldx;
+  const int i0 = ((w - first) * 32 + lane) * 8, step = per * 256;
+  float v[RES_CHUNKS][8];
+#pragma unroll
+  for (int c = 0; c < RES_CHUNKS; ++c) {
+    if (on && i0 + c * step < r.d) {
+      load8<T>(x + i0 + c * step, v[c]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[c][k] = 0.0f;
+    }
+  }
+  if (r.norm_w) {
+    double ss = 0.0;  // exact squares in fp64
+#pragma unroll
+    for (int c = 0; c < RES_CHUNKS; ++c)
+      if (c * step < r.d) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss = fma((double)v[c][k], (double)v[c][k], ss);
+      }
+    ss = warp_sum(ss);
+    if (lane == 0) sc->ss[w] = ss;
+    epilogue_sync();
+    if (w == first && lane == 0 && on) {
+      ss = 0.0;
+      for (int k = 0; k < per; ++k) ss += sc->ss[first + k];
+      sc->rn[t] = rms_factor(ss, r.d);
+    }
+    epilogue_sync();
+    if (on) {
+      const float rn = sc->rn[t];
+#pragma unroll
+      for (int c = 0; c < RES_CHUNKS; ++c)
+        if (i0 + c * step < r.d) {
+          float nw[8];
+          load8<float>(r.norm_w + i0 + c * step, nw);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[c][k] = norm_value(v[c][k], rn, nw[k]);
+        }
+    }
+  }
+  uint32_t mb = 0u;  // absmax as an unsigned pattern: infinities and NaN order above every finite value
+#pragma unroll
+  for (int c = 0; c < RES_CHUNKS; ++c)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mb = max(mb, __float_as_uint(v[c][k]) & 0x7FFFFFFFu);
+  mb = __reduce_max_sync(0xffffffffu, mb);
+  if (lane == 0) sc->m[w] = mb;
+  epilogue_sync();
+  if (!on) return;
+  mb = 0u;
+  for (int k = 0; k < per; ++k) mb = max(mb, sc->m[first + k]);
+  const bool finite = mb < 0x7F800000u;
+  const float s0 = finite ? quant_scale(__uint_as_float(mb)) : __uint_as_float(0x7FC00000u);
+  const float inv = finite ? quant_inv(s0) : 0.0f;
+  if (w == first && lane == 0) {
+    sc->s[t] = s0;
+    if (r.dbg_s && blockIdx.x == 0) r.dbg_s[t] = s0;
+  }
+#pragma unroll
+  for (int c = 0; c < RES_CHUNKS; ++c) {
+    const int i = i0 + c * step;
+    if (i >= r.d) continue;
+    int cd[8];
+    quant_codes<8>(v[c], s0, inv, cd);
+    const uint2 o = finite ? pack_codes(cd) : make_uint2(0u, 0u);
+    *reinterpret_cast<uint2*>(res + (i >> 7) * (RES_ROWS * BK) + t * BK + ((((i & 127) >> 4) ^ (t & 7)) << 4) + (i & 8)) = o;
+    if (r.dbg_q && blockIdx.x == 0) *reinterpret_cast<uint2*>(r.dbg_q + (size_t)t * r.d + i) = o;
+  }
 }
 
 }  // namespace gemm_i8

@@ -69,7 +69,7 @@ __device__ __forceinline__ uint32_t pick(const uint32_t (&v)[32], int j) {
 template <int CG_>
 struct ForwardPolicy {
   static constexpr int CG = CG_;
-  static constexpr bool W_EARLY = true, W_IS_A = false;
+  static constexpr bool W_EARLY = true, W_IS_A = false, RESIDENT = false;
   static constexpr int EPI_WARPS = 8, EPI_COLS = BN_MAX / 2;  // columns of an epilogue warp
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
@@ -111,6 +111,7 @@ struct ForwardPolicy {
       m = -INFINITY;
       S = 0.0f;
     }
+    __device__ __forceinline__ void write_b(const Args&, unsigned char*, int) {}
     __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
       const int tk = t.a0 + row;
       const int sl = (a.r.mode == kGrid ? t.b0 / a.r.tile_b : (int)blockIdx.x / CG) * 2 + half;
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(256) transpose_kernel(const int8_t* __restrict
 template <int CG_, bool DS>
 struct DigitPolicy {
   static constexpr int CG = CG_;
-  static constexpr bool W_EARLY = true, W_IS_A = false;
+  static constexpr bool W_EARLY = true, W_IS_A = false, RESIDENT = false;
   static constexpr int EPI_WARPS = 8, EPI_COLS = BN_MAX / 2;  // columns of an epilogue warp
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
@@ -428,6 +429,7 @@ struct DigitPolicy {
     __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int half_, int lane_)
         : q(q_), half(half_), lane(lane_), sr(reinterpret_cast<float*>(sm) + (half_ * 4 + q_) * 2 * EPI_COLS),
           cu(sr + EPI_COLS), fp(fixed_point(a.srow)) {}
+    __device__ __forceinline__ void write_b(const Args&, unsigned char*, int) {}
     __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
       const int tk = t.a0 + q * 32 + lane;
       const bool valid = tk < a.M;
@@ -547,7 +549,7 @@ struct DigitPolicy {
 template <int CG_>
 struct GradPolicy {
   static constexpr int CG = CG_;
-  static constexpr bool W_EARLY = false, W_IS_A = true;
+  static constexpr bool W_EARLY = false, W_IS_A = true, RESIDENT = false;
   static constexpr int EPI_WARPS = 8;
   struct Args {
     CUtensorMap map_a, map_b;  // transposed W, digits: blocks of 128 bytes
@@ -609,6 +611,7 @@ struct GradPolicy {
           if (cv && c + j < n) atomicAdd(base + (size_t)(c + j) * a.d, (int)v[j]);
       }
     }
+    __device__ __forceinline__ void write_b(const Args&, unsigned char*, int) {}
     __device__ __forceinline__ void prepare(const Args&, const Tile&) {}
     __device__ __forceinline__ void finish(const Args&) {}
   };
@@ -884,7 +887,7 @@ int row_args(typename P::Args& a, int M, int rows, int first, int d, const int8_
   a.r.box_a = BM;
   a.r.box_b = a.r.mode == kRangeB ? 32 / CG : a.r.tile_b / CG;
   a.c.b_tile = a.r.tile_b / CG;
-  a.c.stages = ring_stages(a.c.b_tile, P::EPI_SMEM);
+  a.c.stages = ring_stages(a.c, P::EPI_SMEM);
   a.c.err = err;
   if (!encode_u8_map_sw128(&a.map_a, q, M, d, a.r.box_a) || !encode_u8_map_sw128(&a.map_b, W, V, d, a.r.box_b))
     return DFSSM_EUNSUPPORTED;
@@ -968,7 +971,7 @@ int piece_products(const Piece& p, cudaStream_t st) {
   using G = GradPolicy<CG>;
   typename G::Args g{};
   g.c.b_tile = p.l.tb;
-  g.c.stages = ring_stages(p.l.tb, 0);
+  g.c.stages = ring_stages(g.c, 0);
   g.c.err = p.err;
   if (!encode_blocks_map(&g.map_a, p.wt, (int64_t)(p.l.dp * p.Vp / 128), BM) ||
       !encode_blocks_map(&g.map_b, p.digits, (int64_t)(3 * plane / 128), p.l.tb))

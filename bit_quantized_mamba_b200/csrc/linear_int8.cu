@@ -1,7 +1,8 @@
 // Many-token int8 linear (include/dfssm.h, dfssm_linear_int8): y[t][v] = fl32(acc[t][v] s[t] s_row[v]), the
 // LM head's arithmetic (technical summary §2.B: int8 LM head with per-row scaling; §2.C: per-token int8
 // activations) for any number of tokens.
-//   1. rows_quant: codes and scale of every token (with the final RMSNorm when a weight is given);
+//   1. rows_quant: codes and scale of every token (with the final RMSNorm when a weight is given); for up to
+//      four tokens every CTA of the product does that itself;
 //   2. the tcgen05 int8 product (gemm_i8.cuh) with the rows of W on the tensor memory's lanes and the tokens on
 //      its columns: a warp's store of one token covers 32 consecutive outputs, and few tokens make a narrow
 //      product (16 columns for one token), so that the stream of W alone bounds it.
@@ -36,16 +37,18 @@ __device__ __forceinline__ void scaled(uint32_t acc0, uint32_t acc1, f2 s, f2 w,
   sure = sure && out0 == hi0 && out1 == hi1 && acc0 + (1u << 24) <= (2u << 24) && acc1 + (1u << 24) <= (2u << 24);
 }
 
-template <typename Y, int CG_>
+template <typename Y, int CG_, bool RESIDENT_ = false>
 struct LinearPolicy {
   static constexpr int CG = CG_;
+  static constexpr bool RESIDENT = RESIDENT_;  // one to four tokens, quantized here
   static constexpr bool W_EARLY = true, W_IS_A = true;
   static constexpr int EPI_WARPS = 16, PARTS = EPI_WARPS / 4, EPI_COLS = BN_MAX / PARTS;  // columns of a warp
   struct Args {
     CUtensorMap map_a, map_b;  // W, codes
     RowArgs r;
     Common c;
-    const double* s_tok;  // [M]
+    ResidentArgs x;       // RESIDENT: the tokens, else
+    const double* s_tok;  // [M] their scales
     const float* s_row;   // [V]
     Y* y;
     int64_t ldy;
@@ -53,7 +56,7 @@ struct LinearPolicy {
     int V;
   };
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 1, j, t); }
-  static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
+  static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG, RESIDENT>(a.r, t); }
   static __device__ __forceinline__ Boxes boxes_a(const Args& a, const Tile& t, int) {
     return row_boxes_a<CG>(a.r, &a.map_a, t);
   }
@@ -64,22 +67,29 @@ struct LinearPolicy {
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t a_step() { return UMMA_K >> 4; }
   static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
-  static constexpr int EPI_SMEM = EPI_WARPS * EPI_COLS * 4;
+  static constexpr int EPI_SMEM = EPI_WARPS * EPI_COLS * 4 + (int)sizeof(ResidentScratch);
+  static_assert(EPI_WARPS == RES_WARPS, "the epilogue's warps quantize");
   struct Epilogue {
+    ResidentScratch* res;  // RESIDENT: holds the tokens' scales
     int part, lane, r;  // r: lane of the tile
     float* s;           // scales of this warp's columns (chunks of 16: part, part + PARTS, ..)
     float sw;
     bool plain;         // the warp's scales are of ordinary size
     __device__ __forceinline__ Epilogue(const Args&, unsigned char* sm, int q, int part_, int lane_)
-        : part(part_), lane(lane_), r(q * 32 + lane_),
+        : res(reinterpret_cast<ResidentScratch*>(sm + EPI_WARPS * EPI_COLS * 4)), part(part_), lane(lane_), r(q * 32 + lane_),
           s(reinterpret_cast<float*>(sm) + (part_ * 4 + q) * EPI_COLS) {}
+    __device__ __forceinline__ void write_b(const Args& a, unsigned char* b, int warp) {
+      if (!RESIDENT) return;
+      if (a.x.x_type == DFSSM_BF16) resident_quantize<__nv_bfloat16>(a.x, b, res, warp, lane);
+      else resident_quantize<float>(a.x, b, res, warp, lane);
+    }
     __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
       sw = r < t.na ? __ldg(a.s_row + t.a0 + r) : 1.0f;
       bool ok = ordinary(sw);
 #pragma unroll
       for (int k = 0; k < EPI_COLS / 32; ++k) {
         const int i = k * 32 + lane, c = ((i >> 4) * PARTS + part) * 16 + (i & 15);
-        const float st = c < t.nb ? (float)a.s_tok[t.b0 + c] : 1.0f;
+        const float st = c < t.nb ? (RESIDENT ? res->s[c] : (float)a.s_tok[t.b0 + c]) : 1.0f;
         s[i] = st;
         ok = ok && (ordinary(st) || st == 0.0f);
       }
@@ -135,10 +145,11 @@ struct LinearPolicy {
 
 inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-template <typename Y, int CG>
-int launch_linear(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, const double* s, int M, Y* y,
-                  int64_t ldy, int32_t* acc, int* err, cudaStream_t st) {
-  using P = LinearPolicy<Y, CG>;
+template <typename Y, int CG, bool RESIDENT>
+int launch_linear(const int8_t* W, const float* s_row, int V, const RowsQuantArgs& qa, void* y, int64_t ldy, int32_t* acc,
+                  int* err, cudaStream_t st) {
+  using P = LinearPolicy<Y, CG, RESIDENT>;
+  const int M = qa.M, d = qa.d;
   typename P::Args a{};
   a.r.rows_a = V;
   a.r.rows_b = M;
@@ -149,33 +160,41 @@ int launch_linear(const int8_t* W, const float* s_row, int V, int d, const int8_
   a.r.mode = range ? kRangeA : kGrid;
   a.r.tile_b = range ? BN_MAX : even_tile((V + BM * CG - 1) / (BM * CG), M, max_groups<P>());
   a.r.box_a = range ? 32 : BM;
-  const int bt = range ? (M + 16 * CG - 1) / (16 * CG) * 16 : a.r.tile_b / CG;  // a CTA's columns
+  const int bt = RESIDENT ? RES_ROWS : range ? (M + 16 * CG - 1) / (16 * CG) * 16 : a.r.tile_b / CG;  // a CTA's columns
   a.r.box_b = bt;
   a.c.b_tile = bt;
-  a.c.stages = ring_stages(bt, P::EPI_SMEM);
+  a.c.resident = RESIDENT ? resident_bytes(d) : 0;
+  a.c.stages = ring_stages(a.c, P::EPI_SMEM);
   a.c.err = err;
-  a.s_tok = s;
+  a.x = ResidentArgs{qa.x, qa.x_type, qa.ldx, M, d, qa.norm_w, qa.dbg_q, qa.dbg_s};
+  a.s_tok = qa.s;
   a.s_row = s_row;
-  a.y = y;
+  a.y = static_cast<Y*>(y);
   a.ldy = ldy;
   a.acc = acc;
   a.V = V;
-  if (!encode_u8_map_sw128(&a.map_a, W, V, d, a.r.box_a) || !encode_u8_map_sw128(&a.map_b, q, M, d, bt))
-    return DFSSM_EUNSUPPORTED;
+  if (!encode_u8_map_sw128(&a.map_a, W, V, d, a.r.box_a)) return DFSSM_EUNSUPPORTED;
+  cudaError_t e = cudaSuccess;
+  if (!RESIDENT) {
+    if (!encode_u8_map_sw128(&a.map_b, qa.q, M, d, bt)) return DFSSM_EUNSUPPORTED;
+    e = launch_rows_quant(qa, st);
+  }
   const long long units = range ? (V + 31) / 32
                                 : (long long)((V + BM * CG - 1) / (BM * CG)) * ((M + a.r.tile_b - 1) / a.r.tile_b);
   const int most = max_groups<P>();
-  const cudaError_t e = launch<P>(a, (int)(units < most ? units : most), P::EPI_SMEM, st);
+  if (e == cudaSuccess) e = launch<P>(a, (int)(units < most ? units : most), P::EPI_SMEM, st);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
 }
 
-// Up to 128 tokens the stream of W bounds the product and single CTAs keep more of it in flight; above, pairs halve
-// the traffic of the tokens' codes.
+// One to four tokens: one kernel does it all; up to 128 the stream of W bounds the product and single CTAs keep more of it
+// in flight; above, pairs halve the traffic of the tokens' codes.
 template <typename Y>
-int launch_linear(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, const double* s, int M, void* y,
-                  int64_t ldy, int32_t* acc, int* err, cudaStream_t st) {
-  const auto f = M <= 128 ? launch_linear<Y, 1> : launch_linear<Y, 2>;
-  return f(W, s_row, V, d, q, s, M, static_cast<Y*>(y), ldy, acc, err, st);
+int launch_linear(const int8_t* W, const float* s_row, int V, const RowsQuantArgs& qa, void* y, int64_t ldy, int32_t* acc,
+                  int* err, cudaStream_t st) {
+  const auto f = resident_supported(qa.M, qa.d) ? launch_linear<Y, 1, true>
+                 : qa.M <= 128                  ? launch_linear<Y, 1, false>
+                                                : launch_linear<Y, 2, false>;
+  return f(W, s_row, V, qa, y, ldy, acc, err, st);
 }
 
 }  // namespace
@@ -218,8 +237,6 @@ extern "C" int dfssm_linear_int8(const int8_t* W, const float* s_row, int V, int
     qa.dbg_q = dbg->xq;
     qa.dbg_s = dbg->xscale;
   }
-  const cudaError_t e = launch_rows_quant(qa, s);
-  if (e != cudaSuccess) return record_cuda_failure(e);
   const auto f = y_type == DFSSM_F32 ? launch_linear<float> : launch_linear<__nv_bfloat16>;
-  return f(W, s_row, V, d, qa.q, qa.s, M, y, ldy, dbg ? dbg->acc : nullptr, reinterpret_cast<int*>(p), s);
+  return f(W, s_row, V, qa, y, ldy, dbg ? dbg->acc : nullptr, reinterpret_cast<int*>(p), s);
 }

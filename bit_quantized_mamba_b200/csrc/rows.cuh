@@ -44,4 +44,15 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const fl
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Eight codes as bytes.
+__device__ __forceinline__ uint2 pack_codes(const int (&cd)[8]) {
+  uint32_t lo = 0u, hi = 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    lo |= ((uint32_t)cd[k] & 0xFFu) << (8 * k);
+    hi |= ((uint32_t)cd[k + 4] & 0xFFu) << (8 * k);
+  }
+  return make_uint2(lo, hi);
+}
+
 }  // namespace dfssm

@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_quant_kernel(RowsQuantArgs a)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ double red_ss[RQ_THREADS / 32];
   __shared__ uint32_t red_m[RQ_THREADS / 32];
+  __shared__ float red_rn;
   const int tok = blockIdx.x;
   const T* xr = reinterpret_cast<const T*>(a.x) + (size_t)tok * a.ldx;
   float v[CH][8];
@@ -46,11 +47,15 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_quant_kernel(RowsQuantArgs a)
     ss = warp_sum(ss);
     if (lane == 0) red_ss[warp] = ss;
     __syncthreads();
-    ss = 0.0;
+    if (threadIdx.x == 0) {  // fp64 division and root once, not in every warp
+      ss = 0.0;
 #pragma unroll
-    for (int w = 0; w < RQ_THREADS / 32; ++w) ss += red_ss[w];
-    const float rn = rms_factor(ss, a.d);
-    if (threadIdx.x == 0 && a.rn) a.rn[tok] = rn;
+      for (int w = 0; w < RQ_THREADS / 32; ++w) ss += red_ss[w];
+      red_rn = rms_factor(ss, a.d);
+      if (a.rn) a.rn[tok] = red_rn;
+    }
+    __syncthreads();
+    const float rn = red_rn;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = (threadIdx.x + RQ_THREADS * c) * 8;
@@ -88,14 +93,7 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_quant_kernel(RowsQuantArgs a)
     if (i >= a.d) continue;
     int cd[8];
     quant_codes<8>(v[c], s0, inv, cd);
-    uint32_t lo = 0u, hi = 0u;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      lo |= ((uint32_t)cd[k] & 0xFFu) << (8 * k);
-      hi |= ((uint32_t)cd[k + 4] & 0xFFu) << (8 * k);
-    }
-    if (!finite) lo = hi = 0u;
-    const uint2 o = make_uint2(lo, hi);
+    const uint2 o = finite ? pack_codes(cd) : make_uint2(0u, 0u);
     *reinterpret_cast<uint2*>(a.q + (size_t)tok * a.d + i) = o;
     if (a.dbg_q) *reinterpret_cast<uint2*>(a.dbg_q + (size_t)tok * a.d + i) = o;
   }
