@@ -9,7 +9,7 @@
 //
 // Forward: the int8 product with tokens on the tensor memory's lanes and rows of W on its columns; a thread
 // owns a token's logits of a tile and folds them into a running (max, sum), one pass, 8 bytes kept per
-// token, tile and column half; a second kernel joins them.
+// token, tile and column half; a second kernel joins them.  (Up to 64 tokens: operands exchanged, one kernel.)
 //
 // Gradient with respect to the (dequantised) normalised token:  du = g [sum_{v != y} p_v s_row_v W_v -
 // (1 - p_y) s_row_y W_y].  The coefficients c_v = exp(l_v - m) s_row_v / max|s_row| lie in [0, 1] (or [-1, 1] with
@@ -196,6 +196,24 @@ struct ForwardPolicy {
   };
 };
 
+// Loss and stats of token t from the other rows' (max, sum); stats[2][t] holds the label's logit if there is one.
+__device__ __forceinline__ void write_loss(int t, float m, double S, int M, int V, const int32_t* labels, float* stats,
+                                           float* loss, int* status) {
+  const int y = labels[t];
+  const bool bad = y >= V;
+  if (bad) atomicExch(status, kBadTokenCode);
+  float out = 0.0f, ly = 0.0f;
+  if (y >= 0 && !bad) {
+    ly = __ldcg(stats + 2 * (size_t)M + t);
+    const double z = S == 0.0 ? -INFINITY : ((double)m + log2(S)) * kLn2 - (double)ly;
+    out = (float)(z > 0.0 ? z + log1p(exp(-z)) : log1p(exp(z)));
+  }
+  stats[t] = m;
+  stats[(size_t)M + t] = (float)S;
+  stats[2 * (size_t)M + t] = ly;
+  loss[t] = out;
+}
+
 // Joins the partial (max, sum) of a token and forms its loss.  32 tokens per CTA, 32 slices of slots; the second
 // pass over a slice comes from L1/L2.
 constexpr int LF_SLICES = 32;
@@ -231,21 +249,151 @@ __global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float
   __syncthreads();
   if (sl != 0 || t >= M) return;
   for (int i = 1; i < LF_SLICES; ++i) S += ss[i][lane];
-  const int y = labels[t];
-  const bool bad = y >= V;
-  if (bad) atomicExch(status, kBadTokenCode);
-  float out = 0.0f;
-  float ly = 0.0f;
-  if (y >= 0 && !bad) {
-    ly = stats[2 * (size_t)M + t];
-    const double z = S == 0.0 ? -INFINITY : ((double)m + log2(S)) * kLn2 - (double)ly;
-    out = (float)(z > 0.0 ? z + log1p(exp(-z)) : log1p(exp(z)));
-  }
-  stats[t] = m;
-  stats[(size_t)M + t] = (float)S;
-  stats[2 * (size_t)M + t] = ly;
-  loss[t] = out;
+  write_loss(t, m, S, M, V, labels, stats, loss, status);
 }
+
+// ------------------------------------------------------------------------------------ forward, few tokens
+
+// Up to 64 tokens: rows of W on the lanes, tokens on the columns (sixteen per epilogue warp), so that W streams through
+// a deep ring of narrow stages.  A thread keeps a running (max, sum) over its rows for every token, lanes and
+// warps are joined at the end, and the last CTA to finish joins the CTAs and writes the losses.
+constexpr int SMALL_TOKENS = 64;
+template <bool RESIDENT_>
+struct SmallForwardPolicy {
+  static constexpr int CG = 1;
+  static constexpr bool RESIDENT = RESIDENT_;
+  static constexpr bool W_EARLY = true, W_IS_A = true;
+  static constexpr int EPI_WARPS = 16;
+  static_assert(EPI_WARPS == RES_WARPS, "the epilogue's warps quantize");
+  struct Args {
+    CUtensorMap map_a, map_b;  // W, codes
+    RowArgs r;
+    Common c;
+    ResidentArgs x;         // RESIDENT: the tokens, else
+    const double* s_tok;    // [M] their scales
+    const float* s_row;     // [V]
+    const int32_t* labels;  // [M]
+    float* stats;           // [3][M]
+    float* loss;            // [M]
+    float2* part;           // [CTAs][M]
+    unsigned* done;         // CTAs finished: zero before and after
+    int M, V;
+  };
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 1, j, t); }
+  static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG, RESIDENT>(a.r, t); }
+  static __device__ __forceinline__ Boxes boxes_a(const Args& a, const Tile& t, int) {
+    return row_boxes_a<CG>(a.r, &a.map_a, t);
+  }
+  static __device__ __forceinline__ Boxes boxes_b(const Args& a, const Tile& t, int rank) {
+    return row_boxes_b<CG>(a.r, &a.map_b, t, rank);
+  }
+  static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_sw128(addr); }
+  static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
+  static __device__ __forceinline__ uint64_t a_step() { return UMMA_K >> 4; }
+  static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
+  struct Scratch {
+    ResidentScratch res;
+    float s[SMALL_TOKENS];
+    int label[SMALL_TOKENS];
+    float2 red[4][SMALL_TOKENS];
+    int last;
+  };
+  static constexpr int EPI_SMEM = (int)((sizeof(Scratch) + 15) & ~size_t(15));
+  struct Epilogue {
+    Scratch* sc;
+    int q, part, lane;
+    float sw;
+    float m[16], S[16];
+    __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int part_, int lane_)
+        : sc(reinterpret_cast<Scratch*>(sm)), q(q_), part(part_), lane(lane_) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        m[j] = -INFINITY;
+        S[j] = 0.0f;
+      }
+      // each warp fills (and reads) its own tokens; the four quadrants write the same values
+      const int t = part * 16 + lane;
+      if (lane < 16) {
+        sc->label[t] = t < a.M ? __ldg(a.labels + t) : -1;
+        if (!RESIDENT) sc->s[t] = t < a.M ? (float)a.s_tok[t] : 0.0f;
+      }
+      __syncwarp();
+    }
+    __device__ __forceinline__ void write_b(const Args& a, unsigned char* b, int warp) {
+      if (!RESIDENT) return;
+      if (a.x.x_type == DFSSM_BF16) resident_quantize<__nv_bfloat16>(a.x, b, &sc->res, warp, lane);
+      else resident_quantize<float>(a.x, b, &sc->res, warp, lane);
+    }
+    __device__ __forceinline__ float scale(int t) const { return RESIDENT ? sc->res.s[t & (RES_TOKENS - 1)] : sc->s[t]; }
+    __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
+      const int r = q * 32 + lane;
+      sw = r < t.na ? scale2(__ldg(a.s_row + t.a0 + r)) : 0.0f;
+    }
+    __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
+      const int r = q * 32 + lane, row = t.a0 + r;
+      if (part * 16 >= a.M) return;
+      uint32_t v[16];
+      tmem_ld16(taddr + (uint32_t)(part * 16), v);
+      tmem_wait(v);
+      if (r >= t.na) return;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int tok = part * 16 + j;
+        if (tok >= a.M) break;
+        const float st = scale(tok), x = (float)(int)v[j] * st;
+        if (row == sc->label[tok]) {  // the label's own logit stays out of the sum
+          a.stats[2 * (size_t)a.M + tok] =
+              __double2float_rn(dmul(dmul(int_to_f64((int)v[j]), (double)st), (double)__ldg(a.s_row + row)));
+        } else {
+          const float mx = fmaxf(m[j], x * sw), mz = mx == -INFINITY ? 0.0f : mx;
+          S[j] = S[j] * ex2(m[j] - mz) + ex2(fmaf(x, sw, -mz));
+          m[j] = mx;
+        }
+      }
+    }
+    __device__ __forceinline__ void finish(const Args& a) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float mx = warp_max(m[j]), mz = mx == -INFINITY ? 0.0f : mx;
+        const float s = warp_sum(S[j] * ex2(m[j] - mz));
+        if (lane == j) sc->red[q][part * 16 + j] = make_float2(mx, s);
+      }
+      epilogue_sync();
+      const int tid = threadIdx.x - 64;
+      if (tid < a.M) {
+        float mx = -INFINITY, s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sc->red[i][tid].x);
+        const float mz = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s += sc->red[i][tid].y * ex2(sc->red[i][tid].x - mz);
+        a.part[(size_t)blockIdx.x * a.M + tid] = make_float2(mx, s);
+      }
+      epilogue_sync();
+      if (tid == 0) {
+        __threadfence();
+        sc->last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+        __threadfence();
+      }
+      epilogue_sync();
+      if (!sc->last) return;
+      if (tid == 0) *a.done = 0u;
+      for (int t = tid >> 5; t < a.M; t += EPI_WARPS) {
+        float mx = -INFINITY;
+        for (int i = lane; i < (int)gridDim.x; i += 32) mx = fmaxf(mx, __ldcg(&a.part[(size_t)i * a.M + t].x));
+        mx = warp_max(mx);
+        const float mz = mx == -INFINITY ? 0.0f : mx;
+        double s = 0.0;
+        for (int i = lane; i < (int)gridDim.x; i += 32) {
+          const float2 p = __ldcg(a.part + (size_t)i * a.M + t);
+          s += (double)(p.y * ex2(p.x - mz));
+        }
+        s = warp_sum(s);
+        if (lane == 0) write_loss(t, mx, s, a.M, a.V, a.labels, a.stats, a.loss, a.c.err);
+      }
+    }
+  };
+};
 
 // ------------------------------------------------------------------------------------ gradient
 
@@ -901,14 +1049,52 @@ int row_groups(const RowArgs& r) {
   return (int)(units < most ? units : most);
 }
 
-template <int CG>
-int forward(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, const double* s, int M,
-            const int32_t* labels, float* loss, float* stats, float2* part, int* err, cudaStream_t st) {
-  using P = ForwardPolicy<CG>;
+template <bool RESIDENT>
+int forward_small(const int8_t* W, const float* s_row, int V, const RowsQuantArgs& qa, const int32_t* labels, float* loss,
+                  float* stats, float2* part, int* err, cudaStream_t st) {
+  using P = SmallForwardPolicy<RESIDENT>;
+  const int M = qa.M, d = qa.d;
   typename P::Args a{};
-  const int rc = row_args<P>(a, M, V, 0, d, W, V, q, err);
+  a.r.mode = kRangeA;
+  a.r.rows_a = V;
+  a.r.rows_b = M;
+  a.r.tile_b = BN_MAX;
+  a.r.kblocks = ceil_div(d, BK);
+  a.r.box_a = 32;
+  a.r.box_b = a.c.b_tile = RESIDENT ? RES_ROWS : (M + 15) & ~15;
+  a.c.resident = RESIDENT ? resident_bytes(d) : 0;
+  a.c.stages = ring_stages(a.c, P::EPI_SMEM);
+  a.c.err = err;
+  a.x = ResidentArgs{qa.x, qa.x_type, qa.ldx, M, d, qa.norm_w, nullptr, nullptr};
+  a.s_tok = qa.s;
+  a.s_row = s_row;
+  a.labels = labels;
+  a.stats = stats;
+  a.loss = loss;
+  a.part = part;
+  a.done = reinterpret_cast<unsigned*>(err) + 16;  // beside the status word
+  a.M = M;
+  a.V = V;
+  if (!encode_u8_map_sw128(&a.map_a, W, V, d, a.r.box_a)) return DFSSM_EUNSUPPORTED;
+  cudaError_t e = cudaSuccess;
+  if (!RESIDENT) {
+    if (!encode_u8_map_sw128(&a.map_b, qa.q, M, d, a.r.box_b)) return DFSSM_EUNSUPPORTED;
+    e = launch_rows_quant(qa, st);
+  }
+  const int most = max_groups<P>() < kMaxRangeCtas ? max_groups<P>() : kMaxRangeCtas, units = ceil_div(V, 32);
+  if (e == cudaSuccess) e = launch<P>(a, units < most ? units : most, P::EPI_SMEM, st);
+  return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
+}
+
+template <int CG>
+int forward(const int8_t* W, const float* s_row, int V, const RowsQuantArgs& qa, const int32_t* labels, float* loss,
+            float* stats, float2* part, int* err, cudaStream_t st) {
+  using P = ForwardPolicy<CG>;
+  const int M = qa.M, d = qa.d;
+  typename P::Args a{};
+  const int rc = row_args<P>(a, M, V, 0, d, W, V, qa.q, err);
   if (rc) return rc;
-  a.s_tok = s;
+  a.s_tok = qa.s;
   a.s_row = s_row;
   a.labels = labels;
   a.label_logit = stats + 2 * (size_t)M;
@@ -916,7 +1102,8 @@ int forward(const int8_t* W, const float* s_row, int V, int d, const int8_t* q, 
   a.M = M;
   a.V = V;
   const int groups = row_groups<P>(a.r);
-  cudaError_t e = launch<P>(a, groups, P::EPI_SMEM, st);
+  cudaError_t e = launch_rows_quant(qa, st);
+  if (e == cudaSuccess) e = launch<P>(a, groups, P::EPI_SMEM, st);
   const int slots = 2 * (a.r.mode == kGrid ? ceil_div(V, a.r.tile_b) : groups);
   if (e == cudaSuccess)
     e = launch_pdl(loss_finish_kernel, dim3(ceil_div(M, 32)), dim3(32 * LF_SLICES), 0, st, (const float2*)part, slots, M, V,
@@ -1037,11 +1224,11 @@ extern "C" int dfssm_head_loss(const int8_t* W, const float* s_row, int V, int d
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(workspace);
   const RowsQuantArgs qa = quant_args(x, x_type, ldx, M, d, norm_w, base, w.q, w.s);
-  const cudaError_t e = launch_rows_quant(qa, s);
-  if (e != cudaSuccess) return record_cuda_failure(e);
-  const auto f = layout(M, d).cg == 1 ? forward<1> : forward<2>;
-  return f(W, s_row, V, d, qa.q, qa.s, M, labels, loss, stats, reinterpret_cast<float2*>(base + w.part),
-           reinterpret_cast<int*>(base), s);
+  const auto f = resident_supported(M, d)  ? forward_small<true>
+                 : M <= SMALL_TOKENS       ? forward_small<false>
+                 : layout(M, d).cg == 1    ? forward<1>
+                                           : forward<2>;
+  return f(W, s_row, V, qa, labels, loss, stats, reinterpret_cast<float2*>(base + w.part), reinterpret_cast<int*>(base), s);
 }
 
 extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int V, int d, const void* x,
