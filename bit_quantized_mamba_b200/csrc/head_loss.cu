@@ -18,7 +18,8 @@
 // be above it (they sum to at most S), whose further bits go into a list.  The sum over v is then three exact
 // int8 products of digits with W, each at twice the rate of a bf16 product, free of bf16's rounding and of any
 // order of summation, and a few listed rows of W.  The vocabulary is taken in pieces whose digits stay in L2:
-//   1. transpose: the piece's W as K-major operand of the second product, and W's column sums;
+//   1. transpose: the piece's W as K-major operand of the second product, and W's column sums (with the first piece,
+//      the tokens' factors);
 //   2. the first product again, its epilogue turning logits into digits (and the row scales' gradient
 //      into partial column sums);
 //   3. the second product: digits x transposed W, added to int32 accumulators in memory by integer
@@ -196,26 +197,28 @@ struct ForwardPolicy {
   };
 };
 
-// Loss and stats of token t from the other rows' (max, sum); stats[2][t] holds the label's logit if there is one.
+// Loss and stats of token t from the other rows' (max, sum); stats[2][t] holds the label's logit if there is one, and
+// 1 - p_y afterwards.  z is a difference of logits and wants fp64; exp z and what follows keep fp32's relative
+// precision without.
 __device__ __forceinline__ void write_loss(int t, float m, double S, int M, int V, const int32_t* labels, float* stats,
                                            float* loss, int* status) {
   const int y = labels[t];
   const bool bad = y >= V;
   if (bad) atomicExch(status, kBadTokenCode);
-  float out = 0.0f, ly = 0.0f;
-  if (y >= 0 && !bad) {
-    ly = __ldcg(stats + 2 * (size_t)M + t);
-    const double z = S == 0.0 ? -INFINITY : ((double)m + log2(S)) * kLn2 - (double)ly;
-    out = (float)(z > 0.0 ? z + log1p(exp(-z)) : log1p(exp(z)));
+  float out = 0.0f, rest = 0.0f;
+  if (y >= 0 && !bad && S != 0.0) {
+    const double z = ((double)m + log2(S)) * kLn2 - (double)__ldcg(stats + 2 * (size_t)M + t);
+    const float e = expf(-fabsf((float)z));  // below 1
+    rest = z > 0.0 ? 1.0f / (1.0f + e) : e / (1.0f + e);
+    out = z > 0.0 ? (float)(z + (double)log1pf(e)) : log1pf(e);
   }
   stats[t] = m;
   stats[(size_t)M + t] = (float)S;
-  stats[2 * (size_t)M + t] = ly;
+  stats[2 * (size_t)M + t] = rest;
   loss[t] = out;
 }
 
-// Joins the partial (max, sum) of a token and forms its loss.  32 tokens per CTA, 32 slices of slots; the second
-// pass over a slice comes from L1/L2.
+// Joins the partial (max, sum) of a token and forms its loss.  32 tokens per CTA, 32 slices of slots.
 constexpr int LF_SLICES = 32;
 __global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float2* __restrict__ part, int slots, int M,
                                                                      int V, const int32_t* __restrict__ labels,
@@ -223,33 +226,35 @@ __global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float
                                                                      float* __restrict__ loss, int* status) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ float sm[LF_SLICES][32];
-  __shared__ double ss[LF_SLICES][32];
+  __shared__ float2 sm[LF_SLICES][33];
   const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
   const int t = blockIdx.x * 32 + lane;
-  float m = -INFINITY;
-  if (t < M) {
-#pragma unroll 8
-    for (int s = sl; s < slots; s += LF_SLICES) m = fmaxf(m, part[(size_t)s * M + t].x);
-  }
-  sm[sl][lane] = m;
-  __syncthreads();
+  float m = -INFINITY, S = 0.0f;
+  constexpr int U = 8;  // slots in flight
+  for (int s0 = sl; s0 < slots; s0 += U * LF_SLICES) {
+    float2 p[U];
 #pragma unroll
-  for (int i = 0; i < LF_SLICES; ++i) m = fmaxf(m, sm[i][lane]);
-  const float mz = m == -INFINITY ? 0.0f : m;
-  double S = 0.0;
-  if (t < M) {
-#pragma unroll 8
-    for (int s = sl; s < slots; s += LF_SLICES) {
-      const float2 p = part[(size_t)s * M + t];
-      S += (double)(p.y * ex2(p.x - mz));  // an empty part is (-inf, 0); a NaN sum stays one
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + u * LF_SLICES;
+      p[u] = t < M && s < slots ? part[(size_t)s * M + t] : make_float2(-INFINITY, 0.0f);
     }
+    float mx = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mx = fmaxf(mx, p[u].x);
+    const float mz = mx == -INFINITY ? 0.0f : mx;
+    S *= ex2(m - mz);
+#pragma unroll
+    for (int u = 0; u < U; ++u) S += p[u].y * ex2(p[u].x - mz);  // an empty part is (-inf, 0); a NaN sum stays one
+    m = mx;
   }
-  ss[sl][lane] = S;
+  sm[sl][lane] = make_float2(m, S);
   __syncthreads();
-  if (sl != 0 || t >= M) return;
-  for (int i = 1; i < LF_SLICES; ++i) S += ss[i][lane];
-  write_loss(t, m, S, M, V, labels, stats, loss, status);
+  // warp sl joins token sl: lane i holds slice i
+  const float2 p = sm[lane][sl];
+  const float mx = warp_max(p.x), mz = mx == -INFINITY ? 0.0f : mx;
+  const double sum = warp_sum((double)(p.y * ex2(p.x - mz)));
+  const int tok = blockIdx.x * 32 + sl;
+  if (lane == 0 && tok < M) write_loss(tok, mx, sum, M, V, labels, stats, loss, status);
 }
 
 // ------------------------------------------------------------------------------------ forward, few tokens
@@ -406,17 +411,21 @@ struct TokenFactors {
   double2* fac;   // [M] {f, w_y}
   uint32_t* srow; // {bits of max |s_row|, any negative}: zero before the launch
 };
-__global__ void __launch_bounds__(256) grad_prepare_kernel(const float* __restrict__ stats,
-                                                           const int32_t* __restrict__ labels,
-                                                           const float* __restrict__ dloss,
-                                                           const double* __restrict__ s_tok, int M, int V,
-                                                           const float* __restrict__ s_row, TokenFactors o) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int i = blockIdx.x * 256 + threadIdx.x, n = gridDim.x * 256;
+struct PrepareArgs {
+  const float* stats;
+  const int32_t* labels;
+  const float* dloss;
+  const double* s_tok;
+  const float* s_row;
+  int M, V;
+  TokenFactors out;
+};
+__device__ __forceinline__ void grad_prepare(const PrepareArgs& a, int i, int n) {
+  const TokenFactors& o = a.out;
   uint32_t mb = 0u, neg = 0u;
-  for (int v = i; v < V; v += n) {
-    const float s = __ldg(s_row + v);
+#pragma unroll 4
+  for (int v = i; v < a.V; v += n) {
+    const float s = __ldg(a.s_row + v);
     mb = max(mb, __float_as_uint(s) & 0x7FFFFFFFu);  // orders like |s|, a NaN above all
     neg |= s < 0.0f ? 1u : 0u;
   }
@@ -426,27 +435,25 @@ __global__ void __launch_bounds__(256) grad_prepare_kernel(const float* __restri
     if (mb) atomicMax(o.srow, mb);
     if (neg) atomicOr(o.srow + 1, 1u);
   }
-  for (int t = i; t < M; t += n) {
-    const int y = labels[t];
-    float m = stats[t];
-    const double S = (double)stats[(size_t)M + t];
-    const double ly = (double)stats[2 * (size_t)M + t];
+  for (int t = i; t < a.M; t += n) {
+    const int y = a.labels[t];
+    float m = a.stats[t];
+    const float S = a.stats[(size_t)a.M + t];
+    const double rest = (double)a.stats[2 * (size_t)a.M + t];  // 1 - p_y
     double f = 0.0, wy = 0.0;
     int k = 0;
-    if (y >= 0 && y < V && S != 0.0) {
-      const double g = (double)dloss[t];
-      const double z = ((double)m + log2(S)) * kLn2 - ly;
-      const double rest = 1.0 / (1.0 + exp(-z));  // 1 - p_y
-      f = g * rest / S;
+    if (y >= 0 && y < a.V && S != 0.0f) {
+      const double g = (double)a.dloss[t];
+      f = g * rest / (double)S;
       wy = -g * rest;
-      while (k < 4 && S * (double)(2 << k) <= (double)kListed) ++k;  // S 2^k <= 16
+      while (k < 4 && S * (float)(2 << k) <= (float)kListed) ++k;  // S 2^k <= 16
       const float mk = m - (float)k;
       f *= exp2((double)mk - (double)m);
       m = mk;
     }
     if (m == -INFINITY) m = 0.0f;  // no other row
     o.shift[t] = k;
-    const double s = s_tok[t];
+    const double s = a.s_tok[t];
     // a token without a gradient (ignored, or dloss 0) has none whatever its values are
     o.tok[t] = f == 0.0 && wy == 0.0 ? make_float4(0.f, 0.f, 0.f, 0.f)
                                      : make_float4(m, (float)s, (float)(f * s), (float)(wy * s));
@@ -485,10 +492,17 @@ __device__ __forceinline__ float dither(uint32_t acc) {
 // W's piece [nv rows from v0] as K-major operand of the second product, [d / 128][Vp / 16][128][16] bytes
 // (zero past the vocabulary and past d), and the column sums of W.  A thread turns 16 rows x 4 columns.
 constexpr int TR_ROWS = 16 * 2;  // vocabulary rows per warp
+// The first piece's launch has `prepare` more CTAs (in x, of its first row in y) for the tokens' factors.
 __global__ void __launch_bounds__(256) transpose_kernel(const int8_t* __restrict__ W, int V, int d, int v0, int Vp,
-                                                        int8_t* __restrict__ wt, int32_t* __restrict__ colsum) {
+                                                        int8_t* __restrict__ wt, int32_t* __restrict__ colsum,
+                                                        int prepare, const PrepareArgs pa) {
   pdl_launch_dependents();
   pdl_wait();
+  const int blocks = gridDim.x - prepare;
+  if ((int)blockIdx.x >= blocks) {
+    if (blockIdx.y == 0) grad_prepare(pa, (blockIdx.x - blocks) * 256 + threadIdx.x, prepare * 256);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int db = blockIdx.y, col = db * 128 + 4 * lane;
   const int chunk0 = (blockIdx.x * 8 + warp) * (TR_ROWS / 16);
@@ -698,13 +712,16 @@ template <int CG_>
 struct GradPolicy {
   static constexpr int CG = CG_;
   static constexpr bool W_EARLY = false, W_IS_A = true, RESIDENT = false;
-  static constexpr int EPI_WARPS = 8;
+  static constexpr int EPI_WARPS = 8, EPI_SMEM = 8 * 32 * 8;
   struct Args {
     CUtensorMap map_a, map_b;  // transposed W, digits: blocks of 128 bytes
     Common c;
     int32_t* acc;  // this piece's set: [3][M][d]
     size_t plane;
     int M, d, Vp, tb, kblocks;
+    const float* colpart;  // [M / 32][Vp] partial sums of the row scales' gradient, or NULL
+    float* ds;             // [nv]
+    int nv;
   };
   static __host__ __device__ __forceinline__ long long steps(const Args& a) {
     const int nd = (a.d + BM * CG - 1) / (BM * CG), nt = (a.M + a.tb * CG - 1) / (a.tb * CG);
@@ -744,8 +761,29 @@ struct GradPolicy {
   static __device__ __forceinline__ uint64_t b_step(const Args& a) { return (uint64_t)(2 * a.tb); }
   struct Epilogue {
     int q, half, lane;
-    __device__ __forceinline__ Epilogue(const Args&, unsigned char*, int q_, int half_, int lane_)
-        : q(q_), half(half_), lane(lane_) {}
+    // While the first products accumulate: the piece's part of ds_row, 32 rows of W per CTA at a time, the partial
+    // sums of every 32 tokens in eight slices (one per warp) that are joined in order.
+    __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int half_, int lane_)
+        : q(q_), half(half_), lane(lane_) {
+      if (!a.colpart) return;
+      double* red = reinterpret_cast<double*>(sm);  // [8][32]
+      const int sl = half * 4 + q, parts = (a.M + 31) / 32;
+      for (int b = blockIdx.x * 32; b < a.nv; b += gridDim.x * 32) {
+        const int v = b + lane;
+        double s = 0.0;
+        if (v < a.nv) {
+#pragma unroll 8
+          for (int p = sl; p < parts; p += 8) s += (double)a.colpart[(size_t)p * a.Vp + v];
+        }
+        red[sl * 32 + lane] = s;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (sl == 0 && v < a.nv) {
+          for (int k = 1; k < 8; ++k) s += red[k * 32 + lane];
+          a.ds[v] = (float)s;
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      }
+    }
     __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
       const int col = t.a0 + q * 32 + lane, n = min(t.nb, a.M - t.b0);
       const bool cv = col < a.d;
@@ -764,26 +802,6 @@ struct GradPolicy {
     __device__ __forceinline__ void finish(const Args&) {}
   };
 };
-
-// ds_row of a piece: the partial column sums of every 32 tokens, eight slices of them, joined in order.
-__global__ void __launch_bounds__(256) ds_finish_kernel(const float* __restrict__ colpart, int parts, int Vp, int nv,
-                                                        float* __restrict__ ds) {
-  pdl_launch_dependents();
-  pdl_wait();
-  __shared__ double red[8][32];
-  const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5, v = blockIdx.x * 32 + lane;
-  double s = 0.0;
-  if (v < nv) {
-#pragma unroll 8
-    for (int p = sl; p < parts; p += 8) s += (double)colpart[(size_t)p * Vp + v];
-  }
-  red[sl][lane] = s;
-  __syncthreads();
-  if (sl == 0 && v < nv) {
-    for (int k = 1; k < 8; ++k) s += red[k][lane];
-    ds[v] = (float)s;
-  }
-}
 
 struct GradFinishArgs {
   const int32_t* acc;     // [sets][3][M][d]
@@ -904,23 +922,23 @@ __global__ void __launch_bounds__(256) grad_finish_kernel(GradFinishArgs a) {
   }
 }
 
-__global__ void __launch_bounds__(256) dnorm_finish_kernel(const float* __restrict__ npart, int parts, int d,
-                                                           float* __restrict__ dn) {
+// 32 columns per CTA, 32 slices of the partial sums, joined in order.
+__global__ void __launch_bounds__(1024) dnorm_finish_kernel(const float* __restrict__ npart, int parts, int d,
+                                                            float* __restrict__ dn) {
   pdl_launch_dependents();
   pdl_wait();
-  // 32 columns per CTA, eight slices of the partial sums, joined in order
-  __shared__ double red[8][32];
+  __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
-  double s = 0.0;
-  if (i < d)
+  float s = 0.0f;
+  if (i < d) {
 #pragma unroll 8
-    for (int p = sl; p < parts; p += 8) s += (double)npart[(size_t)p * d + i];
+    for (int p = sl; p < parts; p += 32) s += npart[(size_t)p * d + i];
+  }
   red[sl][lane] = s;
   __syncthreads();
-  if (sl == 0 && i < d) {
-    for (int k = 1; k < 8; ++k) s += red[k][lane];
-    dn[i] = (float)s;
-  }
+  const double sum = warp_sum((double)red[lane][sl]);  // warp sl joins column sl
+  const int c = blockIdx.x * 32 + sl;
+  if (lane == 0 && c < d) dn[c] = (float)sum;
 }
 
 // ------------------------------------------------------------------------------------ host side
@@ -991,7 +1009,7 @@ Pieces pieces(int M, int d, int V) {
   p.sets = ceil_div(p.n, p.per_set);
   return p;
 }
-constexpr int kNormParts = 2 * kSms;
+constexpr int kNormParts = 4 * kSms;
 
 struct BackwardWs {
   size_t q, s, rn, tok, fac, shift, list, zero, srow, listed, colsum, acc, zero_end, digits, wt, colpart, npart, total;
@@ -1151,14 +1169,11 @@ int piece_products(const Piece& p, cudaStream_t st) {
   a.tb = p.l.tb;
   a.plane = plane;
   cudaError_t e = launch<P>(a, row_groups<P>(a.r), P::EPI_SMEM, st);
-  if (DS && e == cudaSuccess)
-    e = launch_pdl(ds_finish_kernel, dim3(ceil_div(p.nv, 32)), dim3(256), 0, st, (const float*)p.colpart,
-                   ceil_div(p.M, 32), p.Vp, p.nv, p.ds_row + p.v0);
   if (e != cudaSuccess) return record_cuda_failure(e);
   using G = GradPolicy<CG>;
   typename G::Args g{};
   g.c.b_tile = p.l.tb;
-  g.c.stages = ring_stages(g.c, 0);
+  g.c.stages = ring_stages(g.c, G::EPI_SMEM);
   g.c.err = p.err;
   if (!encode_blocks_map(&g.map_a, p.wt, (int64_t)(p.l.dp * p.Vp / 128), BM) ||
       !encode_blocks_map(&g.map_b, p.digits, (int64_t)(3 * plane / 128), p.l.tb))
@@ -1170,9 +1185,12 @@ int piece_products(const Piece& p, cudaStream_t st) {
   g.Vp = p.Vp;
   g.tb = p.l.tb;
   g.kblocks = ceil_div(p.nv, BK);
+  g.colpart = DS ? p.colpart : nullptr;
+  g.ds = DS ? p.ds_row + p.v0 : nullptr;
+  g.nv = p.nv;
   const long long steps = G::steps(g);
   const int most = max_groups<G>();
-  e = launch<G>(g, (int)(steps < most ? steps : most), 0, st);
+  e = launch<G>(g, (int)(steps < most ? steps : most), G::EPI_SMEM, st);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
 }
 
@@ -1269,12 +1287,9 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   e = launch_rows_quant(qa, s);
   if (e != cudaSuccess) return record_cuda_failure(e);
   TokenFactors tf{reinterpret_cast<float4*>(base + w.tok), reinterpret_cast<int*>(base + w.shift),
-                  reinterpret_cast<double2*>(base + w.fac),
-                  reinterpret_cast<uint32_t*>(base + w.srow)};
-  const int work = M > V / 4 ? M : V / 4;
-  e = launch_pdl(grad_prepare_kernel, dim3(ceil_div(work, 256) < kSms ? ceil_div(work, 256) : kSms), dim3(256), 0, s,
-                 stats, labels, dloss, (const double*)qa.s, M, V, s_row, tf);
-  if (e != cudaSuccess) return record_cuda_failure(e);
+                  reinterpret_cast<double2*>(base + w.fac), reinterpret_cast<uint32_t*>(base + w.srow)};
+  const PrepareArgs pa{stats, labels, dloss, qa.s, s_row, M, V, tf};
+  const int work = ceil_div(M > V ? M : V, 256);
 
   const Pieces pc = pieces(M, d, V);
   int32_t* colsum = reinterpret_cast<int32_t*>(base + w.colsum);
@@ -1303,8 +1318,9 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
     p.v0 = i * pc.rows;
     p.nv = V - p.v0 < pc.rows ? V - p.v0 : pc.rows;
     p.acc = acc + (size_t)(i / pc.per_set) * 3 * M * d;
-    e = launch_pdl(transpose_kernel, dim3(ceil_div(ceil_div(p.nv, BK) * BK, TR_ROWS * 8), (int)(p.l.dp / 128)),
-                   dim3(256), 0, s, W, V, d, p.v0, pc.rows, p.wt, colsum);
+    const int prepare = i > 0 ? 0 : work < kSms ? work : kSms;
+    e = launch_pdl(transpose_kernel, dim3(ceil_div(ceil_div(p.nv, BK) * BK, TR_ROWS * 8) + prepare, (int)(p.l.dp / 128)),
+                   dim3(256), 0, s, W, V, d, p.v0, pc.rows, p.wt, colsum, prepare, pa);
     if (e != cudaSuccess) return record_cuda_failure(e);
     st = products(p, s);
     if (st) return st;
@@ -1333,7 +1349,7 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   const int parts = M < kNormParts ? M : kNormParts;
   e = x_type == DFSSM_BF16 ? launch_grad_finish<__nv_bfloat16>(fa, parts, s) : launch_grad_finish<float>(fa, parts, s);
   if (e == cudaSuccess && dnorm_w)
-    e = launch_pdl(dnorm_finish_kernel, dim3(ceil_div(d, 32)), dim3(256), 0, s, (const float*)fa.npart, parts, d,
+    e = launch_pdl(dnorm_finish_kernel, dim3(ceil_div(d, 32)), dim3(1024), 0, s, (const float*)fa.npart, parts, d,
                    dnorm_w);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
 }
