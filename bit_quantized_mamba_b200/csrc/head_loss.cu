@@ -37,7 +37,8 @@ using namespace gemm_i8;
 
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr double kLn2 = 0.69314718055994530942;
-constexpr int kMaxRangeCtas = 160;  // partial slots are sized without asking the device
+constexpr int kMaxRangeCtas = 160;  // workspaces are sized without asking the device:
+constexpr int kSms = 148;           // the streaming multiprocessors of a B200
 
 inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -947,19 +948,6 @@ __global__ void __launch_bounds__(1024) dnorm_finish_kernel(const float* __restr
 struct ForwardWs {
   size_t q, s, part, total;
 };
-int forward_slots(int V) {
-  const int grid = ceil_div(V, BN_MAX / 2), range = ceil_div(V, 32) < kMaxRangeCtas ? ceil_div(V, 32) : kMaxRangeCtas;
-  return 2 * (grid > range ? grid : range);
-}
-ForwardWs forward_ws(int M, int d, int V) {
-  ForwardWs w;
-  w.q = kStatusBytes;
-  w.s = w.q + al256((size_t)M * d);
-  w.part = w.s + al256(sizeof(double) * (size_t)M);
-  w.total = w.part + al256(sizeof(float2) * (size_t)forward_slots(V) * M);
-  return w;
-}
-
 // How tokens and columns are tiled: up to 128 tokens by single CTAs (the stream of W bounds the products), above
 // by pairs.
 struct Layout {
@@ -976,13 +964,26 @@ Layout layout(int M, int d) {
   return l;
 }
 
+int forward_slots(int M, int d, int V) {
+  const int cg = layout(M, d).cg, rows = ceil_div(M, BM * cg);
+  const int grid = ceil_div(V, even_tile(rows, V, kSms / cg)), range = ceil_div(V, 32) < kMaxRangeCtas ? ceil_div(V, 32) : kMaxRangeCtas;
+  return 2 * (M > BM * cg ? grid : range);
+}
+ForwardWs forward_ws(int M, int d, int V) {
+  ForwardWs w;
+  w.q = kStatusBytes;
+  w.s = w.q + al256((size_t)M * d);
+  w.part = w.s + al256(sizeof(double) * (size_t)M);
+  w.total = w.part + al256(sizeof(float2) * (size_t)forward_slots(M, d, V) * M);
+  return w;
+}
+
 // The vocabulary's pieces: rows per piece (a multiple of 256), and how many accumulator sets keep the int32 sums
 // in range (|digit| <= 128, |W| <= 128: 2^14 rows-worth per row, so at most 131071 rows a set).
 struct Pieces {
   int rows, n, per_set, sets;
 };
 constexpr size_t kPieceBytes = 80u << 20;  // digits and transposed W of a piece: they stay in the 126 MB L2
-constexpr int kSms = 148;
 Pieces pieces(int M, int d, int V) {
   const Layout l = layout(M, d);
   size_t t = kPieceBytes / (3 * l.mp + l.dp + l.mp / 8) / BN_MAX;  // tiles of 256 rows
@@ -1049,7 +1050,7 @@ int row_args(typename P::Args& a, int M, int rows, int first, int d, const int8_
   a.r.b_first = first;
   a.r.kblocks = ceil_div(d, BK);
   a.r.mode = M <= BM * CG ? kRangeB : kGrid;
-  a.r.tile_b = a.r.mode == kRangeB ? BN_MAX : even_tile(ceil_div(M, BM * CG), rows, max_groups<P>());
+  a.r.tile_b = a.r.mode == kRangeB ? BN_MAX : even_tile(ceil_div(M, BM * CG), rows, kSms / CG);
   a.r.box_a = BM;
   a.r.box_b = a.r.mode == kRangeB ? 32 / CG : a.r.tile_b / CG;
   a.c.b_tile = a.r.tile_b / CG;

@@ -18,23 +18,25 @@ namespace {
 
 using namespace gemm_i8;
 
-// fl32(acc s w) of the definition, its fp64 product rounded once, in fp32: with x = acc exact (|acc| <= 2^24), p = fl(x s)
+// fl32(acc s w) of the definition, its fp64 product rounded once, in fp32: with x = acc exact (|acc| < 2^24), p = fl(x s)
 // and e = x s - p, the product is y + r, y = fl(p w), r = (p w - y) + e w, where r alone is rounded, by less than
 // 2^-47 |y|.  Where y + r rounds the same with r moved by 2^-46 |y| either way, that is the definition's value;
 // otherwise (about one in 2^20) `sure` is cleared and the caller takes fp64.  (In fp64 throughout, the fp64 and
 // conversion units bound the product: 2048 x 50288 x 2048 took 215 us of 133 us without an epilogue.)
 // s and w in [2^-40, 2^40] (ordinary) keep every term normal; s = 0 gives acc = 0.
 __device__ __forceinline__ bool ordinary(float s) { return fabsf(s) >= 0x1p-40f && fabsf(s) <= 0x1p40f; }
-__device__ __forceinline__ void scaled(uint32_t acc0, uint32_t acc1, f2 s, f2 w, bool& sure, float& out0, float& out1) {
-  const f2 x = pack2((float)(int)acc0, (float)(int)acc1);
-  const f2 p = mul2(x, s), e = fma2(x, s, neg2(p));
-  const f2 y = mul2(p, w), r = fma2(e, w, fma2(p, w, neg2(y)));
-  const f2 d = abs2(y), t = pack2(0x1p-46f, 0x1p-46f);
-  const f2 lo = add2(y, fma2(neg2(d), t, r)), hi = add2(y, fma2(d, t, r));
+// Two at once; ns = -s and nw = -w spare the negations.
+__device__ __forceinline__ void scaled(uint32_t acc0, uint32_t acc1, f2 s, f2 ns, f2 w, f2 nw, bool& sure, float& out0,
+                                       float& out1) {
+  const float x0 = (float)(int)acc0, x1 = (float)(int)acc1;
+  const f2 x = pack2(x0, x1), t = pack2(0x1p-46f, 0x1p-46f), nt = pack2(-0x1p-46f, -0x1p-46f);
+  const f2 np = mul2(x, ns), e = fma2(x, s, np);
+  const f2 y = mul2(np, nw), r = fma2(e, w, fma2(np, nw, mul2(np, w)));
+  const f2 lo = add2(y, fma2(y, nt, r)), hi = add2(y, fma2(y, t, r));
   float hi0, hi1;
   unpack2(lo, out0, out1);
   unpack2(hi, hi0, hi1);
-  sure = sure && out0 == hi0 && out1 == hi1 && acc0 + (1u << 24) <= (2u << 24) && acc1 + (1u << 24) <= (2u << 24);
+  sure = sure && out0 == hi0 && out1 == hi1 && fabsf(x0) < 0x1p24f && fabsf(x1) < 0x1p24f;
 }
 
 template <typename Y, int CG_, bool RESIDENT_ = false>
@@ -67,17 +69,17 @@ struct LinearPolicy {
   static __device__ __forceinline__ uint64_t bdesc(const Args&, uint32_t addr) { return umma_desc_k_sw128(addr); }
   static __device__ __forceinline__ uint64_t a_step() { return UMMA_K >> 4; }
   static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
-  static constexpr int EPI_SMEM = EPI_WARPS * EPI_COLS * 4 + (int)sizeof(ResidentScratch);
+  static constexpr int EPI_SMEM = EPI_WARPS * EPI_COLS * 8 + (int)sizeof(ResidentScratch);
   static_assert(EPI_WARPS == RES_WARPS, "the epilogue's warps quantize");
   struct Epilogue {
     ResidentScratch* res;  // RESIDENT: holds the tokens' scales
     int part, lane, r;  // r: lane of the tile
-    float* s;           // scales of this warp's columns (chunks of 16: part, part + PARTS, ..)
+    float* s;           // scales of this warp's columns (chunks of 16: part, part + PARTS, ..), then negated
     float sw;
     bool plain;         // the warp's scales are of ordinary size
     __device__ __forceinline__ Epilogue(const Args&, unsigned char* sm, int q, int part_, int lane_)
-        : res(reinterpret_cast<ResidentScratch*>(sm + EPI_WARPS * EPI_COLS * 4)), part(part_), lane(lane_), r(q * 32 + lane_),
-          s(reinterpret_cast<float*>(sm) + (part_ * 4 + q) * EPI_COLS) {}
+        : res(reinterpret_cast<ResidentScratch*>(sm + EPI_WARPS * EPI_COLS * 8)), part(part_), lane(lane_), r(q * 32 + lane_),
+          s(reinterpret_cast<float*>(sm) + (part_ * 4 + q) * 2 * EPI_COLS) {}
     __device__ __forceinline__ void write_b(const Args& a, unsigned char* b, int warp) {
       if (!RESIDENT) return;
       if (a.x.x_type == DFSSM_BF16) resident_quantize<__nv_bfloat16>(a.x, b, res, warp, lane);
@@ -91,6 +93,7 @@ struct LinearPolicy {
         const int i = k * 32 + lane, c = ((i >> 4) * PARTS + part) * 16 + (i & 15);
         const float st = c < t.nb ? (RESIDENT ? res->s[c] : (float)a.s_tok[t.b0 + c]) : 1.0f;
         s[i] = st;
+        s[EPI_COLS + i] = -st;
         ok = ok && (ordinary(st) || st == 0.0f);
       }
       plain = __all_sync(0xffffffffu, ok);
@@ -100,8 +103,9 @@ struct LinearPolicy {
       const bool rv = r < t.na;
       uint32_t v[16];
       const float* st = s;
-      const f2 sw2 = pack2(sw, sw);
+      const f2 w2 = pack2(sw, sw), nw2 = pack2(-sw, -sw);
       Y* yp = a.y + (int64_t)(t.b0 + part * 16) * a.ldy + row;
+      const uint32_t ld = (uint32_t)a.ldy;
       if (part * 16 < t.nb) tmem_ld16(taddr + (uint32_t)(part * 16), v);
 #pragma unroll 1
       for (int c = part * 16; c < t.nb; c += 16 * PARTS, st += 16) {
@@ -116,9 +120,9 @@ struct LinearPolicy {
         bool sure = plain;
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
-          const float4 s4 = *reinterpret_cast<const float4*>(st + j);
-          scaled(v[j], v[j + 1], pack2(s4.x, s4.y), sw2, sure, out[j], out[j + 1]);
-          scaled(v[j + 2], v[j + 3], pack2(s4.z, s4.w), sw2, sure, out[j + 2], out[j + 3]);
+          const float4 s4 = *reinterpret_cast<const float4*>(st + j), n4 = *reinterpret_cast<const float4*>(st + EPI_COLS + j);
+          scaled(v[j], v[j + 1], pack2(s4.x, s4.y), pack2(n4.x, n4.y), w2, nw2, sure, out[j], out[j + 1]);
+          scaled(v[j + 2], v[j + 3], pack2(s4.z, s4.w), pack2(n4.z, n4.w), w2, nw2, sure, out[j + 2], out[j + 3]);
         }
         if (!sure) {
 #pragma unroll
@@ -126,16 +130,15 @@ struct LinearPolicy {
             out[j] = __double2float_rn(dmul(dmul(int_to_f64((int)v[j]), (double)st[j]), (double)sw));
         }
         if (c + 16 * PARTS < t.nb) tmem_ld16(taddr + (uint32_t)(c + 16 * PARTS), v);  // the next chunk, while this one is stored
-        if (n == 16) {
+        if (rv && n == 16) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j, yp += a.ldy)
-            if (rv) *yp = (Y)out[j];
-        } else {
+          for (int j = 0; j < 16; ++j) yp[(uint64_t)ld * j] = (Y)out[j];
+        } else if (rv) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j, yp += a.ldy)
-            if (rv && j < n) *yp = (Y)out[j];
+          for (int j = 0; j < 16; ++j)
+            if (j < n) yp[(uint64_t)ld * j] = (Y)out[j];
         }
-        yp += (16 * PARTS - 16) * a.ldy;
+        yp += 16 * PARTS * a.ldy;
       }
       __syncwarp();  // the scales are read: the next tile's may be written
     }
@@ -213,6 +216,7 @@ extern "C" int dfssm_linear_int8(const int8_t* W, const float* s_row, int V, int
   int st = check_int8_matrix(W, V, d);
   if (st) return st;
   if (!s_row || M < 0 || ldy < V || (y_type != DFSSM_F32 && y_type != DFSSM_BF16)) return DFSSM_EINVAL;
+  if (ldy > INT32_MAX) return DFSSM_EUNSUPPORTED;
   if (M == 0) return DFSSM_OK;
   st = check_rows(x, x_type, ldx, d);
   if (st) return st;

@@ -361,7 +361,7 @@ enum { DFSSM_F32 = 0, DFSSM_BF16 = 1 };
  * Int8 linear of M tokens: y[t][v] = fl32(acc[t][v] s[t] s_row[v]) (fp64, this order), acc = W q (int32, exact),
  * with (q, s) the per-token absmax int8 quantization of x, as dfssm_lm_head for one token, bit for bit.
  *   norm_w device f32 [d] (16-byte aligned) or NULL: the tokens are first RMS-normalised as in
- *   dfssm_head_greedy.  y [M][V] of type y_type, rows ldy >= V elements apart (element alignment); bf16
+ *   dfssm_head_greedy.  y [M][V] of type y_type, rows ldy >= V (at most 2^31 - 1) elements apart (element alignment); bf16
  *   outputs are the fp32 result rounded once more.  A token that holds an infinity or a NaN gives NaN outputs.
  *   dbg (may be NULL): acc [M][V], xq [M][d] (8-byte aligned) and xscale [M] are written; lora_t is not.
  *   M = 1 is a stream of W; M in the hundreds is bound by the tensor cores.

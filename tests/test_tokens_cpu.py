@@ -55,6 +55,7 @@ def test_linear_int8_refusals(L):
     assert f(yt=-1) == -1
     assert f(ldx=31) == -1
     assert f(ldy=9) == -1
+    assert f(ldy=1 << 31) == -3
     assert f(x=24) == -2
     assert f(ldx=34) == -2            # fp32 rows not 16-byte aligned
     assert f(xt=1, ldx=36) == -2      # bf16 rows
