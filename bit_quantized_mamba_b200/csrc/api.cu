@@ -273,7 +273,7 @@ bool dfssm::device_ok() {
 
 int dfssm::check_int8_matrix(const int8_t* W, int V, int d) {
   if (!W || V < 1 || d < 16 || d % 16) return DFSSM_EINVAL;
-  if (d > 8192) return DFSSM_EUNSUPPORTED;
+  if (d > 8192 || V > 1 << 30) return DFSSM_EUNSUPPORTED;
   return aligned(W, 16) ? DFSSM_OK : DFSSM_EALIGN;
 }
 
@@ -369,7 +369,7 @@ size_t dfssm_workspace_size(int op, int a, int b, int c) {
     case DFSSM_OP_EMBED_BACKWARD:
     case DFSSM_OP_HEAD_LOSS:
     case DFSSM_OP_HEAD_LOSS_BACKWARD:
-      if (a < 0 || b < 16 || b % 16 || b > 8192 || c < 1) return 0;
+      if (a < 0 || b < 16 || b % 16 || b > 8192 || c < 1 || c > 1 << 30) return 0;
       if (a == 0) return dfssm::kStatusBytes;
       if (op == DFSSM_OP_LINEAR_INT8) return dfssm::linear_int8_workspace_bytes(a, b);
       if (op == DFSSM_OP_EMBED_BACKWARD) return dfssm::embed_backward_workspace_bytes(a, b, c);

@@ -476,7 +476,7 @@ __device__ __forceinline__ FixedPoint fixed_point(const uint32_t* srow) {
   const bool neg = srow[1] != 0u;
   FixedPoint p;
   p.range = neg ? 1 << 23 : 1 << 24;
-  p.unit = smax == 0.0f ? 0.0f : (float)(p.range - 64) / scale2(smax);
+  p.unit = smax < 1e-30f ? 0.0f : (float)(p.range - 64) / scale2(smax);  // (so small, nothing of du is left either)
   p.offset = neg ? 1 << 23 : 0;
   p.step = p.unit == 0.0f ? 0.0 : 1.0 / ((double)p.unit * kLog2e);
   return p;
@@ -1259,6 +1259,7 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   int st = check_int8_matrix(W, V, d);
   if (st) return st;
   if (!s_row || M < 0 || (dnorm_w && !norm_w)) return DFSSM_EINVAL;
+  if (V > 1 << 24) return DFSSM_EUNSUPPORTED;  // W's column sums are int32
   if (M == 0) {  // no tokens: the sums over them are zero
     if (!al(ds_row, 4) || !al(dnorm_w, 4)) return DFSSM_EALIGN;
     if ((ds_row || dnorm_w) && !device_ok()) return DFSSM_EDEVICE;

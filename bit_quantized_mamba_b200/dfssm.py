@@ -535,7 +535,7 @@ def linear_int8(W, s_row, x, y=None, norm_w=None, out_dtype=torch.float32, ws=No
     be strided.  debug: dict of optional taps acc [M][V], xq [M][d], xscale [M]."""
     V, d = _matrix(W)
     M = x.shape[0]
-    st = _on(stream, W, s_row, x, y, norm_w, ws)
+    st = _on(stream, W, s_row, x, y, norm_w, ws, *(debug.values() if debug else ()))
     if y is None:
         y = _new(stream, (M, V), out_dtype, x.device)
     ws = _ws(ws, stream, OP_LINEAR_INT8, M, d, V, x.device)

@@ -345,7 +345,7 @@ int dfssm_generate(const dfssm_layer_t* layers, int n_layers, const dfssm_dims_t
  * matrix with a scale per row): the lookup, the product, the loss over the vocabulary, and the gradients.
  * Common to these calls:
  *   W device i8 [V][d] (16-byte aligned), s_row device f32 [V]; d % 16 == 0, d >= 16 (otherwise DFSSM_EINVAL),
- *   d <= 8192 (otherwise DFSSM_EUNSUPPORTED).
+ *   d <= 8192 and V <= 2^30 (otherwise DFSSM_EUNSUPPORTED; dfssm_head_loss_backward: V <= 2^24).
  *   Activations are rows of d values of type DFSSM_F32 or DFSSM_BF16, ld* elements apart (ld* >= d, else
  *   DFSSM_EINVAL), every row 16-byte aligned (else DFSSM_EALIGN); values between rows are neither read nor
  *   written.  Outputs must not overlap inputs or each other.
@@ -399,7 +399,8 @@ int dfssm_embed_tokens_backward(const int8_t* W, int V, int d, const int32_t* to
  *   loss[t] = log sum_v exp l[t][v] - l[t][labels[t]]     device f32 [M]
  * labels device i32 [M]; a negative label is ignored (loss 0, no gradient), one >= V is ignored too and gives
  * DFSSM_EINVAL from dfssm_device_status.  A token that holds an infinity or a NaN has loss NaN.
- * stats device f32 [3][M] receives what dfssm_head_loss_backward needs (opaque).
+ * stats device f32 [3][M] receives what dfssm_head_loss_backward needs (opaque).  Up to 64 tokens the CTAs count
+ * themselves in the workspace: zero-filled before its first use, every call leaves the count zero.
  * workspace: dfssm_workspace_size(DFSSM_OP_HEAD_LOSS, M, d, V).
  */
 int dfssm_head_loss(const int8_t* W, const float* s_row, int V, int d, const void* x, int x_type, int64_t ldx,
@@ -415,8 +416,8 @@ int dfssm_head_loss(const int8_t* W, const float* s_row, int V, int d, const voi
  *   ds_row[v] = sum_t G[t][v] acc[t][v] s[t]     device f32 [V] or NULL (not computed)
  *   dnorm_w[i] = sum_t du[t][i] x[t][i] r[t]     device f32 [d] or NULL (not computed; needs norm_w)
  * W's codes are frozen integers and get no gradient.  Within du the coefficients softmax s_row are rounded to 24
- * bits of their largest possible value in the token (23 and a sign when a row scale is negative), and
- * everything after that is exact up to the final rounding.
+ * bits below a part of at least 1/16 of their largest possible value (23 and a sign when a row scale is negative), and
+ * everything after that is exact up to the final rounding.  (Row scales all below 1e-30 leave dx its label's part.)
  * workspace: dfssm_workspace_size(DFSSM_OP_HEAD_LOSS_BACKWARD, M, d, V).
  */
 int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int V, int d, const void* x, int x_type,

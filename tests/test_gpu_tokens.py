@@ -358,6 +358,30 @@ def test_head_loss_and_gradients(dev, M, V, d, dtype):
     check_head(dfssm, W, sr, x, nw, labels, dloss)
 
 
+@pytest.mark.parametrize("M,V,d,signed", [(300, 70000, 48, False), (20, 140000, 32, True), (4096, 9000, 64, False),
+                                          (64, 66000, 16, False), (65, 1000, 4096, True)])
+def test_head_gradient_in_pieces_of_the_vocabulary(dev, M, V, d, signed):
+    """Vocabularies of several pieces, and past one set of int32 accumulators; token counts at the kernels' limits."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(M + V, dev)
+    W, sr = matrix(g, V, d, dev, signed=signed)
+    x = rows(g, M, d, dev, torch.float32)
+    labels = torch.randint(-V // 9, V, (M,), generator=g, device=dev, dtype=torch.int32)
+    check_head(dfssm, W, sr, x, torch.rand(d, generator=g, device=dev) + 0.5, labels, torch.rand(M, generator=g, device=dev))
+
+
+def test_head_gradient_of_constant_rows_stays_in_range(dev):
+    """Every code at its limit and uniform coefficients: the largest digit sums there can be."""
+    from bit_quantized_mamba_b200 import dfssm
+    V, d, M = 65536, 16, 3
+    for code in (-128, 127):
+        W = torch.full((V, d), code, dtype=torch.int8, device=dev)
+        sr = torch.full((V,), 1e-3, device=dev)
+        x = torch.randn(M, d, generator=gen(3, dev), device=dev)
+        labels = torch.tensor([0, V - 1, 77], dtype=torch.int32, device=dev)
+        check_head(dfssm, W, sr, x, None, labels, torch.ones(M, device=dev))
+
+
 @pytest.mark.parametrize("strength", [0.3, 1.0, 4.0])
 def test_head_loss_of_confident_tokens(dev, strength):
     """Tokens that point at their label, up to losses far below the fp32 step of the logits: loss and gradient

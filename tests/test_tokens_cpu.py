@@ -22,6 +22,7 @@ def test_workspace_sizes():
         assert D.workspace_size(op, 4, 60, 10) == 0      # d % 16
         assert D.workspace_size(op, 4, 8208, 10) == 0    # d > 8192
         assert D.workspace_size(op, 4, 64, 0) == 0       # no rows
+        assert D.workspace_size(op, 4, 64, (1 << 30) + 1) == 0
         a, b = D.workspace_size(op, 100, 2048, 50288), D.workspace_size(op, 3000, 2048, 50288)
         assert 256 < a < b
     assert D.workspace_size(D.OP_EMBED_TOKENS, 0, 0, 0) == 256
@@ -40,13 +41,14 @@ def matrix_refusals(call):
     assert call(16, 10, 24) == -1
     assert call(16, 10, 0) == -1
     assert call(16, 10, 8208) == -3
+    assert call(16, (1 << 30) + 1, 32) == -3
     assert call(8, 10, 32) == -2
 
 
 def test_linear_int8_refusals(L):
     def f(W=16, s=16, V=10, d=32, x=16, xt=0, ldx=32, M=4, nw=None, y=16, yt=0, ldy=10, ws=256, n=BIG):
         return L.dfssm_linear_int8(W, s, V, d, x, xt, ldx, M, nw, y, yt, ldy, ws, n, None, None)
-    matrix_refusals(lambda W, V, d: f(W=W, V=V, d=d, ldx=max(d, 32)))
+    matrix_refusals(lambda W, V, d: f(W=W, V=V, d=d, ldx=max(d, 32), ldy=max(V, 10)))
     assert f(s=None) == -1
     assert f(x=None) == -1
     assert f(y=None) == -1
@@ -105,6 +107,7 @@ def test_head_loss_backward_refusals(L):
           ws=256, nb=BIG):
         return L.dfssm_head_loss_backward(W, s, V, d, x, t, ldx, M, nw, y, st, g, dx, lddx, ds, dn, ws, nb, None)
     matrix_refusals(lambda W, V, d: f(W=W, V=V, d=d, ldx=max(d, 32), lddx=max(d, 32)))
+    assert f(V=(1 << 24) + 1) == -3
     for kw, want in ((dict(s=None), -1), (dict(x=None), -1), (dict(M=-1), -1), (dict(y=None), -1), (dict(st=None), -1),
                      (dict(g=None), -1), (dict(dx=None), -1), (dict(nw=None), -1), (dict(t=9), -1), (dict(lddx=16), -1),
                      (dict(lddx=33), -2), (dict(dx=8), -2), (dict(ds=1), -2), (dict(dn=2), -2), (dict(g=3), -2),
