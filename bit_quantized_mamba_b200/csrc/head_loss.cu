@@ -54,13 +54,14 @@ __device__ __forceinline__ float ex2(float x) {
 // 4.0e-8 off instead of 3.4e-8).
 __device__ __forceinline__ float scale2(float s_row) { return __double2float_rn((double)s_row * kLog2e); }
 
-// v[j] of an array in registers.
-__device__ __forceinline__ uint32_t pick(const uint32_t (&v)[32], int j) {
-  uint32_t x[16];
+// v[j] of an array in registers, N a power of two.
+template <int N>
+__device__ __forceinline__ uint32_t pick(const uint32_t (&v)[N], int j) {
+  uint32_t x[N / 2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = (j & 16) ? v[i + 16] : v[i];
+  for (int i = 0; i < N / 2; ++i) x[i] = (j & (N / 2)) ? v[i + N / 2] : v[i];
 #pragma unroll
-  for (int n = 8; n > 0; n >>= 1)
+  for (int n = N / 4; n > 0; n >>= 1)
 #pragma unroll
     for (int i = 0; i < n; ++i) x[i] = (j & n) ? x[i + n] : x[i];
   return x[0];
@@ -552,7 +553,7 @@ template <int CG_, bool DS>
 struct DigitPolicy {
   static constexpr int CG = CG_;
   static constexpr bool W_EARLY = true, W_IS_A = false, RESIDENT = false;
-  static constexpr int EPI_WARPS = 8, EPI_COLS = BN_MAX / 2;  // columns of an epilogue warp
+  static constexpr int EPI_WARPS = 16, PARTS = EPI_WARPS / 4, EPI_COLS = BN_MAX / PARTS;  // columns of a warp
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
     RowArgs r;
@@ -583,14 +584,14 @@ struct DigitPolicy {
   static __device__ __forceinline__ uint64_t b_step(const Args&) { return UMMA_K >> 4; }
   static constexpr int EPI_SMEM = EPI_WARPS * EPI_COLS * 8;
   struct Epilogue {
-    int q, half, lane;
-    float* sr;   // row scales of this warp's columns (chunks of 32: half, half + 2, ..), in units of log 2
+    int q, part, lane;
+    float* sr;   // row scales of this warp's columns (chunks of 16: part, part + PARTS, ..), in units of log 2
     float* cu;   // the same times the steps per unit
     FixedPoint fp;
     float4 tf;
     int label, most;
-    __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int half_, int lane_)
-        : q(q_), half(half_), lane(lane_), sr(reinterpret_cast<float*>(sm) + (half_ * 4 + q_) * 2 * EPI_COLS),
+    __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int part_, int lane_)
+        : q(q_), part(part_), lane(lane_), sr(reinterpret_cast<float*>(sm) + (part_ * 4 + q_) * 2 * EPI_COLS),
           cu(sr + EPI_COLS), fp(fixed_point(a.srow)) {}
     __device__ __forceinline__ void write_b(const Args&, unsigned char*, int) {}
     __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
@@ -601,10 +602,10 @@ struct DigitPolicy {
       most = (fp.range << (valid ? a.shift[tk] : 0)) - 1 + fp.offset;
 #pragma unroll
       for (int k = 0; k < EPI_COLS / 32; ++k) {
-        const int c = k * 64 + half * 32 + lane;
+        const int i = k * 32 + lane, c = ((i >> 4) * PARTS + part) * 16 + (i & 15);
         const float w = c < t.nb ? scale2(__ldg(a.s_row + a.v0 + t.b0 + c)) : 0.0f;
-        sr[k * 32 + lane] = w;
-        cu[k * 32 + lane] = w * fp.unit;
+        sr[i] = w;
+        cu[i] = w * fp.unit;
       }
       __syncwarp();
     }
@@ -612,21 +613,21 @@ struct DigitPolicy {
       const int tk = t.a0 + q * 32 + lane;
       const bool valid = tk < a.M;
       unsigned char* dst = a.digits + (size_t)(tk / a.tb) * a.tb * a.Vp + (size_t)(tk % a.tb) * 16;
-      uint32_t v[32];
+      uint32_t v[16];
       const float *w1 = sr, *u1 = cu;
       const f2 s2 = pack2(tf.y, tf.y), m2 = pack2(-tf.x, -tf.x), f_s = pack2(tf.z, tf.z);
-      if (half * 32 < t.nb) tmem_ld32(taddr + (uint32_t)(half * 32), v);
-#pragma unroll 1  // four copies of the body would not stay in the instruction cache
-      for (int c = half * 32; c < t.nb; c += 64, w1 += 32, u1 += 32) {
+      if (part * 16 < t.nb) tmem_ld16(taddr + (uint32_t)(part * 16), v);
+#pragma unroll 1  // copies of the body would not stay in the instruction cache
+      for (int c = part * 16; c < t.nb; c += 16 * PARTS, w1 += 16, u1 += 16) {
         tmem_wait(v);
         const int v0 = t.b0 + c;  // within the piece
         const uint32_t lc = (uint32_t)(label - v0);
-        const bool any = __any_sync(0xffffffffu, lc < 32u);
-        const float at_label = any ? (float)(int)pick(v, (int)(lc & 31u)) : 0.0f;
-        f2 h[16];
+        const bool any = __any_sync(0xffffffffu, lc < 16u);
+        const float at_label = any ? (float)(int)pick(v, (int)(lc & 15u)) : 0.0f;
+        f2 h[8];
         uint32_t high = 0u;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < 8; ++j) {
           const f2 w = *reinterpret_cast<const f2*>(w1 + 2 * j), u = *reinterpret_cast<const f2*>(u1 + 2 * j);
           const f2 av = pack2((float)(int)v[2 * j], (float)(int)v[2 * j + 1]);
           float e0, e1, n0, n1;
@@ -638,10 +639,10 @@ struct DigitPolicy {
           v[2 * j + 1] = (uint32_t)__viaddmin_s32(__float2int_rn(n1), fp.offset, most);
           high |= v[2 * j] | v[2 * j + 1];
         }
-        if (any && lc < 32u) {  // the label's own column: no digits, and its gradient of the row scale
+        if (any && lc < 16u) {  // the label's own column: no digits, and its gradient of the row scale
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float h0, h1;
+          for (int j = 0; j < 8; ++j) {
+            float h0 = 0.0f, h1 = 0.0f;
             if (DS) unpack2(h[j], h0, h1);
             if ((int)lc == 2 * j) v[2 * j] = (uint32_t)fp.offset, h0 = tf.w * at_label;
             if ((int)lc == 2 * j + 1) v[2 * j + 1] = (uint32_t)fp.offset, h1 = tf.w * at_label;
@@ -652,8 +653,8 @@ struct DigitPolicy {
           // few: the order of a list does not matter, its sum is taken in integers
           uint32_t which = 0u;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) which |= (v[j] >> 24 ? 1u : 0u) << j;
-          if (c + 32 > t.nb) which &= ~(0xFFFFFFFFu << (t.nb - c));
+          for (int j = 0; j < 16; ++j) which |= (v[j] >> 24 ? 1u : 0u) << j;
+          if (c + 16 > t.nb) which &= ~(0xFFFFFFFFu << (t.nb - c));
           while (which) {
             const int j = __ffs(which) - 1, i = atomicAdd(a.listed + tk, 1);
             which &= which - 1u;
@@ -662,42 +663,40 @@ struct DigitPolicy {
         }
         if (valid) {
           unsigned char* dp = dst + (size_t)(v0 >> 4) * a.tb * 16;
+          uint32_t o[3][4];
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            uint32_t o[3][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t* x = v + 16 * g + 4 * i;
-              const uint32_t p = __byte_perm(x[0], x[1], 0x5140), r = __byte_perm(x[2], x[3], 0x5140);
-              const uint32_t u = __byte_perm(x[0], x[1], 0x0062), w = __byte_perm(x[2], x[3], 0x0062);
-              o[0][i] = __byte_perm(p, r, 0x5410) ^ 0x80808080u;
-              o[1][i] = __byte_perm(p, r, 0x7632) ^ 0x80808080u;
-              o[2][i] = __byte_perm(u, w, 0x5410) ^ 0x80808080u;
-            }
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-              *reinterpret_cast<uint4*>(dp + k * a.plane + (size_t)g * a.tb * 16) =
-                  make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t* x = v + 4 * i;
+            const uint32_t p = __byte_perm(x[0], x[1], 0x5140), r = __byte_perm(x[2], x[3], 0x5140);
+            const uint32_t u = __byte_perm(x[0], x[1], 0x0062), w = __byte_perm(x[2], x[3], 0x0062);
+            o[0][i] = __byte_perm(p, r, 0x5410) ^ 0x80808080u;
+            o[1][i] = __byte_perm(p, r, 0x7632) ^ 0x80808080u;
+            o[2][i] = __byte_perm(u, w, 0x5410) ^ 0x80808080u;
           }
-        }
-        if (c + 64 < t.nb) tmem_ld32(taddr + (uint32_t)c + 64, v);  // the next chunk
-        if (DS) {
-          // column sums over the warp's 32 tokens: halves exchanged at every step, lane j ends with column j
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) {
-            const bool up = (lane & (2 * o)) != 0;
+          for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<uint4*>(dp + k * a.plane) = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+        }
+        if (c + 16 * PARTS < t.nb) tmem_ld16(taddr + (uint32_t)(c + 16 * PARTS), v);  // the next chunk
+        if (DS) {
+          // column sums over the warp's 32 tokens: halves exchanged at every step, lanes 2 j and 2 j + 1 end with
+          // column j
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) {
+            const bool up = (lane & (4 * o)) != 0;
 #pragma unroll
             for (int j = 0; j < o; ++j) {
               f2 give = up ? h[j] : h[j + o];
               const f2 keep = up ? h[j + o] : h[j];
-              give.v = __shfl_xor_sync(0xffffffffu, give.v, 2 * o);
+              give.v = __shfl_xor_sync(0xffffffffu, give.v, 4 * o);
               h[j] = add2(keep, give);
             }
           }
           float h0, h1;
           unpack2(h[0], h0, h1);
-          h0 = ((lane & 1) ? h1 : h0) + __shfl_xor_sync(0xffffffffu, (lane & 1) ? h0 : h1, 1);
-          if (c + lane < t.nb) a.colpart[(size_t)(t.a0 / 32 + q) * a.Vp + v0 + lane] = h0;
+          h0 = ((lane & 2) ? h1 : h0) + __shfl_xor_sync(0xffffffffu, (lane & 2) ? h0 : h1, 2);
+          h0 += __shfl_xor_sync(0xffffffffu, h0, 1);
+          if (!(lane & 1) && c + (lane >> 1) < t.nb) a.colpart[(size_t)(t.a0 / 32 + q) * a.Vp + v0 + (lane >> 1)] = h0;
         }
       }
       __syncwarp();  // the scales are read: the next tile's may be written
@@ -713,7 +712,7 @@ template <int CG_>
 struct GradPolicy {
   static constexpr int CG = CG_;
   static constexpr bool W_EARLY = false, W_IS_A = true, RESIDENT = false;
-  static constexpr int EPI_WARPS = 8, EPI_SMEM = 8 * 32 * 8;
+  static constexpr int EPI_WARPS = 16, PARTS = EPI_WARPS / 4, EPI_SMEM = EPI_WARPS * 32 * 8;
   struct Args {
     CUtensorMap map_a, map_b;  // transposed W, digits: blocks of 128 bytes
     Common c;
@@ -761,35 +760,35 @@ struct GradPolicy {
   static __device__ __forceinline__ uint64_t a_step() { return 2 * BM; }
   static __device__ __forceinline__ uint64_t b_step(const Args& a) { return (uint64_t)(2 * a.tb); }
   struct Epilogue {
-    int q, half, lane;
+    int q, part, lane;
     // While the first products accumulate: the piece's part of ds_row, 32 rows of W per CTA at a time, the partial
-    // sums of every 32 tokens in eight slices (one per warp) that are joined in order.
-    __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int half_, int lane_)
-        : q(q_), half(half_), lane(lane_) {
+    // sums of every 32 tokens in a slice per warp, joined in order.
+    __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int part_, int lane_)
+        : q(q_), part(part_), lane(lane_) {
       if (!a.colpart) return;
-      double* red = reinterpret_cast<double*>(sm);  // [8][32]
-      const int sl = half * 4 + q, parts = (a.M + 31) / 32;
+      double* red = reinterpret_cast<double*>(sm);  // [EPI_WARPS][32]
+      const int sl = part * 4 + q, parts = (a.M + 31) / 32;
       for (int b = blockIdx.x * 32; b < a.nv; b += gridDim.x * 32) {
         const int v = b + lane;
         double s = 0.0;
         if (v < a.nv) {
 #pragma unroll 8
-          for (int p = sl; p < parts; p += 8) s += (double)a.colpart[(size_t)p * a.Vp + v];
+          for (int p = sl; p < parts; p += EPI_WARPS) s += (double)a.colpart[(size_t)p * a.Vp + v];
         }
         red[sl * 32 + lane] = s;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(EPI_WARPS * 32) : "memory");
         if (sl == 0 && v < a.nv) {
-          for (int k = 1; k < 8; ++k) s += red[k * 32 + lane];
+          for (int k = 1; k < EPI_WARPS; ++k) s += red[k * 32 + lane];
           a.ds[v] = (float)s;
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(EPI_WARPS * 32) : "memory");
       }
     }
     __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
       const int col = t.a0 + q * 32 + lane, n = min(t.nb, a.M - t.b0);
       const bool cv = col < a.d;
       int32_t* base = a.acc + ((size_t)t.aux * a.M + t.b0) * a.d + col;
-      for (int c = half * 32; c < n; c += 64) {
+      for (int c = part * 32; c < n; c += 32 * PARTS) {
         uint32_t v[32];
         tmem_ld32(taddr + (uint32_t)c, v);
         tmem_wait(v);
