@@ -11,8 +11,8 @@
 //      other SMs write the zero rows of the dense gradient, whose stores are most of the traffic; more tokens
 //      take a radix sort over the whole device.
 //   2. the sorted positions are cut into windows of equal length, one CTA each, however often a token
-//      repeats; a run of equal tokens inside a window is final, one that crosses windows leaves a partial sum;
-//   3. the partial sums of a run are added in order.
+//      repeats; a run of equal tokens inside a window is final, one that crosses windows leaves partial sums, which
+//      the last of its CTAs to finish adds in order.
 
 #include "common.cuh"
 #include "internal.h"
@@ -192,6 +192,8 @@ struct SortFillArgs {
   int sort;         // 1: CTA 0 sorts (n <= SORT_MAX)
   int32_t* ids;     // [n] sorted
   int32_t* pos;     // [n] their positions
+  unsigned* done;   // [windows] counters of the sums, zeroed here
+  int windows;
   float* dE;        // dense gradient whose untouched rows are written zero, or NULL
   float* ds_row;    // likewise
   int* status;
@@ -204,6 +206,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) sort_fill_kernel(SortFillArgs
   pdl_launch_dependents();
   pdl_wait();
   if (a.sort && blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < a.windows; i += SORT_THREADS) a.done[i] = 0u;
     sort_one_cta(a.tokens, a.n, a.V, a.passes, a.ids, a.pos, a.status, sm);
     return;
   }
@@ -243,6 +246,8 @@ struct RadixArgs {
   int32_t* pos_out;
   uint32_t* cnt;           // [256][tiles]
   int n, V, tiles, shift;
+  unsigned* done;          // [windows] counters of the sums, zeroed with pass 0
+  int windows;
   int* status;
 };
 __device__ __forceinline__ uint32_t radix_key(const RadixArgs& a, int i) {
@@ -254,6 +259,8 @@ __global__ void __launch_bounds__(SORT_THREADS) radix_count_kernel(RadixArgs a) 
   pdl_launch_dependents();
   pdl_wait();
   __shared__ uint32_t h[256];
+  if (!a.pos_in)
+    for (int i = blockIdx.x * SORT_THREADS + threadIdx.x; i < a.windows; i += gridDim.x * SORT_THREADS) a.done[i] = 0u;
   if (threadIdx.x < 256) h[threadIdx.x] = 0u;
   __syncthreads();
   for (int k = 0; k < TILE / SORT_THREADS; ++k) {
@@ -343,18 +350,69 @@ struct SumArgs {
   float* ds_row;        // or NULL
   float* part;          // [windows][2][d] sums of the runs that cross a window's start (0) or only its end (1)
   float* dpart;         // [windows][2] their products with W's row
+  unsigned* done;       // [windows] CTAs finished of the run that starts in the window and leaves it
   int n, V, d, window, accumulate;
 };
 constexpr int MAX_WINDOW = 64;
 
+// Adds the partial sums of run v over windows w0 .. w1 in order (whole CTA).
+template <int CH>
+__device__ __forceinline__ void join_run(const SumArgs& a, int v, long long w0, long long w1) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (a.ds_row && warp == 0) {
+    float s = 0.0f;
+    for (long long x = w0 + 1 + lane; x <= w1; x += 32) s += __ldcg(a.dpart + (size_t)x * 2);
+    s = warp_sum(s);
+    if (lane == 0) {
+      s += __ldcg(a.dpart + (size_t)w0 * 2 + 1);
+      a.ds_row[v] = a.accumulate ? a.ds_row[v] + s : s;
+    }
+  }
+  if (!a.dE) return;
+  constexpr int U = 4;  // partial rows in flight
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = (threadIdx.x + 256 * c) * 8;
+    if (i >= a.d) continue;
+    const auto load = [&](size_t slot, float (&p)[8]) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part + slot * a.d + i));
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(a.part + slot * a.d + i) + 1);
+      p[0] = x.x, p[1] = x.y, p[2] = x.z, p[3] = x.w;
+      p[4] = y.x, p[5] = y.y, p[6] = y.z, p[7] = y.w;
+    };
+    float acc[8];
+    load((size_t)w0 * 2 + 1, acc);
+    for (long long x0 = w0 + 1; x0 <= w1; x0 += U) {
+      float p[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (x0 + u <= w1) load((size_t)(x0 + u) * 2, p[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (x0 + u <= w1) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] += p[u][j];
+        }
+    }
+    float* e = a.dE + (size_t)v * a.d + i;
+    if (a.accumulate) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += e[j];
+    }
+    store8<float>(e, acc);
+  }
+}
+
 // A window of sorted positions: rows added in order, run by run.  A run is final when both its ends lie in the
-// window.
+// window; of a longer one the last CTA to finish joins the partial sums.
 template <typename T, int CH>
 __global__ void __launch_bounds__(256, CH == 1 ? 4 : CH == 2 ? 3 : 2) window_kernel(SumArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ int32_t id[MAX_WINDOW + 2], ps[MAX_WINDOW];
   __shared__ float dots[MAX_WINDOW][8];
+  __shared__ long long from, to;  // windows of the first run (where it starts) and of the last (where it ends)
+  __shared__ int last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int k0 = blockIdx.x * a.window, nk = min(a.window, a.n - k0);
   // id[0] and id[nk + 1]: the neighbours outside (-1 where there is none)
@@ -440,74 +498,67 @@ __global__ void __launch_bounds__(256, CH == 1 ? 4 : CH == 2 ? 3 : 2) window_ker
       start = r + 1;
     }
   }
-  if (!a.ds_row) return;
   __syncthreads();
   const int r = threadIdx.x;
-  if (r >= nk) return;
-  const int v = id[r + 1];
-  if (v >= a.V || (r + 1 < nk && id[r + 2] == v)) return;
-  float s = 0.0f;
+  if (a.ds_row && r < nk) {
+    const int v = id[r + 1];
+    if (v < a.V && !(r + 1 < nk && id[r + 2] == v)) {
+      float s = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) s += dots[r][w];
-  int s0 = r;  // the run's first row in the window
-  while (s0 > 0 && id[s0] == v) --s0;
-  const bool before = s0 == 0 && id[0] == v, after = r + 1 == nk && id[nk + 1] == v;
-  if (before || after) a.dpart[(size_t)blockIdx.x * 2 + (before ? 0 : 1)] = s;
-  else a.ds_row[v] = a.accumulate ? a.ds_row[v] + s : s;
-}
-
-// Runs that cross windows: the CTA of the window where such a run starts adds the run's partial sums in order,
-// 512 columns per blockIdx.y.
-__global__ void __launch_bounds__(64) join_kernel(SumArgs a) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const long long w = blockIdx.x, k0 = w * a.window, k1 = k0 + a.window;
-  if (k1 >= a.n) return;
-  const int v = a.ids[k1 - 1], next = a.ids[k1], first = a.ids[k0], prev = k0 > 0 ? a.ids[k0 - 1] : -1;
-  if (v >= a.V || next != v) return;
-  if (first == v && prev == v) return;  // the run started earlier
-  // windows w + 1 .. we hold more of it: window x does if x's boundary with the one before lies within the run
-  const int lane = threadIdx.x & 31;
-  long long we = w;
-  while (true) {
-    const long long k = (we + 1 + lane) * a.window;
-    const bool in = k < a.n && a.ids[k - 1] == v && a.ids[k] == v;
-    const uint32_t out = ~__ballot_sync(0xffffffffu, in);
-    we += out ? __ffs(out) - 1 : 32;
-    if (out) break;
-  }
-  if (a.ds_row && blockIdx.y == 0 && threadIdx.x < 32) {
-    float s = 0.0f;
-    for (long long x = w + 1 + lane; x <= we; x += 32) s += a.dpart[(size_t)x * 2];
-    s = warp_sum(s);
-    if (lane == 0) {
-      s += a.dpart[(size_t)w * 2 + 1];
-      a.ds_row[v] = a.accumulate ? a.ds_row[v] + s : s;
+      for (int w = 0; w < 8; ++w) s += dots[r][w];
+      int s0 = r;  // the run's first row in the window
+      while (s0 > 0 && id[s0] == v) --s0;
+      const bool before = s0 == 0 && id[0] == v, after = r + 1 == nk && id[nk + 1] == v;
+      if (before || after) a.dpart[(size_t)blockIdx.x * 2 + (before ? 0 : 1)] = s;
+      else a.ds_row[v] = a.accumulate ? a.ds_row[v] + s : s;
     }
   }
-  const int i = (blockIdx.y * 64 + threadIdx.x) * 8;
-  if (!a.dE || i >= a.d) return;
-  float acc[8];
-  load8<float>(a.part + ((size_t)w * 2 + 1) * a.d + i, acc);
-  constexpr int U = 8;  // partial rows in flight
-  for (long long x0 = w + 1; x0 <= we; x0 += U) {
-    float p[U][8];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (x0 + u <= we) load8<float>(a.part + (size_t)(x0 + u) * 2 * a.d + i, p[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (x0 + u <= we) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += p[u][j];
+  // runs that cross the window's ends
+  const bool lead = id[1] < a.V && id[0] == id[1], tail = id[nk] < a.V && id[nk + 1] == id[nk];
+  if (!lead && !tail) return;
+  const bool one = lead && tail && id[1] == id[nk];  // the window lies within one run
+  const long long w = blockIdx.x;
+  // windows the runs extend over, 32 boundaries between windows at a time: the one before window x lies within the run
+  // if the ids on both sides are v
+  if (warp == 0) {
+    long long x = w;
+    if (lead) {
+      x = w - 1;
+      while (true) {
+        const long long k = (x - lane) * a.window;
+        const bool in = k > 0 && a.ids[k - 1] == id[1] && a.ids[k] == id[1];
+        const uint32_t out = ~__ballot_sync(0xffffffffu, in);
+        x -= out ? __ffs(out) - 1 : 32;
+        if (out) break;
       }
+    }
+    if (lane == 0) from = x;
+  } else if (warp == 1) {
+    long long x = w;
+    if (tail) {
+      while (true) {
+        const long long k = (x + 1 + lane) * a.window;
+        const bool in = k < a.n && a.ids[k - 1] == id[nk] && a.ids[k] == id[nk];
+        const uint32_t out = ~__ballot_sync(0xffffffffu, in);
+        x += out ? __ffs(out) - 1 : 32;
+        if (out) break;
+      }
+    }
+    if (lane == 0) to = x;
   }
-  float* e = a.dE + (size_t)v * a.d + i;
-  if (a.accumulate) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] += e[j];
+  for (int side = 0; side < 2; ++side) {  // the first run, then the last
+    if (side == 0 ? !lead : !tail || one) continue;
+    __syncthreads();  // the partial sums are written, `from` and `to` set
+    const long long w0 = side == 0 ? from : w, w1 = side == 0 && !one ? w : to;
+    if (threadIdx.x == 0) {
+      __threadfence();
+      last = atomicAdd(a.done + w0, 1u) == (unsigned)(w1 - w0);
+      __threadfence();
+    }
+    __syncthreads();
+    if (last) join_run<CH>(a, side == 0 ? id[1] : id[nk], w0, w1);
   }
-  store8<float>(e, acc);
 }
 
 template <typename T>
@@ -524,7 +575,7 @@ int window_rows(int n) {
 }
 
 struct BackwardWs {
-  size_t ids, pos, ids2, pos2, cnt, part, dpart, total;
+  size_t ids, pos, ids2, pos2, cnt, done, part, dpart, total;
 };
 BackwardWs backward_ws(int n, int d) {
   const size_t list = al256(sizeof(int32_t) * (size_t)n);
@@ -536,7 +587,8 @@ BackwardWs backward_ws(int n, int d) {
   w.ids2 = w.pos + list;
   w.pos2 = w.ids2 + (big ? list : 0);
   w.cnt = w.pos2 + (big ? list : 0);
-  w.part = w.cnt + (big ? al256(sizeof(uint32_t) * 256 * (((size_t)n + TILE - 1) / TILE)) : 0);
+  w.done = w.cnt + (big ? al256(sizeof(uint32_t) * 256 * (((size_t)n + TILE - 1) / TILE)) : 0);
+  w.part = w.done + al256(sizeof(unsigned) * windows);
   w.dpart = w.part + al256(sizeof(float) * 2 * windows * (size_t)d);
   w.total = w.dpart + al256(sizeof(float) * 2 * windows);
   return w;
@@ -605,6 +657,8 @@ extern "C" int dfssm_embed_tokens_backward(const int8_t* W, int V, int d, const 
     w = backward_ws(n, d);
     f.ids = reinterpret_cast<int32_t*>(base + w.ids);
     f.pos = reinterpret_cast<int32_t*>(base + w.pos);
+    f.done = reinterpret_cast<unsigned*>(base + w.done);
+    f.windows = (int)(((long long)n + window_rows(n) - 1) / window_rows(n));
     f.status = reinterpret_cast<int*>(base);
   }
   if (f.sort || !accumulate) {
@@ -626,6 +680,8 @@ extern "C" int dfssm_embed_tokens_backward(const int8_t* W, int V, int d, const 
     r.n = n;
     r.V = V;
     r.tiles = (n + TILE - 1) / TILE;
+    r.done = f.done;
+    r.windows = f.windows;
     r.status = f.status;
     for (int p = 0; p < passes; ++p) {
       r.ids_out = buf[p & 1][0];
@@ -655,9 +711,7 @@ extern "C" int dfssm_embed_tokens_backward(const int8_t* W, int V, int d, const 
   a.d = d;
   a.window = window_rows(n);
   a.accumulate = accumulate;
-  const int windows = (int)(((long long)n + a.window - 1) / a.window);
-  e = dh_type == DFSSM_BF16 ? launch_window<__nv_bfloat16>(a, windows, s) : launch_window<float>(a, windows, s);
-  if (e == cudaSuccess)
-    e = launch_pdl(join_kernel, dim3(windows, (d + 511) / 512), dim3(64), 0, s, a);
+  a.done = f.done;
+  e = dh_type == DFSSM_BF16 ? launch_window<__nv_bfloat16>(a, f.windows, s) : launch_window<float>(a, f.windows, s);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
 }

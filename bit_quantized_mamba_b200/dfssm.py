@@ -486,20 +486,20 @@ def _on(stream, *tensors):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _new(stream, shape, dtype, device, zero=False):
-    """A tensor allocated on the call's stream, so that its memory is not reused while the call still runs."""
-    make = torch.zeros if zero else torch.empty
+def _new(stream, like, shape, dtype, zero=False):
+    """A tensor on like's device, allocated on the call's stream, so that its memory is not reused while the call
+    still runs."""
     if stream is None:
-        return make(shape, dtype=dtype, device=device)
+        return like.new_zeros(shape, dtype=dtype) if zero else like.new_empty(shape, dtype=dtype)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(s):
-        return make(shape, dtype=dtype, device=device)
+        return like.new_zeros(shape, dtype=dtype) if zero else like.new_empty(shape, dtype=dtype)
 
 
-def _ws(ws, stream, op, a, b, c, device):
+def _ws(ws, stream, op, a, b, c, like):
     if ws is not None:
         return ws
-    return _new(stream, max(workspace_size(op, a, b, c), 256), torch.uint8, device, zero=True)
+    return _new(stream, like, (max(workspace_size(op, a, b, c), 256),), torch.uint8, zero=True)
 
 
 def _rows(t, n, d, what):
@@ -537,8 +537,8 @@ def linear_int8(W, s_row, x, y=None, norm_w=None, out_dtype=torch.float32, ws=No
     M = x.shape[0]
     st = _on(stream, W, s_row, x, y, norm_w, ws, *(debug.values() if debug else ()))
     if y is None:
-        y = _new(stream, (M, V), out_dtype, x.device)
-    ws = _ws(ws, stream, OP_LINEAR_INT8, M, d, V, x.device)
+        y = _new(stream, x, (M, V), out_dtype)
+    ws = _ws(ws, stream, OP_LINEAR_INT8, M, d, V, x)
     dbg = None
     if debug is not None:
         dbg = DebugT(_vector(debug.get("acc"), M * V, torch.int32, "acc"), None,
@@ -560,8 +560,8 @@ def embed_tokens(W, s_row, tokens, h=None, dtype=torch.float32, ws=None, stream=
     n = tokens.numel()
     st = _on(stream, W, s_row, tokens, h, ws)
     if h is None:
-        h = _new(stream, (n, d), dtype, W.device)
-    ws = _ws(ws, stream, OP_EMBED_TOKENS, 0, 0, 0, W.device)
+        h = _new(stream, W, (n, d), dtype)
+    ws = _ws(ws, stream, OP_EMBED_TOKENS, 0, 0, 0, W)
     ph, th, lh = _rows(h, n, d, "h")
     _check("dfssm_embed_tokens", lib().dfssm_embed_tokens(
         W.data_ptr(), _vector(s_row, V, torch.float32, "s_row"), V, d, _vector(tokens, n, torch.int32, "tokens"),
@@ -581,10 +581,10 @@ def embed_tokens_backward(W, tokens, dh, dE=None, ds_row=None, accumulate=False,
             raise ValueError("accumulate needs dE or ds_row")
     else:
         if dE is None:
-            dE = _new(stream, (V, d), torch.float32, W.device)
+            dE = _new(stream, W, (V, d), torch.float32)
         if ds_row is None:
-            ds_row = _new(stream, (V,), torch.float32, W.device)
-    ws = _ws(ws, stream, OP_EMBED_BACKWARD, n, d, V, W.device)
+            ds_row = _new(stream, W, (V,), torch.float32)
+    ws = _ws(ws, stream, OP_EMBED_BACKWARD, n, d, V, W)
     pd, td, ld = _rows(dh, n, d, "dh")
     _check("dfssm_embed_tokens_backward", lib().dfssm_embed_tokens_backward(
         W.data_ptr(), V, d, _vector(tokens, n, torch.int32, "tokens"), n, pd, td, ld,
@@ -600,10 +600,10 @@ def head_loss(W, s_row, x, labels, norm_w=None, loss=None, stats=None, ws=None, 
     M = x.shape[0]
     st = _on(stream, W, s_row, x, labels, norm_w, loss, stats, ws)
     if loss is None:
-        loss = _new(stream, (M,), torch.float32, x.device)
+        loss = _new(stream, x, (M,), torch.float32)
     if stats is None:
-        stats = _new(stream, (3, M), torch.float32, x.device)
-    ws = _ws(ws, stream, OP_HEAD_LOSS, M, d, V, x.device)
+        stats = _new(stream, x, (3, M), torch.float32)
+    ws = _ws(ws, stream, OP_HEAD_LOSS, M, d, V, x)
     px, tx, lx = _rows(x, M, d, "x")
     _check("dfssm_head_loss", lib().dfssm_head_loss(
         W.data_ptr(), _vector(s_row, V, torch.float32, "s_row"), V, d, px, tx, lx, M,
@@ -622,12 +622,12 @@ def head_loss_backward(W, s_row, x, labels, stats, dloss, norm_w=None, dx=None, 
     M = x.shape[0]
     st = _on(stream, W, s_row, x, labels, stats, dloss, norm_w, dx, ds_row, dnorm_w, ws)
     if dx is None:
-        dx = _new(stream, (M, d), x.dtype, x.device)
+        dx = _new(stream, x, (M, d), x.dtype)
     if ds_row is None and scales:
-        ds_row = _new(stream, (V,), torch.float32, x.device)
+        ds_row = _new(stream, x, (V,), torch.float32)
     if dnorm_w is None and norm_w is not None:
-        dnorm_w = _new(stream, (d,), torch.float32, x.device)
-    ws = _ws(ws, stream, OP_HEAD_LOSS_BACKWARD, M, d, V, x.device)
+        dnorm_w = _new(stream, x, (d,), torch.float32)
+    ws = _ws(ws, stream, OP_HEAD_LOSS_BACKWARD, M, d, V, x)
     px, tx, lx = _rows(x, M, d, "x")
     pd, td, ld = _rows(dx, M, d, "dx")
     if td != tx:
