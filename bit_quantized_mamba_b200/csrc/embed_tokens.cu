@@ -46,10 +46,10 @@ __global__ void __launch_bounds__(256) embed_tokens_kernel(EmbedTokensArgs a) {
   constexpr int N = sizeof(T) == 4 ? 4 : 8, STEP = WPT * 32 * N, U = 4;  // values a thread handles at a time
   const int per_cta = 8 / WPT, sub = (threadIdx.x >> 5) / WPT, i0 = (threadIdx.x % (WPT * 32)) * N;
   for (int t = blockIdx.x * per_cta + sub; t < a.n; t += gridDim.x * per_cta) {
-    const int tok = __ldg(a.tokens + t);
+    const int tok = ld_s32(a.tokens + t);
     const bool ok = tok >= 0 && tok < a.V;
     if (!ok && i0 == 0) atomicExch(a.status, kBadTokenCode);
-    const float sc = ok ? __ldg(a.s_row + tok) : 0.0f;
+    const float sc = ok ? ld_f32(a.s_row + tok) : 0.0f;
     const int8_t* row = a.W + (size_t)(ok ? tok : 0) * a.d;
     T* h = reinterpret_cast<T*>(a.h) + (int64_t)t * a.ldh;
     for (int i = i0; i < a.d; i += U * STEP) {
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) sort_fill_kernel(SortFillArgs
     __syncthreads();
 #pragma unroll 4
     for (int i = threadIdx.x; i < a.n; i += SORT_THREADS) {
-      const uint32_t r = (uint32_t)(__ldg(a.tokens + i) - r0);
+      const uint32_t r = (uint32_t)(ld_s32(a.tokens + i) - r0);
       if (r < (uint32_t)nr) sm[r] = 1;
     }
     __syncthreads();

@@ -199,8 +199,9 @@ __device__ __forceinline__ void issue(const Boxes& o, int kb, unsigned char* dst
     if (leader) tma_load<CG>(dst + i * o.box * BK, o.map, kb * o.dx, o.y + kb * o.dy + i * o.box, bar);
 }
 
-// With PDL the kernel may start while the one that writes the tokens' codes still runs: the first round of W is
-// requested without waiting for it.  Returns the number of K steps.  (Converged warp.)
+// With PDL the kernel may start while the one that writes the tokens' codes still runs: with W_EARLY the first round
+// of W, whose codes are written before the call is enqueued, is requested without waiting for it.  Returns the number
+// of K steps.  (Converged warp.)
 template <class P>
 __device__ __forceinline__ int request_w(const typename P::Args& ar, unsigned char* smem, uint64_t* full,
                                          uint32_t full_bar, int rank, bool leader) {
@@ -588,10 +589,9 @@ __device__ __forceinline__ void resident_quantize(const ResidentArgs& r, unsigne
     ss = warp_sum(ss);
     if (lane == 0) sc->ss[w] = ss;
     epilogue_sync();
-    if (w == first && lane == 0 && on) {
-      ss = 0.0;
-      for (int k = 0; k < per; ++k) ss += sc->ss[first + k];
-      sc->rn[t] = rms_factor(ss, r.d);
+    if (w == first) {
+      ss = warp_sum(lane < per ? sc->ss[first + lane] : 0.0);
+      if (lane == 0 && on) sc->rn[t] = rms_factor(ss, r.d);
     }
     epilogue_sync();
     if (on) {

@@ -128,7 +128,7 @@ struct ForwardPolicy {
 #pragma unroll
       for (int k = 0; k < EPI_COLS / 32; ++k) {
         const int c = k * 64 + half * 32 + lane;
-        sr[k * 32 + lane] = c < t.nb ? scale2(__ldg(a.s_row + t.b0 + c)) : 0.0f;
+        sr[k * 32 + lane] = c < t.nb ? scale2(ld_f32(a.s_row + t.b0 + c)) : 0.0f;
       }
       __syncwarp();
     }
@@ -151,7 +151,7 @@ struct ForwardPolicy {
         for (int j = 0; j < 16; ++j) x[j] = mul2(pack2((float)(int)v[2 * j], (float)(int)v[2 * j + 1]), st2);
         if (lc < 32u && c + (int)lc < t.nb) {
           const int al = (int)pick(v, (int)lc);
-          a.label_logit[tok] = __double2float_rn(dmul(dmul(int_to_f64(al), a.s_tok[tok]), (double)__ldg(a.s_row + label)));
+          a.label_logit[tok] = __double2float_rn(dmul(dmul(int_to_f64(al), a.s_tok[tok]), (double)ld_f32(a.s_row + label)));
         }
         if (c + 64 < t.nb) tmem_ld32(taddr + (uint32_t)c + 64, v);  // the next chunk, while this one is summed
         float mx = m;
@@ -222,10 +222,9 @@ __device__ __forceinline__ void write_loss(int t, float m, double S, int M, int 
 
 // Joins the partial (max, sum) of a token and forms its loss.  32 tokens per CTA, 32 slices of slots.
 constexpr int LF_SLICES = 32;
-__global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float2* __restrict__ part, int slots, int M,
-                                                                     int V, const int32_t* __restrict__ labels,
-                                                                     float* __restrict__ stats,
-                                                                     float* __restrict__ loss, int* status) {
+__global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float2* part, int slots, int M, int V,
+                                                                     const int32_t* labels, float* stats, float* loss,
+                                                                     int* status) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ float2 sm[LF_SLICES][33];
@@ -321,7 +320,7 @@ struct SmallForwardPolicy {
       // each warp fills (and reads) its own tokens; the four quadrants write the same values
       const int t = part * 16 + lane;
       if (lane < 16) {
-        sc->label[t] = t < a.M ? __ldg(a.labels + t) : -1;
+        sc->label[t] = t < a.M ? ld_s32(a.labels + t) : -1;
         if (!RESIDENT) sc->s[t] = t < a.M ? (float)a.s_tok[t] : 0.0f;
       }
       __syncwarp();
@@ -334,7 +333,7 @@ struct SmallForwardPolicy {
     __device__ __forceinline__ float scale(int t) const { return RESIDENT ? sc->res.s[t & (RES_TOKENS - 1)] : sc->s[t]; }
     __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
       const int r = q * 32 + lane;
-      sw = r < t.na ? scale2(__ldg(a.s_row + t.a0 + r)) : 0.0f;
+      sw = r < t.na ? scale2(ld_f32(a.s_row + t.a0 + r)) : 0.0f;
     }
     __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
       const int r = q * 32 + lane, row = t.a0 + r;
@@ -350,7 +349,7 @@ struct SmallForwardPolicy {
         const float st = scale(tok), x = (float)(int)v[j] * st;
         if (row == sc->label[tok]) {  // the label's own logit stays out of the sum
           a.stats[2 * (size_t)a.M + tok] =
-              __double2float_rn(dmul(dmul(int_to_f64((int)v[j]), (double)st), (double)__ldg(a.s_row + row)));
+              __double2float_rn(dmul(dmul(int_to_f64((int)v[j]), (double)st), (double)ld_f32(a.s_row + row)));
         } else {
           const float mx = fmaxf(m[j], x * sw), mz = mx == -INFINITY ? 0.0f : mx;
           S[j] = S[j] * ex2(m[j] - mz) + ex2(fmaf(x, sw, -mz));
@@ -427,7 +426,7 @@ __device__ __forceinline__ void grad_prepare(const PrepareArgs& a, int i, int n)
   uint32_t mb = 0u, neg = 0u;
 #pragma unroll 4
   for (int v = i; v < a.V; v += n) {
-    const float s = __ldg(a.s_row + v);
+    const float s = ld_f32(a.s_row + v);
     mb = max(mb, __float_as_uint(s) & 0x7FFFFFFFu);  // orders like |s|, a NaN above all
     neg |= s < 0.0f ? 1u : 0u;
   }
@@ -495,9 +494,8 @@ __device__ __forceinline__ float dither(uint32_t acc) {
 // (zero past the vocabulary and past d), and the column sums of W.  A thread turns 16 rows x 4 columns.
 constexpr int TR_ROWS = 16 * 2;  // vocabulary rows per warp
 // The first piece's launch has `prepare` more CTAs (in x, of its first row in y) for the tokens' factors.
-__global__ void __launch_bounds__(256) transpose_kernel(const int8_t* __restrict__ W, int V, int d, int v0, int Vp,
-                                                        int8_t* __restrict__ wt, int32_t* __restrict__ colsum,
-                                                        int prepare, const PrepareArgs pa) {
+__global__ void __launch_bounds__(256) transpose_kernel(const int8_t* W, int V, int d, int v0, int Vp, int8_t* wt,
+                                                        int32_t* colsum, int prepare, const PrepareArgs pa) {
   pdl_launch_dependents();
   pdl_wait();
   const int blocks = gridDim.x - prepare;
@@ -516,7 +514,7 @@ __global__ void __launch_bounds__(256) transpose_kernel(const int8_t* __restrict
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int v = v0 + chunk * 16 + r;
-      w[r] = (v < V && col < d) ? __ldg(reinterpret_cast<const uint32_t*>(W + (size_t)v * d + col)) : 0u;
+      w[r] = (v < V && col < d) ? ld_u32(W + (size_t)v * d + col) : 0u;
     }
     uint4 o[4];
 #pragma unroll
@@ -603,7 +601,7 @@ struct DigitPolicy {
 #pragma unroll
       for (int k = 0; k < EPI_COLS / 32; ++k) {
         const int i = k * 32 + lane, c = ((i >> 4) * PARTS + part) * 16 + (i & 15);
-        const float w = c < t.nb ? scale2(__ldg(a.s_row + a.v0 + t.b0 + c)) : 0.0f;
+        const float w = c < t.nb ? scale2(ld_f32(a.s_row + a.v0 + t.b0 + c)) : 0.0f;
         sr[i] = w;
         cu[i] = w * fp.unit;
       }
@@ -845,7 +843,7 @@ __global__ void __launch_bounds__(256) grad_finish_kernel(GradFinishArgs a) {
     const int y = a.labels[t];
     const bool kept = y >= 0 && y < a.V;
     const int nl = min(a.listed[t], kListed);
-    const double f = fac.x * fp.step, wy = kept ? fac.y * (double)__ldg(a.s_row + y) : 0.0;
+    const double f = fac.x * fp.step, wy = kept ? fac.y * (double)ld_f32(a.s_row + y) : 0.0;
     float du[CH][8], xv[CH][8];
     double dot = 0.0;
 #pragma unroll
@@ -867,7 +865,7 @@ __global__ void __launch_bounds__(256) grad_finish_kernel(GradFinishArgs a) {
           for (int k = 0; k < 8; ++k) sum[k] += (long long)n[k] << (8 * g);
         }
       for (int l = 0; l < nl; ++l) {
-        const int2 e = __ldg(a.list + (size_t)t * kListed + l);
+        const int2 e = a.list[(size_t)t * kListed + l];
         const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.W + (size_t)e.x * a.d + i));
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -923,8 +921,7 @@ __global__ void __launch_bounds__(256) grad_finish_kernel(GradFinishArgs a) {
 }
 
 // 32 columns per CTA, 32 slices of the partial sums, joined in order.
-__global__ void __launch_bounds__(1024) dnorm_finish_kernel(const float* __restrict__ npart, int parts, int d,
-                                                            float* __restrict__ dn) {
+__global__ void __launch_bounds__(1024) dnorm_finish_kernel(const float* npart, int parts, int d, float* dn) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ float red[32][33];

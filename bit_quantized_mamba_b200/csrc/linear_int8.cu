@@ -86,7 +86,7 @@ struct LinearPolicy {
       else resident_quantize<float>(a.x, b, res, warp, lane);
     }
     __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
-      sw = r < t.na ? __ldg(a.s_row + t.a0 + r) : 1.0f;
+      sw = r < t.na ? ld_f32(a.s_row + t.a0 + r) : 1.0f;
       bool ok = ordinary(sw);
 #pragma unroll
       for (int k = 0; k < EPI_COLS / 32; ++k) {

@@ -1,4 +1,4 @@
-// Eight consecutive values of a row, fp32 or bf16, 16-byte aligned.
+// Loads in stream order, and eight consecutive values of a row (fp32 or bf16, 16-byte aligned).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -7,17 +7,34 @@
 
 namespace dfssm {
 
+// What an earlier kernel of the stream may have written is read with these after pdl_wait(): the compiler may move a
+// read-only load (__ldg, or one through a __restrict__ parameter) above that wait, as nothing in the kernel itself
+// writes the memory; volatile assembly keeps its place.
+__device__ __forceinline__ uint32_t ld_u32(const void* p) {
+  uint32_t r;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ int ld_s32(const int32_t* p) { return (int)ld_u32(p); }
+__device__ __forceinline__ float ld_f32(const float* p) { return __uint_as_float(ld_u32(p)); }
+__device__ __forceinline__ uint4 ld_u32x4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8]);
 template <>
 __device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  const uint4 a = ld_u32x4(p), b = ld_u32x4(p + 4);
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
 }
 template <>
 __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 a = ld_u32x4(p);
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

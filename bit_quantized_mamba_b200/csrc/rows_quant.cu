@@ -27,12 +27,13 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_quant_kernel(RowsQuantArgs a)
   __shared__ float red_rn;
   const int tok = blockIdx.x;
   const T* xr = reinterpret_cast<const T*>(a.x) + (size_t)tok * a.ldx;
-  float v[CH][8];
+  float v[CH][8], nw[CH][8];  // the row, and the norm's weight with it
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = (threadIdx.x + RQ_THREADS * c) * 8;
     if (i < a.d) {
       load8<T>(xr + i, v[c]);
+      if (a.norm_w) load8<float>(a.norm_w + i, nw[c]);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[c][k] = 0.0f;
@@ -47,12 +48,13 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_quant_kernel(RowsQuantArgs a)
     ss = warp_sum(ss);
     if (lane == 0) red_ss[warp] = ss;
     __syncthreads();
-    if (threadIdx.x == 0) {  // fp64 division and root once, not in every warp
-      ss = 0.0;
-#pragma unroll
-      for (int w = 0; w < RQ_THREADS / 32; ++w) ss += red_ss[w];
-      red_rn = rms_factor(ss, a.d);
-      if (a.rn) a.rn[tok] = red_rn;
+    if (warp == 0) {  // fp64 division and root once, not in every warp
+      ss = warp_sum(lane < RQ_THREADS / 32 ? red_ss[lane] : 0.0);
+      const float r = rms_factor(ss, a.d);
+      if (lane == 0) {
+        red_rn = r;
+        if (a.rn) a.rn[tok] = r;
+      }
     }
     __syncthreads();
     const float rn = red_rn;
@@ -60,10 +62,8 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_quant_kernel(RowsQuantArgs a)
     for (int c = 0; c < CH; ++c) {
       const int i = (threadIdx.x + RQ_THREADS * c) * 8;
       if (i < a.d) {
-        float w[8];
-        load8<float>(a.norm_w + i, w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[c][k] = norm_value(v[c][k], rn, w[k]);
+        for (int k = 0; k < 8; ++k) v[c][k] = norm_value(v[c][k], rn, nw[c][k]);
       }
     }
   }

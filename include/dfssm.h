@@ -23,7 +23,8 @@
  *   - Every call is asynchronous on `stream` (a cudaStream_t; NULL = legacy default stream).  Inputs
  *     must not be modified, and outputs not read, until the stream reaches the call.  Weights and
  *     parameters must be fully written before the call is enqueued (kernels may read them before they
- *     wait on the preceding kernel of the stream).
+ *     wait on the preceding kernel of the stream).  The many-token calls on the int8 matrix read only its
+ *     codes W so: row scales and norm weights, which training updates, are read in stream order.
  *   - Arguments are validated before anything is launched; on a negative status nothing was enqueued.
  *   - Concurrency: calls that share a workspace must not overlap on the GPU.  The library's only state
  *     outside the caller's buffers is per-device and set once (the kernels' shared-memory attribute and

@@ -551,6 +551,45 @@ def test_training_step_in_a_graph_and_on_another_stream(dev):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_parameters_updated_in_the_stream(dev, M):
+    """Row scales and norm weights that the stream itself updates between steps (a captured loop without a pause
+    between its kernels) give the bits of steps taken one at a time."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(23, dev)
+    V, d, n = 1501, 512, 4
+    W, sr0 = matrix(g, V, d, dev)
+    nw0 = torch.rand(d, generator=g, device=dev) + 0.5
+    tok = torch.randint(0, V, (n, M), generator=g, device=dev, dtype=torch.int32)
+    lab = torch.randint(-1, V, (n, M), generator=g, device=dev, dtype=torch.int32)
+    dloss = torch.full((M,), 1 / M, device=dev)
+    ws = workspaces(dfssm, M, d, V, dev)
+    sr, nw, t, y = sr0.clone(), nw0.clone(), tok[0].clone(), lab[0].clone()
+
+    def steps(pause):
+        sr.copy_(sr0), nw.copy_(nw0)
+        outs = []
+        for k in range(n):
+            t.copy_(tok[k]), y.copy_(lab[k])
+            pause()
+            out = training_step(dfssm, W, sr, nw, t, y, dloss, ws)
+            pause()
+            outs.append(out)
+            sr.mul_(1.25), nw.mul_(0.75)
+        return outs
+
+    want = [[a.clone() for a in out] for out in steps(torch.cuda.synchronize)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = steps(lambda: None)
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
+
+
 def test_outputs_allocated_for_an_explicit_stream(dev):
     from bit_quantized_mamba_b200 import dfssm
     g = gen(22, dev)
