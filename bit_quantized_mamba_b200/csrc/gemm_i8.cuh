@@ -51,10 +51,10 @@ struct Tile {
 template <int CG>
 __device__ __forceinline__ int mma_n(int nb) { return (nb + 16 * CG - 1) & ~(16 * CG - 1); }
 
-// kind::i8 instruction descriptor: D s32, A and B s8, both K-major, M = 128 CG, N = n.
+// kind::i8 instruction descriptor: D s32, A and B s8, B and (unless a_mn) A K-major, M = 128 CG, N = n.
 template <int CG>
-__device__ __forceinline__ uint32_t idesc(int n) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)((BM * CG) >> 4) << 24);
+__device__ __forceinline__ uint32_t idesc(int n, bool a_mn) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)((BM * CG) >> 4) << 24);
 }
 template <int CG>
 __device__ __forceinline__ void umma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t id,
@@ -143,10 +143,10 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// The TMA copies of an operand's K step kb: n boxes of `box` rows of 128 bytes at (kb dx, y + kb dy + i box).
+// The TMA copies of an operand's K step kb: n boxes of `box` rows of 128 bytes at (x + kb dx, y + kb dy + i box).
 struct Boxes {
   const CUtensorMap* map;
-  int n, box, y, dx, dy;
+  int n, box, y, dx, dy, x = 0;
 };
 
 // What every policy's arguments start with.
@@ -196,7 +196,7 @@ __device__ __forceinline__ Tile own_tile(Tile t, int rank) {
 template <int CG>
 __device__ __forceinline__ void issue(const Boxes& o, int kb, unsigned char* dst, uint32_t bar, bool leader) {
   for (int i = 0; i < o.n; ++i)
-    if (leader) tma_load<CG>(dst + i * o.box * BK, o.map, kb * o.dx, o.y + kb * o.dy + i * o.box, bar);
+    if (leader) tma_load<CG>(dst + i * o.box * BK, o.map, o.x + kb * o.dx, o.y + kb * o.dy + i * o.box, bar);
 }
 
 // With PDL the kernel may start while the one that writes the tokens' codes still runs: with W_EARLY the first round
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(threads<P>(), 1) gemm_i8_kernel(const __grid_c
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN_MAX);
-      const uint32_t id = idesc<CG>(mma_n<CG>(t.nb));
+      const uint32_t id = idesc<CG>(mma_n<CG>(t.nb), P::A_MN);
       uint32_t accum = 0u;
       for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next()) {
         if (!mbar_wait_warp(&full[ring.s], ring.phase, &abort_flag)) {

@@ -72,7 +72,7 @@ __device__ __forceinline__ uint32_t pick(const uint32_t (&v)[N], int j) {
 template <int CG_>
 struct ForwardPolicy {
   static constexpr int CG = CG_;
-  static constexpr bool W_EARLY = true, W_IS_A = false, RESIDENT = false;
+  static constexpr bool W_EARLY = true, W_IS_A = false, A_MN = false, RESIDENT = false;
   static constexpr int EPI_WARPS = 8, EPI_COLS = BN_MAX / 2;  // columns of an epilogue warp
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
@@ -268,7 +268,7 @@ template <bool RESIDENT_>
 struct SmallForwardPolicy {
   static constexpr int CG = 1;
   static constexpr bool RESIDENT = RESIDENT_;
-  static constexpr bool W_EARLY = true, W_IS_A = true;
+  static constexpr bool W_EARLY = true, W_IS_A = true, A_MN = false;
   static constexpr int EPI_WARPS = 16;
   static_assert(EPI_WARPS == RES_WARPS, "the epilogue's warps quantize");
   struct Args {
@@ -490,67 +490,17 @@ __device__ __forceinline__ float dither(uint32_t acc) {
   return __uint_as_float(((acc * 0x9E3779B1u) & 0x7FFFFFu) | 0x3F800000u);
 }
 
-// W's piece [nv rows from v0] as K-major operand of the second product, [d / 128][Vp / 16][128][16] bytes
-// (zero past the vocabulary and past d), and the column sums of W.  A thread turns 16 rows x 4 columns.
-constexpr int TR_ROWS = 16 * 2;  // vocabulary rows per warp
-// The first piece's launch has `prepare` more CTAs (in x, of its first row in y) for the tokens' factors.
-__global__ void __launch_bounds__(256) transpose_kernel(const int8_t* W, int V, int d, int v0, int Vp, int8_t* wt,
-                                                        int32_t* colsum, int prepare, const PrepareArgs pa) {
+__global__ void __launch_bounds__(256) prepare_kernel(PrepareArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int blocks = gridDim.x - prepare;
-  if ((int)blockIdx.x >= blocks) {
-    if (blockIdx.y == 0) grad_prepare(pa, (blockIdx.x - blocks) * 256 + threadIdx.x, prepare * 256);
-    return;
-  }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int db = blockIdx.y, col = db * 128 + 4 * lane;
-  const int chunk0 = (blockIdx.x * 8 + warp) * (TR_ROWS / 16);
-  int sums[4] = {0, 0, 0, 0};
-  for (int i = 0; i < TR_ROWS / 16; ++i) {
-    const int chunk = chunk0 + i;
-    if (chunk * 16 >= Vp) break;
-    uint32_t w[16];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int v = v0 + chunk * 16 + r;
-      w[r] = (v < V && col < d) ? ld_u32(W + (size_t)v * d + col) : 0u;
-    }
-    uint4 o[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {  // 4 x 4 byte transpose of rows 4 g .. 4 g + 3
-      const uint32_t a = __byte_perm(w[4 * g], w[4 * g + 1], 0x5140), b = __byte_perm(w[4 * g], w[4 * g + 1], 0x7362);
-      const uint32_t e = __byte_perm(w[4 * g + 2], w[4 * g + 3], 0x5140),
-                     f = __byte_perm(w[4 * g + 2], w[4 * g + 3], 0x7362);
-      const uint32_t t[4] = {__byte_perm(a, e, 0x5410), __byte_perm(a, e, 0x7632), __byte_perm(b, f, 0x5410),
-                             __byte_perm(b, f, 0x7632)};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        sums[k] = dp4a_ss(t[k], 0x01010101u, sums[k]);
-        (g == 0 ? o[k].x : g == 1 ? o[k].y : g == 2 ? o[k].z : o[k].w) = t[k];
-      }
-    }
-    uint4* dst = reinterpret_cast<uint4*>(wt + ((size_t)db * (Vp / 16) + chunk) * 2048) + 4 * lane;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) dst[k] = o[k];
-  }
-  __shared__ int part[8][128];
-  *reinterpret_cast<int4*>(&part[warp][4 * lane]) = make_int4(sums[0], sums[1], sums[2], sums[3]);
-  __syncthreads();
-  const int i = threadIdx.x;
-  if (i < 128 && db * 128 + i < d) {
-    int s = 0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) s += part[w][i];
-    if (s) atomicAdd(colsum + db * 128 + i, s);
-  }
+  grad_prepare(a, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
 // The first product of the gradient: digits of a piece, and the row scales' gradient per 32 tokens.
 template <int CG_, bool DS>
 struct DigitPolicy {
   static constexpr int CG = CG_;
-  static constexpr bool W_EARLY = true, W_IS_A = false, RESIDENT = false;
+  static constexpr bool W_EARLY = true, W_IS_A = false, A_MN = false, RESIDENT = false;
   static constexpr int EPI_WARPS = 16, PARTS = EPI_WARPS / 4, EPI_COLS = BN_MAX / PARTS;  // columns of a warp
   struct Args {
     CUtensorMap map_a, map_b;  // codes, W
@@ -709,17 +659,18 @@ struct DigitPolicy {
 template <int CG_>
 struct GradPolicy {
   static constexpr int CG = CG_;
-  static constexpr bool W_EARLY = false, W_IS_A = true, RESIDENT = false;
+  static constexpr bool W_EARLY = false, W_IS_A = true, A_MN = true, RESIDENT = false;
   static constexpr int EPI_WARPS = 16, PARTS = EPI_WARPS / 4, EPI_SMEM = EPI_WARPS * 32 * 8;
   struct Args {
-    CUtensorMap map_a, map_b;  // transposed W, digits: blocks of 128 bytes
+    CUtensorMap map_a, map_b;  // W in boxes of 128 x 128, digits in blocks of 128 bytes
     Common c;
     int32_t* acc;  // this piece's set: [3][M][d]
     size_t plane;
-    int M, d, Vp, tb, kblocks;
+    int M, d, Vp, tb, kblocks, v0, nv;
     const float* colpart;  // [M / 32][Vp] partial sums of the row scales' gradient, or NULL
     float* ds;             // [nv]
-    int nv;
+    const int8_t* W;
+    int32_t* colsum;       // [d] += column sums of the piece
   };
   static __host__ __device__ __forceinline__ long long steps(const Args& a) {
     const int nd = (a.d + BM * CG - 1) / (BM * CG), nt = (a.M + a.tb * CG - 1) / (a.tb * CG);
@@ -744,25 +695,27 @@ struct GradPolicy {
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile&) {
     return CG * (A_BYTES + (uint32_t)a.tb * BK);
   }
-  // both operands were laid out as the product reads them: eight 16-byte K columns of all rows are contiguous
+  // 128 rows x 128 columns of W as they are: zero past the vocabulary and past d
   static __device__ __forceinline__ Boxes boxes_a(const Args& a, const Tile& t, int) {
-    return Boxes{&a.map_a, 1, BM, (int)((size_t)t.a0 * a.Vp / 128), 0, BM};
+    return Boxes{&a.map_a, 1, BK, a.v0, 0, BK, t.a0};
   }
+  // the digits were laid out as the product reads them: eight 16-byte K columns of all rows are contiguous
   static __device__ __forceinline__ Boxes boxes_b(const Args& a, const Tile& t, int rank) {
     return Boxes{&a.map_b, 1, a.tb, (int)((t.aux * a.plane + (size_t)(t.b0 + rank * a.tb) * a.Vp) / 128), 0, a.tb};
   }
-  static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_k_plain(addr, BM * 16); }
+  static __device__ __forceinline__ uint64_t adesc(uint32_t addr) { return umma_desc_mn_sw128(addr); }
   static __device__ __forceinline__ uint64_t bdesc(const Args& a, uint32_t addr) {
     return umma_desc_k_plain(addr, a.tb * 16);
   }
-  static __device__ __forceinline__ uint64_t a_step() { return 2 * BM; }
+  static __device__ __forceinline__ uint64_t a_step() { return UMMA_K * 128 >> 4; }
   static __device__ __forceinline__ uint64_t b_step(const Args& a) { return (uint64_t)(2 * a.tb); }
   struct Epilogue {
     int q, part, lane;
-    // While the first products accumulate: the piece's part of ds_row, 32 rows of W per CTA at a time, the partial
-    // sums of every 32 tokens in a slice per warp, joined in order.
+    // While the first products accumulate: the column sums of the piece, and its part of ds_row, 32 rows of W per
+    // CTA at a time, the partial sums of every 32 tokens in a slice per warp, joined in order.
     __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int part_, int lane_)
         : q(q_), part(part_), lane(lane_) {
+      column_sums(a, reinterpret_cast<int*>(sm));
       if (!a.colpart) return;
       double* red = reinterpret_cast<double*>(sm);  // [EPI_WARPS][32]
       const int sl = part * 4 + q, parts = (a.M + 31) / 32;
@@ -774,12 +727,56 @@ struct GradPolicy {
           for (int p = sl; p < parts; p += EPI_WARPS) s += (double)a.colpart[(size_t)p * a.Vp + v];
         }
         red[sl * 32 + lane] = s;
-        asm volatile("bar.sync 1, %0;" ::"n"(EPI_WARPS * 32) : "memory");
+        sync();
         if (sl == 0 && v < a.nv) {
           for (int k = 1; k < EPI_WARPS; ++k) s += red[k * 32 + lane];
           a.ds[v] = (float)s;
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(EPI_WARPS * 32) : "memory");
+        sync();
+      }
+    }
+    static __device__ __forceinline__ void sync() { asm volatile("bar.sync 1, %0;" ::"n"(EPI_WARPS * 32) : "memory"); }
+    // Blocks of 128 rows x 512 columns in an even range per CTA, rows before columns; a warp takes eight rows, a lane
+    // 16 columns, two sums of bytes + 128 per register (at most 8 x 255).
+    __device__ __forceinline__ void column_sums(const Args& a, int* red) const {
+      static_assert(EPI_WARPS * 8 == 128 && EPI_SMEM >= 512 * 4, "a block of columns");
+      const int w = part * 4 + q, i = w * 32 + lane;
+      const int nr = (a.nv + 127) / 128, total = nr * ((a.d + 511) / 512);
+      const int u1 = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
+      red[i] = 0;
+      sync();
+      for (int u = (int)((long long)total * blockIdx.x / gridDim.x); u < u1; ++u) {
+        const int cb = u / nr, r0 = (u - cb * nr) * 128 + w * 8, col = cb * 512 + lane * 16;
+        const int n = col < a.d ? min(8, a.nv - r0) : 0;
+        uint4 x[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          x[r] = r < n ? ld_u32x4(a.W + (size_t)(a.v0 + r0 + r) * a.d + col) : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t even[4] = {0u, 0u, 0u, 0u}, odd[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const uint32_t y[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t b = y[k] ^ 0x80808080u;
+            even[k] += b & 0x00FF00FFu;
+            odd[k] += (b >> 8) & 0x00FF00FFu;
+          }
+        }
+        if (n > 0) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint32_t h = (k & 1) ? odd[k >> 2] : even[k >> 2];
+            atomicAdd_block(red + k * 32 + lane, (int)((k & 2) ? h >> 16 : h & 0xFFFFu) - 8 * 128);
+          }
+        }
+        if (u + 1 == u1 || (u + 1) / nr != cb) {
+          sync();
+          const int c = cb * 512 + lane * 16 + w;
+          if (c < a.d && red[i]) atomicAdd(a.colsum + c, red[i]);
+          red[i] = 0;
+          sync();
+        }
       }
     }
     __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
@@ -1009,7 +1006,7 @@ Pieces pieces(int M, int d, int V) {
 constexpr int kNormParts = 4 * kSms;
 
 struct BackwardWs {
-  size_t q, s, rn, tok, fac, shift, list, zero, srow, listed, colsum, acc, zero_end, digits, wt, colpart, npart, total;
+  size_t q, s, rn, tok, fac, shift, list, zero, srow, listed, colsum, acc, zero_end, digits, colpart, npart, total;
 };
 BackwardWs backward_ws(int M, int d, int V) {
   const Pieces p = pieces(M, d, V);
@@ -1029,8 +1026,7 @@ BackwardWs backward_ws(int M, int d, int V) {
   w.acc = w.colsum + al256(sizeof(int32_t) * (size_t)d);
   w.zero_end = w.acc + al256(sizeof(int32_t) * 3 * (size_t)p.sets * M * d);
   w.digits = w.zero_end;
-  w.wt = w.digits + al256(3 * l.mp * p.rows);
-  w.colpart = w.wt + al256(l.dp * p.rows);
+  w.colpart = w.digits + al256(3 * l.mp * p.rows);
   w.npart = w.colpart + al256(sizeof(float) * 4 * l.cg * (size_t)ceil_div(M, BM * l.cg) * p.rows);
   w.total = w.npart + al256(sizeof(float) * (size_t)(M < kNormParts ? M : kNormParts) * d);
   return w;
@@ -1136,8 +1132,8 @@ struct Piece {
   int* listed;
   int2* list;
   unsigned char* digits;
-  int8_t* wt;
   float* colpart;
+  int32_t* colsum;  // [d]
   int32_t* acc;     // the piece's set
   float* ds_row;    // [V] or NULL
   int* err;
@@ -1172,7 +1168,7 @@ int piece_products(const Piece& p, cudaStream_t st) {
   g.c.b_tile = p.l.tb;
   g.c.stages = ring_stages(g.c, G::EPI_SMEM);
   g.c.err = p.err;
-  if (!encode_blocks_map(&g.map_a, p.wt, (int64_t)(p.l.dp * p.Vp / 128), BM) ||
+  if (!encode_u8_map_sw128(&g.map_a, p.W, p.V, p.d, BK) ||
       !encode_blocks_map(&g.map_b, p.digits, (int64_t)(3 * plane / 128), p.l.tb))
     return DFSSM_EUNSUPPORTED;
   g.acc = p.acc;
@@ -1184,7 +1180,10 @@ int piece_products(const Piece& p, cudaStream_t st) {
   g.kblocks = ceil_div(p.nv, BK);
   g.colpart = DS ? p.colpart : nullptr;
   g.ds = DS ? p.ds_row + p.v0 : nullptr;
+  g.v0 = p.v0;
   g.nv = p.nv;
+  g.W = p.W;
+  g.colsum = p.colsum;
   const long long steps = G::steps(g);
   const int most = max_groups<G>();
   e = launch<G>(g, (int)(steps < most ? steps : most), G::EPI_SMEM, st);
@@ -1288,6 +1287,8 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
                   reinterpret_cast<double2*>(base + w.fac), reinterpret_cast<uint32_t*>(base + w.srow)};
   const PrepareArgs pa{stats, labels, dloss, qa.s, s_row, M, V, tf};
   const int work = ceil_div(M > V ? M : V, 256);
+  e = launch_pdl(prepare_kernel, dim3(work < kSms ? work : kSms), dim3(256), 0, s, pa);
+  if (e != cudaSuccess) return record_cuda_failure(e);
 
   const Pieces pc = pieces(M, d, V);
   int32_t* colsum = reinterpret_cast<int32_t*>(base + w.colsum);
@@ -1301,8 +1302,8 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   p.listed = reinterpret_cast<int*>(base + w.listed);
   p.list = reinterpret_cast<int2*>(base + w.list);
   p.digits = reinterpret_cast<unsigned char*>(base + w.digits);
-  p.wt = reinterpret_cast<int8_t*>(base + w.wt);
   p.colpart = reinterpret_cast<float*>(base + w.colpart);
+  p.colsum = colsum;
   p.ds_row = ds_row;
   p.err = reinterpret_cast<int*>(base);
   p.V = V;
@@ -1316,10 +1317,6 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
     p.v0 = i * pc.rows;
     p.nv = V - p.v0 < pc.rows ? V - p.v0 : pc.rows;
     p.acc = acc + (size_t)(i / pc.per_set) * 3 * M * d;
-    const int prepare = i > 0 ? 0 : work < kSms ? work : kSms;
-    e = launch_pdl(transpose_kernel, dim3(ceil_div(ceil_div(p.nv, BK) * BK, TR_ROWS * 8) + prepare, (int)(p.l.dp / 128)),
-                   dim3(256), 0, s, W, V, d, p.v0, pc.rows, p.wt, colsum, prepare, pa);
-    if (e != cudaSuccess) return record_cuda_failure(e);
     st = products(p, s);
     if (st) return st;
   }

@@ -43,7 +43,7 @@ template <typename Y, int CG_, bool RESIDENT_ = false>
 struct LinearPolicy {
   static constexpr int CG = CG_;
   static constexpr bool RESIDENT = RESIDENT_;  // one to four tokens, quantized here
-  static constexpr bool W_EARLY = true, W_IS_A = true;
+  static constexpr bool W_EARLY = true, W_IS_A = true, A_MN = false;
   static constexpr int EPI_WARPS = 16, PARTS = EPI_WARPS / 4, EPI_COLS = BN_MAX / PARTS;  // columns of a warp
   struct Args {
     CUtensorMap map_a, map_b;  // W, codes

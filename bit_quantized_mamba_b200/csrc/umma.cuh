@@ -125,6 +125,17 @@ __device__ __forceinline__ uint64_t umma_desc_k_sw128(uint32_t smem_addr) {
   d |= (uint64_t)2 << 61;                        // 128-byte swizzle
   return d;
 }
+// Operand stored with K as rows ("MN-major"): 128 bytes of its M or N dimension per K row, 128-byte-swizzled, 8-row
+// groups 1024 bytes apart; 32 bytes of K are 32 rows, 4096 bytes.
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(1024 >> 4) << 16;  // leading byte offset: the next 128 of M or N (there are no more)
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
 // K-major operand without swizzle: 8-row x 16-byte blocks of 128 contiguous bytes, the next eight rows 128
 // bytes on, the next 16 bytes of K `k_stride` bytes on.
 __device__ __forceinline__ uint64_t umma_desc_k_plain(uint32_t smem_addr, int k_stride) {
