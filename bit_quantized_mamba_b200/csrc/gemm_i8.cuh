@@ -47,6 +47,12 @@ struct Tile {
   int aux;  // the policy's own
 };
 
+// a / b of numbers that are short nearly always: every warp divides for every tile, and a 64-bit division is a hundred
+// instructions.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Columns of the product: nb rounded up to what the instruction (16) and an even split over a pair (2 x 16) need.
 template <int CG>
 __device__ __forceinline__ int mma_n(int nb) { return (nb + 16 * CG - 1) & ~(16 * CG - 1); }
@@ -484,8 +490,9 @@ __device__ __forceinline__ bool row_tile(const RowArgs& r, int w_is_a, int j, Ti
     const int tb = (r.rows_b + r.tile_b - 1) / r.tile_b;
     const long long i = group + (long long)j * groups;
     if (i >= (long long)ta * tb) return false;
-    const int ia = w_is_a ? (int)(i / tb) : (int)(i % ta);
-    const int ib = w_is_a ? (int)(i % tb) : (int)(i / ta);
+    const int by = w_is_a ? tb : ta, q = (int)quotient(i, by), m = (int)(i - (long long)q * by);
+    const int ia = w_is_a ? q : m;
+    const int ib = w_is_a ? m : q;
     t.a0 = ia * TA;
     t.b0 = ib * r.tile_b;
     t.na = min(TA, r.rows_a - t.a0);
@@ -494,8 +501,8 @@ __device__ __forceinline__ bool row_tile(const RowArgs& r, int w_is_a, int j, Ti
   }
   const int rows_w = r.mode == kRangeA ? r.rows_a : r.rows_b;
   const long long units = (rows_w + 31) / 32;
-  const int w0 = (int)(units * group / groups) * 32;
-  const int w1 = min((int)(units * (group + 1) / groups) * 32, rows_w);
+  const int w0 = (int)quotient(units * group, groups) * 32;
+  const int w1 = min((int)quotient(units * (group + 1), groups) * 32, rows_w);
   if (r.mode == kRangeA) {
     t.a0 = w0 + TA * j;
     if (t.a0 >= w1) return false;

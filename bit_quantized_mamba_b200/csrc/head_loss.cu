@@ -679,8 +679,8 @@ struct GradPolicy {
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) {
     const int group = blockIdx.x / CG, groups = gridDim.x / CG;
     const long long total = steps(a);
-    const long long s0 = total * group / groups, s1 = total * (group + 1) / groups;
-    const long long u = s0 / a.kblocks + j, first = u * a.kblocks;
+    const long long s0 = quotient(total * group, groups), s1 = quotient(total * (group + 1), groups);
+    const long long u = quotient(s0, a.kblocks) + j, first = u * a.kblocks;
     if (first >= s1 || s0 >= s1) return false;
     t.kb0 = (int)((s0 > first ? s0 : first) - first);
     t.kb1 = (int)((s1 < first + a.kblocks ? s1 : first + a.kblocks) - first);
