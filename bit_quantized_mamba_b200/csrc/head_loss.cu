@@ -405,12 +405,14 @@ struct SmallForwardPolicy {
 
 constexpr int kListed = 16;  // coefficients of a token that may need more than 24 bits
 
-// Per-token factors of the gradient, and the largest |s_row| (bits) with a flag for negative scales.
+// Per-token factors of the gradient, and per CTA of the kernel that prepares them the largest |s_row| (bits) of its
+// rows with a flag for negative scales.
+constexpr int kPrepareCtas = 128, kPrepareThreads = 512;
 struct TokenFactors {
   float4* tok;    // [M] {m', s, f s, w_y s}: m' = m - k, f = g p_max 2^-k, w_y = -g (1 - p_y)
   int* shift;     // [M] k
   double2* fac;   // [M] {f, w_y}
-  uint32_t* srow; // {bits of max |s_row|, any negative}: zero before the launch
+  uint2* srow;    // [kPrepareCtas] {bits of max |s_row|, any negative}
 };
 struct PrepareArgs {
   const float* stats;
@@ -420,9 +422,17 @@ struct PrepareArgs {
   const float* s_row;
   int M, V;
   TokenFactors out;
+  uint4* zero;      // to be zeroed
+  size_t zeros;     // 16 bytes each
 };
-__device__ __forceinline__ void grad_prepare(const PrepareArgs& a, int i, int n) {
+// The tokens' factors, the row scales' range, and zeros in what the products add to.
+__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(PrepareArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ uint2 red[kPrepareThreads / 32];
+  const int i = blockIdx.x * kPrepareThreads + threadIdx.x, n = kPrepareCtas * kPrepareThreads;
   const TokenFactors& o = a.out;
+  for (size_t z = i; z < a.zeros; z += n) a.zero[z] = make_uint4(0u, 0u, 0u, 0u);
   uint32_t mb = 0u, neg = 0u;
 #pragma unroll 4
   for (int v = i; v < a.V; v += n) {
@@ -432,9 +442,12 @@ __device__ __forceinline__ void grad_prepare(const PrepareArgs& a, int i, int n)
   }
   mb = __reduce_max_sync(0xffffffffu, mb);
   neg = __reduce_or_sync(0xffffffffu, neg);
-  if ((threadIdx.x & 31) == 0) {
-    if (mb) atomicMax(o.srow, mb);
-    if (neg) atomicOr(o.srow + 1, 1u);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_uint2(mb, neg);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const uint2 r = threadIdx.x < kPrepareThreads / 32 ? red[threadIdx.x] : make_uint2(0u, 0u);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, r.x), g = __reduce_or_sync(0xffffffffu, r.y);
+    if (threadIdx.x == 0) o.srow[blockIdx.x] = make_uint2(m, g);
   }
   for (int t = i; t < a.M; t += n) {
     const int y = a.labels[t];
@@ -471,9 +484,14 @@ struct FixedPoint {
   int range;     // 2^24, or 2^23
   double step;   // what one step stands for, of exp(l - m') s_row
 };
-__device__ __forceinline__ FixedPoint fixed_point(const uint32_t* srow) {
-  const float smax = __uint_as_float(srow[0]);
-  const bool neg = srow[1] != 0u;
+__device__ __forceinline__ FixedPoint fixed_point(const uint2* srow) {  // (whole warps)
+  uint2 r[kPrepareCtas / 32];
+#pragma unroll
+  for (int k = 0; k < kPrepareCtas / 32; ++k) r[k] = srow[k * 32 + (threadIdx.x & 31)];
+#pragma unroll
+  for (int k = 1; k < kPrepareCtas / 32; ++k) r[0] = make_uint2(max(r[0].x, r[k].x), r[0].y | r[k].y);
+  const float smax = __uint_as_float(__reduce_max_sync(0xffffffffu, r[0].x));
+  const bool neg = __reduce_or_sync(0xffffffffu, r[0].y) != 0u;
   FixedPoint p;
   p.range = neg ? 1 << 23 : 1 << 24;
   p.unit = smax < 1e-30f ? 0.0f : (float)(p.range - 64) / scale2(smax);  // (so small, nothing of du is left either)
@@ -490,12 +508,6 @@ __device__ __forceinline__ float dither(uint32_t acc) {
   return __uint_as_float(((acc * 0x9E3779B1u) & 0x7FFFFFu) | 0x3F800000u);
 }
 
-__global__ void __launch_bounds__(256) prepare_kernel(PrepareArgs a) {
-  pdl_launch_dependents();
-  pdl_wait();
-  grad_prepare(a, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
-}
-
 // The first product of the gradient: digits of a piece, and the row scales' gradient per 32 tokens.
 template <int CG_, bool DS>
 struct DigitPolicy {
@@ -509,7 +521,7 @@ struct DigitPolicy {
     const float4* tok;      // [M]
     const int32_t* labels;  // [M]
     const float* s_row;     // [V]
-    const uint32_t* srow;
+    const uint2* srow;
     const int* shift;       // [M]
     int* listed;            // [M] entries of a token's list, zero before the first piece
     int2* list;             // [M][kListed] {row of W, number / 2^24}
@@ -801,7 +813,7 @@ struct GradPolicy {
 struct GradFinishArgs {
   const int32_t* acc;     // [sets][3][M][d]
   const int32_t* colsum;  // [d]
-  const uint32_t* srow;
+  const uint2* srow;
   const double2* fac;     // [M]
   const int* listed;      // [M]
   const int2* list;       // [M][kListed]
@@ -1006,7 +1018,7 @@ Pieces pieces(int M, int d, int V) {
 constexpr int kNormParts = 4 * kSms;
 
 struct BackwardWs {
-  size_t q, s, rn, tok, fac, shift, list, zero, srow, listed, colsum, acc, zero_end, digits, colpart, npart, total;
+  size_t q, s, rn, tok, fac, shift, list, srow, zero, listed, colsum, acc, zero_end, digits, colpart, npart, total;
 };
 BackwardWs backward_ws(int M, int d, int V) {
   const Pieces p = pieces(M, d, V);
@@ -1019,9 +1031,9 @@ BackwardWs backward_ws(int M, int d, int V) {
   w.fac = w.tok + al256(sizeof(float4) * (size_t)M);
   w.shift = w.fac + al256(sizeof(double2) * (size_t)M);
   w.list = w.shift + al256(sizeof(int) * (size_t)M);
-  w.zero = w.list + al256(sizeof(int2) * kListed * (size_t)M);
-  w.srow = w.zero;
-  w.listed = w.srow + 256;
+  w.srow = w.list + al256(sizeof(int2) * kListed * (size_t)M);
+  w.zero = w.srow + al256(sizeof(uint2) * kPrepareCtas);
+  w.listed = w.zero;
   w.colsum = w.listed + al256(sizeof(int) * (size_t)M);
   w.acc = w.colsum + al256(sizeof(int32_t) * (size_t)d);
   w.zero_end = w.acc + al256(sizeof(int32_t) * 3 * (size_t)p.sets * M * d);
@@ -1277,17 +1289,15 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   if (!device_ok()) return DFSSM_EDEVICE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(workspace);
-  cudaError_t e = cudaMemsetAsync(base + w.zero, 0, w.zero_end - w.zero, s);
-  if (e != cudaSuccess) return record_cuda_failure(e);
   RowsQuantArgs qa = quant_args(x, x_type, ldx, M, d, norm_w, base, w.q, w.s);
   qa.rn = reinterpret_cast<float*>(base + w.rn);
-  e = launch_rows_quant(qa, s);
+  cudaError_t e = launch_rows_quant(qa, s);
   if (e != cudaSuccess) return record_cuda_failure(e);
   TokenFactors tf{reinterpret_cast<float4*>(base + w.tok), reinterpret_cast<int*>(base + w.shift),
-                  reinterpret_cast<double2*>(base + w.fac), reinterpret_cast<uint32_t*>(base + w.srow)};
-  const PrepareArgs pa{stats, labels, dloss, qa.s, s_row, M, V, tf};
-  const int work = ceil_div(M > V ? M : V, 256);
-  e = launch_pdl(prepare_kernel, dim3(work < kSms ? work : kSms), dim3(256), 0, s, pa);
+                  reinterpret_cast<double2*>(base + w.fac), reinterpret_cast<uint2*>(base + w.srow)};
+  const PrepareArgs pa{stats, labels, dloss, qa.s, s_row, M, V, tf, reinterpret_cast<uint4*>(base + w.zero),
+                       (w.zero_end - w.zero) / 16};
+  e = launch_pdl(prepare_kernel, dim3(kPrepareCtas), dim3(kPrepareThreads), 0, s, pa);
   if (e != cudaSuccess) return record_cuda_failure(e);
 
   const Pieces pc = pieces(M, d, V);
