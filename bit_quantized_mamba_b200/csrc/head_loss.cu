@@ -17,15 +17,21 @@
 // tau = 2^-k ~ min(1, S / 16): below tau a coefficient is three base-256 digits, and at most 16 of a token's can
 // be above it (they sum to at most S), whose further bits go into a list.  The sum over v is then three exact
 // int8 products of digits with W, each at twice the rate of a bf16 product, free of bf16's rounding and of any
-// order of summation, and a few listed rows of W.  The vocabulary is taken in pieces whose digits stay in L2:
-//   1. transpose: the piece's W as K-major operand of the second product, and W's column sums (with the first piece,
-//      the tokens' factors);
-//   2. the first product again, its epilogue turning logits into digits (and the row scales' gradient
+// order of summation, and a few listed rows of W.  A kernel first works out the tokens' factors and max|s_row|; then
+// the vocabulary is taken in pieces whose digits stay in L2:
+//   1. the first product again, its epilogue turning logits into digits (and the row scales' gradient
 //      into partial column sums);
-//   3. the second product: digits x transposed W, added to int32 accumulators in memory by integer
-//      atomics (any order gives the same sum), the (tile, digit, K) space split evenly over the CTAs.
+//   2. the second product: digits x W, whose rows are its K dimension as they lie in memory ("MN-major" operand;
+//      a transposed copy cost 40 us at 2048 tokens, 50288 rows), added to int32 accumulators in memory by
+//      integer atomics (any order gives the same sum), the (tile, digit, K) space split evenly over the CTAs.
+//      Its epilogue's warps meanwhile take the column sums of W and join those of the row scales' gradient.
 // At the end one kernel joins the digits, the listed rows and the label's row and applies the norm's backward.
 // The digits are stored as signed bytes (digit - 128); the column sums of W give the 128s back.
+//
+// 2048 tokens x 50288 rows x 2048: loss 165 us (2550 TOPS), loss and gradients 958 us (2200 TOPS of five products).
+// Bound by power: with operands that do not change the products alone run at 3270 TOPS under the same cap.
+// Measured and dropped: the digits of a piece in one kernel with the second product of the piece before, tiles of both in
+// turn (1026 us; 1046 in blocks of 1024 tokens): the same energy, and twice the digits to keep in L2.
 
 #include "gemm_i8.cuh"
 #include "rows.cuh"
@@ -988,7 +994,9 @@ ForwardWs forward_ws(int M, int d, int V) {
 struct Pieces {
   int rows, n, per_set, sets;
 };
-constexpr size_t kPieceBytes = 80u << 20;  // digits and transposed W of a piece: they stay in the 126 MB L2
+// Digits and W of a piece: they stay in the 126 MB L2 with part of the accumulators (2048 tokens x 50288 rows: 50 MB
+// 1026 us, 60: 985, 80: 971, 110: 975, 140: 975).
+constexpr size_t kPieceBytes = 80u << 20;
 Pieces pieces(int M, int d, int V) {
   const Layout l = layout(M, d);
   size_t t = kPieceBytes / (3 * l.mp + l.dp + l.mp / 8) / BN_MAX;  // tiles of 256 rows
