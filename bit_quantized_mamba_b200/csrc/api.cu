@@ -277,6 +277,8 @@ int dfssm::check_int8_matrix(const int8_t* W, int V, int d) {
   return aligned(W, 16) ? DFSSM_OK : DFSSM_EALIGN;
 }
 
+int dfssm::check_tokens(int M) { return M < 0 ? DFSSM_EINVAL : M > 1 << 30 ? DFSSM_EUNSUPPORTED : DFSSM_OK; }
+
 int dfssm::check_rows(const void* x, int x_type, int64_t ldx, int d) {
   if (!x || (x_type != DFSSM_F32 && x_type != DFSSM_BF16) || ldx < d) return DFSSM_EINVAL;
   const int64_t size = x_type == DFSSM_F32 ? 4 : 2;
@@ -369,7 +371,7 @@ size_t dfssm_workspace_size(int op, int a, int b, int c) {
     case DFSSM_OP_EMBED_BACKWARD:
     case DFSSM_OP_HEAD_LOSS:
     case DFSSM_OP_HEAD_LOSS_BACKWARD:
-      if (a < 0 || b < 16 || b % 16 || b > 8192 || c < 1 || c > 1 << 30) return 0;
+      if (a < 0 || a > 1 << 30 || b < 16 || b % 16 || b > 8192 || c < 1 || c > 1 << 30) return 0;
       if (a == 0) return dfssm::kStatusBytes;
       if (op == DFSSM_OP_LINEAR_INT8) return dfssm::linear_int8_workspace_bytes(a, b);
       if (op == DFSSM_OP_EMBED_BACKWARD) return dfssm::embed_backward_workspace_bytes(a, b, c);

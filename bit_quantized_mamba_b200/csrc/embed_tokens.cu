@@ -609,7 +609,9 @@ extern "C" int dfssm_embed_tokens(const int8_t* W, const float* s_row, int V, in
   using namespace dfssm;
   int st = check_int8_matrix(W, V, d);
   if (st) return st;
-  if (!s_row || n < 0) return DFSSM_EINVAL;
+  if (!s_row) return DFSSM_EINVAL;
+  st = check_tokens(n);
+  if (st) return st;
   if (n == 0) return DFSSM_OK;
   st = check_rows(h, h_type, ldh, d);
   if (st) return st;
@@ -629,7 +631,9 @@ extern "C" int dfssm_embed_tokens_backward(const int8_t* W, int V, int d, const 
   using namespace dfssm;
   int st = check_int8_matrix(W, V, d);
   if (st) return st;
-  if (n < 0 || (!dE && !ds_row)) return DFSSM_EINVAL;
+  if (!dE && !ds_row) return DFSSM_EINVAL;
+  st = check_tokens(n);
+  if (st) return st;
   if (!al(dE, 16) || !al(ds_row, 4)) return DFSSM_EALIGN;
   if (n > 0) {
     st = check_rows(dh, dh_type, lddh, d);

@@ -1246,7 +1246,9 @@ extern "C" int dfssm_head_loss(const int8_t* W, const float* s_row, int V, int d
   using namespace dfssm;
   int st = check_int8_matrix(W, V, d);
   if (st) return st;
-  if (!s_row || M < 0) return DFSSM_EINVAL;
+  if (!s_row) return DFSSM_EINVAL;
+  st = check_tokens(M);
+  if (st) return st;
   if (M == 0) return DFSSM_OK;
   st = check_rows(x, x_type, ldx, d);
   if (st) return st;
@@ -1273,7 +1275,9 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   using namespace dfssm;
   int st = check_int8_matrix(W, V, d);
   if (st) return st;
-  if (!s_row || M < 0 || (dnorm_w && !norm_w)) return DFSSM_EINVAL;
+  if (!s_row || (dnorm_w && !norm_w)) return DFSSM_EINVAL;
+  st = check_tokens(M);
+  if (st) return st;
   if (V > 1 << 24) return DFSSM_EUNSUPPORTED;  // W's column sums are int32
   if (M == 0) {  // no tokens: the sums over them are zero
     if (!al(ds_row, 4) || !al(dnorm_w, 4)) return DFSSM_EALIGN;

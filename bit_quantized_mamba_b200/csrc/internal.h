@@ -224,8 +224,10 @@ bool encode_u8_map_sw128(CUtensorMap* map, const void* base, int rows, int row_b
 // Memory as blocks of 128 contiguous bytes, copied unchanged in boxes of box_blocks blocks.
 bool encode_blocks_map(CUtensorMap* map, const void* base, int64_t blocks, int box_blocks);
 // Argument checks shared by the many-token operators on an int8 matrix W [V][d] (common to the embedding,
-// the linear and the loss), and of rows of d values of type x_type, ldx apart (16-byte aligned rows).
+// the linear and the loss), of the number of tokens, and of rows of d values of type x_type, ldx apart (16-byte
+// aligned rows).
 int check_int8_matrix(const int8_t* W, int V, int d);
+int check_tokens(int M);
 int check_rows(const void* x, int x_type, int64_t ldx, int d);
 // The current device is an sm_100 part.
 bool device_ok();

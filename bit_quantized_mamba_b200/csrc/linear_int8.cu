@@ -219,7 +219,9 @@ extern "C" int dfssm_linear_int8(const int8_t* W, const float* s_row, int V, int
   using namespace dfssm;
   int st = check_int8_matrix(W, V, d);
   if (st) return st;
-  if (!s_row || M < 0 || ldy < V || (y_type != DFSSM_F32 && y_type != DFSSM_BF16)) return DFSSM_EINVAL;
+  if (!s_row || ldy < V || (y_type != DFSSM_F32 && y_type != DFSSM_BF16)) return DFSSM_EINVAL;
+  st = check_tokens(M);
+  if (st) return st;
   if (ldy > INT32_MAX) return DFSSM_EUNSUPPORTED;
   if (M == 0) return DFSSM_OK;
   st = check_rows(x, x_type, ldx, d);

@@ -346,7 +346,8 @@ int dfssm_generate(const dfssm_layer_t* layers, int n_layers, const dfssm_dims_t
  * matrix with a scale per row): the lookup, the product, the loss over the vocabulary, and the gradients.
  * Common to these calls:
  *   W device i8 [V][d] (16-byte aligned), s_row device f32 [V]; d % 16 == 0, d >= 16 (otherwise DFSSM_EINVAL),
- *   d <= 8192 and V <= 2^30 (otherwise DFSSM_EUNSUPPORTED; dfssm_head_loss_backward: V <= 2^24).
+ *   d <= 8192 and V <= 2^30 (otherwise DFSSM_EUNSUPPORTED; dfssm_head_loss_backward: V <= 2^24),
+ *   at most 2^30 tokens (otherwise DFSSM_EUNSUPPORTED).
  *   Activations are rows of d values of type DFSSM_F32 or DFSSM_BF16, ld* elements apart (ld* >= d, else
  *   DFSSM_EINVAL), every row 16-byte aligned (else DFSSM_EALIGN); values between rows are neither read nor
  *   written.  Outputs must not overlap inputs or each other.

@@ -590,6 +590,44 @@ def test_parameters_updated_in_the_stream(dev, M):
             assert torch.equal(u, v)
 
 
+def test_offsets_past_32_bits(dev):
+    """Outputs, gradients and accumulators of more than 2^31 elements, and rows 2^31 - 1 apart: the last tokens get
+    the bits that they get in a small call."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(24, dev)
+    W, sr = matrix(g, 50000, 16, dev)
+    x = rows(g, 45000, 16, dev, torch.bfloat16)
+    y = dfssm.linear_int8(W, sr, x, out_dtype=torch.bfloat16)
+    assert y.numel() > 2 ** 31
+    assert torch.equal(y[-300:], dfssm.linear_int8(W, sr, x[-300:], out_dtype=torch.bfloat16))
+    del y
+    far = torch.empty(3 * (2 ** 31 - 1), device=dev, dtype=torch.bfloat16).as_strided((3, 50000), (2 ** 31 - 1, 1))
+    dfssm.linear_int8(W, sr, x[:3], y=far)
+    assert torch.equal(far, dfssm.linear_int8(W, sr, x[:3], out_dtype=torch.bfloat16))
+    del far
+    M, V, d = 100000, 300, 8192  # three digits of 819 M accumulators
+    W, sr = matrix(g, V, d, dev)
+    x = rows(g, M, d, dev, torch.bfloat16)
+    lab = torch.randint(0, V, (M,), generator=g, device=dev, dtype=torch.int32)
+    dl = torch.rand(M, generator=g, device=dev)
+    loss, stats = dfssm.head_loss(W, sr, x, lab)
+    dx, _, _ = dfssm.head_loss_backward(W, sr, x, lab, stats, dl, scales=False)
+    few = slice(M - 300, M)
+    loss1, _ = dfssm.head_loss(W, sr, x[few], lab[few])
+    # (the forward's sums are grouped by its tiles: equal up to their roundings, so the same statistics go in)
+    assert torch.allclose(loss[few], loss1, rtol=0, atol=40 * U * float(loss1.abs().max() + 10))
+    dx1, _, _ = dfssm.head_loss_backward(W, sr, x[few], lab[few], stats[:, few].contiguous(), dl[few], scales=False)
+    assert torch.equal(dx[few], dx1)
+    del x, dx, dx1
+    V = 300000  # 2.5 G elements of the dense gradient
+    W = torch.ones(V, d, device=dev, dtype=torch.int8)
+    tok = torch.tensor([V - 1, 5, V - 1, 262144], device=dev, dtype=torch.int32)
+    dh = rows(g, 4, d, dev, torch.float32)
+    dE, ds = dfssm.embed_tokens_backward(W, tok, dh)
+    assert torch.equal(dE[V - 1], dh[0] + dh[2]) and torch.equal(dE[5], dh[1]) and torch.equal(dE[262144], dh[3])
+    assert int(torch.count_nonzero(dE[300:262144:997])) == 0 and int(torch.count_nonzero(ds)) == 3
+
+
 def test_outputs_allocated_for_an_explicit_stream(dev):
     from bit_quantized_mamba_b200 import dfssm
     g = gen(22, dev)

@@ -116,6 +116,19 @@ def test_head_loss_backward_refusals(L):
         assert f(**kw) == want, kw
 
 
+def test_too_many_tokens(L):
+    """More than 2^30 tokens are refused before anything is looked at, and have no workspace."""
+    M = (1 << 30) + 1
+    assert L.dfssm_linear_int8(16, 16, 10, 32, 16, 0, 32, M, None, 16, 0, 10, 256, BIG, None, None) == -3
+    assert L.dfssm_embed_tokens(16, 16, 10, 32, 16, M, 16, 0, 32, 256, BIG, None) == -3
+    assert L.dfssm_embed_tokens_backward(16, 10, 32, 16, M, 16, 0, 32, 16, 16, 0, 256, BIG, None) == -3
+    assert L.dfssm_head_loss(16, 16, 10, 32, 16, 0, 32, M, None, 16, 16, 16, 256, BIG, None) == -3
+    assert L.dfssm_head_loss_backward(16, 16, 10, 32, 16, 0, 32, M, None, 16, 16, 16, 16, 32, 16, None, 256, BIG,
+                                      None) == -3
+    for op in (10, 12, 13, 14):
+        assert L.dfssm_workspace_size(op, M, 32, 10) == 0 and L.dfssm_workspace_size(op, M - 1, 32, 10) > 0
+
+
 def test_binding_checks_shapes_and_types():
     from bit_quantized_mamba_b200 import dfssm as D
     with pytest.raises(ValueError):
