@@ -49,7 +49,7 @@ struct Tile {
 
 // a / b of numbers that are short nearly always: every warp divides for every tile, and a 64-bit division is a hundred
 // instructions.
-__device__ __forceinline__ long long quotient(long long a, int b) {
+__host__ __device__ __forceinline__ long long quotient(long long a, int b) {
   return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 

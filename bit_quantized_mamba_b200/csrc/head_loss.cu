@@ -23,7 +23,8 @@
 //      into partial column sums);
 //   2. the second product: digits x W, whose rows are its K dimension as they lie in memory ("MN-major" operand;
 //      a transposed copy cost 40 us at 2048 tokens, 50288 rows), added to int32 accumulators in memory by
-//      integer atomics (any order gives the same sum), the (tile, digit, K) space split evenly over the CTAs.
+//      integer atomics (any order gives the same sum): rounds of whole (tile, digit) units, one per CTA pair, and
+//      what is left split evenly along K.
 //      Its epilogue's warps meanwhile take the column sums of W and join those of the row scales' gradient.
 // At the end one kernel joins the digits, the listed rows and the label's row and applies the norm's backward.
 // The digits are stored as signed bytes (digit - 128); the column sums of W give the 128s back.
@@ -672,8 +673,19 @@ struct DigitPolicy {
 };
 
 // The second product: accumulators [set][3][M][d] += digits x transposed W of a piece.  Lanes are columns of W
-// (128 a CTA), columns are tokens (tb a CTA); the (token tile, digit, column tile, K) space is cut into one even
-// contiguous range per CTA or pair.
+// (128 a CTA), columns are tokens (tb a CTA).  A unit is a (token tile, digit, column tile) over all of the piece; groups
+// (CTAs or pairs) take whole units in rounds, so that all of them read the same rows of W and digits at a time, and
+// the units of a last, incomplete round are cut into one even range of K steps per group.  (All of it cut evenly, with
+// every group at another K: 958 us instead of 920 at 2048 tokens, 283 MB a piece from DRAM instead of 127.)
+// (units of work, and rounds in which every group takes a whole one)
+__host__ __device__ __forceinline__ long long grad_units(int M, int d, int lanes, int tokens) {
+  return 3LL * ((d + lanes - 1) / lanes) * ((M + tokens - 1) / tokens);
+}
+__host__ __device__ __forceinline__ long long grad_rounds(long long units, int groups) {
+  const long long whole = quotient(units, groups), rest = units - whole * groups;
+  if (rest * 10 >= 9LL * groups) return whole + 1;
+  return whole > 0 && rest > 0 && rest * 8 < groups ? whole - 1 : whole;
+}
 template <int CG_>
 struct GradPolicy {
   static constexpr int CG = CG_;
@@ -690,18 +702,28 @@ struct GradPolicy {
     const int8_t* W;
     int32_t* colsum;       // [d] += column sums of the piece
   };
-  static __host__ __device__ __forceinline__ long long steps(const Args& a) {
-    const int nd = (a.d + BM * CG - 1) / (BM * CG), nt = (a.M + a.tb * CG - 1) / (a.tb * CG);
-    return (long long)3 * nd * nt * a.kblocks;
+  static __host__ __device__ __forceinline__ long long units(const Args& a) {
+    return grad_units(a.M, a.d, BM * CG, a.tb * CG);
   }
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) {
     const int group = blockIdx.x / CG, groups = gridDim.x / CG;
-    const long long total = steps(a);
-    const long long s0 = quotient(total * group, groups), s1 = quotient(total * (group + 1), groups);
-    const long long u = quotient(s0, a.kblocks) + j, first = u * a.kblocks;
-    if (first >= s1 || s0 >= s1) return false;
-    t.kb0 = (int)((s0 > first ? s0 : first) - first);
-    t.kb1 = (int)((s1 < first + a.kblocks ? s1 : first + a.kblocks) - first);
+    const long long all = units(a), whole = grad_rounds(all, groups);
+    long long u = (long long)j * groups + group;
+    if (j < whole) {
+      if (u >= all) return false;
+      t.kb0 = 0;
+      t.kb1 = a.kblocks;
+    } else {
+      const long long rest = (all - whole * groups) * a.kblocks;
+      if (rest <= 0) return false;
+      const long long s0 = quotient(rest * group, groups), s1 = quotient(rest * (group + 1), groups);
+      u = quotient(s0, a.kblocks) + (j - whole);
+      const long long first = u * a.kblocks;
+      if (first >= s1 || s0 >= s1) return false;
+      t.kb0 = (int)((s0 > first ? s0 : first) - first);
+      t.kb1 = (int)((s1 < first + a.kblocks ? s1 : first + a.kblocks) - first);
+      u += whole * groups;
+    }
     const int nd = (a.d + BM * CG - 1) / (BM * CG), ui = (int)u;
     t.a0 = ui % nd * BM * CG;
     t.na = BM * CG;
@@ -994,28 +1016,29 @@ ForwardWs forward_ws(int M, int d, int V) {
 struct Pieces {
   int rows, n, per_set, sets;
 };
-// Digits and W of a piece: they stay in the 126 MB L2 with part of the accumulators (2048 tokens x 50288 rows: 50 MB
-// 1026 us, 60: 985, 80: 971, 110: 975, 140: 975).
-constexpr size_t kPieceBytes = 80u << 20;
+// Bytes of digits and W of a piece at most.  Where the second product is one split along K, every CTA is at another K and
+// the piece has to stay in the 126 MB L2 (333 tokens x 50288 x 2048: 80 MB 231 us, 120: 239, 220: 247).  Where CTAs
+// take whole units they read the same K at a time, and fewer pieces are better (2048 tokens: 80 MB 920 us, 120: 880,
+// 160: 868, 220: 861, 440: 860).
+constexpr size_t kPieceBytes = 80u << 20, kSyncBytes = 220u << 20;
 Pieces pieces(int M, int d, int V) {
   const Layout l = layout(M, d);
-  size_t t = kPieceBytes / (3 * l.mp + l.dp + l.mp / 8) / BN_MAX;  // tiles of 256 rows
-  if (t < 8) t = 8;
-  if (t > 256) t = 256;
-  const int vt = ceil_div(V, BN_MAX), mt = ceil_div(M, BM * l.cg);
-  if ((int)t < vt) {
-    // whole waves of tiles where a few fit, else equal pieces
-    int g = mt, b = kSms / l.cg;
-    while (b) {
-      const int r = g % b;
-      g = b, b = r;
+  const bool sync = grad_rounds(grad_units(M, d, BM * l.cg, l.tb * l.cg), kSms / l.cg) > 0;
+  size_t t = (sync ? kSyncBytes : kPieceBytes) / (3 * l.mp + l.dp + l.mp / 8) / BN_MAX;  // tiles of 256 rows
+  const int vt = ceil_div(V, BN_MAX), mt = ceil_div(M, BM * l.cg), groups = kSms / l.cg;
+  const int most = (int)(t < 8 ? 8 : t > 256 ? 256 : t);
+  // of the sizes up to that, the one with the least rounds of digit tiles, a piece counting as two more
+  int best = 0;
+  long long least = 0;
+  for (int k = most < vt ? most : vt; k > 0 && k * 4 > most; --k) {
+    const int full = vt / k, rest = vt % k;
+    const long long cost = (long long)full * (ceil_div(mt * k, groups) + 2) + (rest ? ceil_div(mt * rest, groups) + 2 : 0);
+    if (!best || cost < least) {
+      best = k;
+      least = cost;
     }
-    const int wave = kSms / l.cg / g;
-    if (wave <= (int)t) t = t / wave * wave;
-    else t = ceil_div(vt, ceil_div(vt, (int)t));
-  } else {
-    t = vt;
   }
+  t = best ? best : vt;
   Pieces p;
   p.rows = (int)t * BN_MAX;
   p.n = ceil_div(V, p.rows);
@@ -1205,7 +1228,7 @@ int piece_products(const Piece& p, cudaStream_t st) {
   g.nv = p.nv;
   g.W = p.W;
   g.colsum = p.colsum;
-  const long long steps = G::steps(g);
+  const long long steps = G::units(g) * g.kblocks;
   const int most = max_groups<G>();
   e = launch<G>(g, (int)(steps < most ? steps : most), G::EPI_SMEM, st);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
