@@ -29,10 +29,13 @@
 // At the end one kernel joins the digits, the listed rows and the label's row and applies the norm's backward.
 // The digits are stored as signed bytes (digit - 128); the column sums of W give the 128s back.
 //
-// 2048 tokens x 50288 rows x 2048: loss 165 us (2550 TOPS), loss and gradients 958 us (2200 TOPS of five products).
-// Bound by power: with operands that do not change the products alone run at 3270 TOPS under the same cap.
+// 2048 tokens x 50288 rows x 2048: loss 165 us (2550 TOPS), loss and gradients 861 us (2450 TOPS of five products).
+// Bound by power: with operands that do not change the products alone run at 3270 TOPS under the same cap.  What the
+// gradient takes beyond its products is the digits' epilogue (205 us for a product that alone takes 150).
 // Measured and dropped: the digits of a piece in one kernel with the second product of the piece before, tiles of both in
-// turn (1026 us; 1046 in blocks of 1024 tokens): the same energy, and twice the digits to keep in L2.
+// turn (1026 us where it took 962 apart); digits balanced around zero, which need no column sums but take a bit off the
+// range (no gain); in the digits' epilogue the next columns fetched ahead, wider loads of the scales, the next
+// tile's token data fetched into L1 (no gain each).
 
 #include "gemm_i8.cuh"
 #include "rows.cuh"
