@@ -370,6 +370,19 @@ def test_head_gradient_in_pieces_of_the_vocabulary(dev, M, V, d, signed):
     check_head(dfssm, W, sr, x, torch.rand(d, generator=g, device=dev) + 0.5, labels, torch.rand(M, generator=g, device=dev))
 
 
+@pytest.mark.parametrize("M,V,d", [(2100, 3001, 2048), (1300, 2500, 1536), (1300, 1000, 1024), (2304, 700, 640),
+                                   (128, 1500, 8192), (600, 26000, 1040), (2048, 50288, 2048)])
+def test_head_gradient_in_rounds_of_whole_units(dev, M, V, d):
+    """Sizes whose second product has whole units for every SM: with a full last round, one split along K, none, and
+    in two pieces of the vocabulary."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(M + V + d, dev)
+    W, sr = matrix(g, V, d, dev)
+    x = rows(g, M, d, dev, torch.float32)
+    labels = torch.randint(-V // 9, V, (M,), generator=g, device=dev, dtype=torch.int32)
+    check_head(dfssm, W, sr, x, torch.rand(d, generator=g, device=dev) + 0.5, labels, torch.rand(M, generator=g, device=dev))
+
+
 def test_head_gradient_of_constant_rows_stays_in_range(dev):
     """Every code at its limit and uniform coefficients: the largest digit sums there can be."""
     from bit_quantized_mamba_b200 import dfssm
