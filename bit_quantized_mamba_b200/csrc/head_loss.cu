@@ -29,7 +29,7 @@
 // At the end one kernel joins the digits, the listed rows and the label's row and applies the norm's backward.
 // The digits are stored as signed bytes (digit - 128); the column sums of W give the 128s back.
 //
-// 2048 tokens x 50288 rows x 2048: loss 165 us (2550 TOPS), loss and gradients 861 us (2450 TOPS of five products).
+// 2048 tokens x 50288 rows x 2048: loss 165 us (2550 TOPS), loss and gradients 868 us (2430 TOPS of five products).
 // Bound by power: with operands that do not change the products alone run at 3270 TOPS under the same cap.  What the
 // gradient takes beyond its products is the digits' epilogue (205 us for a product that alone takes 150).
 // Measured and dropped: the digits of a piece in one kernel with the second product of the piece before, tiles of both in
@@ -1022,8 +1022,8 @@ struct Pieces {
 // Bytes of digits and W of a piece at most.  Where the second product is one split along K, every CTA is at another K and
 // the piece has to stay in the 126 MB L2 (333 tokens x 50288 x 2048: 80 MB 231 us, 120: 239, 220: 247).  Where CTAs
 // take whole units they read the same K at a time, and fewer pieces are better (2048 tokens: 80 MB 920 us, 120: 880,
-// 160: 868, 220: 861, 440: 860).
-constexpr size_t kPieceBytes = 80u << 20, kSyncBytes = 220u << 20;
+// 160: 868, 220: 861, 440: 860); 160 MB keep the workspace below half of what fp32 logits would take.
+constexpr size_t kPieceBytes = 80u << 20, kSyncBytes = 160u << 20;
 Pieces pieces(int M, int d, int V) {
   const Layout l = layout(M, d);
   const bool sync = grad_rounds(grad_units(M, d, BM * l.cg, l.tb * l.cg), kSms / l.cg) > 0;
