@@ -95,7 +95,7 @@ struct ForwardPolicy {
     float2* part;           // [slots][M] (max, sum) in units of log 2
     int M, V;
   };
-  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 0, j, t); }
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG, false>(a.r, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
   static __device__ __forceinline__ Boxes boxes_a(const Args& a, const Tile& t, int) {
     return row_boxes_a<CG>(a.r, &a.map_a, t);
@@ -295,7 +295,7 @@ struct SmallForwardPolicy {
     unsigned* done;         // CTAs finished: zero before and after
     int M, V;
   };
-  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 1, j, t); }
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG, true, false>(a.r, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG, RESIDENT>(a.r, t); }
   static __device__ __forceinline__ Boxes boxes_a(const Args& a, const Tile& t, int) {
     return row_boxes_a<CG>(a.r, &a.map_a, t);
@@ -540,7 +540,7 @@ struct DigitPolicy {
     int M, v0, Vp, tb;
     size_t plane;           // bytes of one digit's plane
   };
-  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 0, j, t); }
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG, false>(a.r, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG>(a.r, t); }
   static __device__ __forceinline__ Boxes boxes_a(const Args& a, const Tile& t, int) {
     return row_boxes_a<CG>(a.r, &a.map_a, t);

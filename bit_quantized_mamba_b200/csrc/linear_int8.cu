@@ -61,7 +61,7 @@ struct LinearPolicy {
     int32_t* acc;         // [M][V] or NULL
     int V;
   };
-  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG>(a.r, 1, j, t); }
+  static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG, true, CG == 2>(a.r, j, t); }
   static __device__ __forceinline__ uint32_t bytes(const Args& a, const Tile& t) { return row_bytes<CG, RESIDENT>(a.r, t); }
   static __device__ __forceinline__ Boxes boxes_a(const Args& a, const Tile& t, int) {
     return row_boxes_a<CG>(a.r, &a.map_a, t);
