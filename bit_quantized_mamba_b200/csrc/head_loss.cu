@@ -370,6 +370,7 @@ struct SmallForwardPolicy {
     __device__ __forceinline__ void finish(const Args& a) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
+        if (RESIDENT && part * 16 + j >= a.M) break;  // (1 token: 27 -> 26 us; with more the branches cost 2 us)
         const float mx = warp_max(m[j]), mz = mx == -INFINITY ? 0.0f : mx;
         const float s = warp_sum(S[j] * ex2(m[j] - mz));
         if (lane == j) sc->red[q][part * 16 + j] = make_float2(mx, s);
