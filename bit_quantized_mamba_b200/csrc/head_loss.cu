@@ -14,7 +14,7 @@
 // Gradient with respect to the (dequantised) normalised token:  du = g [sum_{v != y} p_v s_row_v W_v -
 // (1 - p_y) s_row_y W_y].  The coefficients c_v = exp(l_v - m) s_row_v / max|s_row| lie in [0, 1] (or [-1, 1] with
 // negative scales) whatever the token.  They are written in fixed point, in steps of 2^-24 tau with
-// tau = 2^-k ~ min(1, S / 16): below tau a coefficient is three base-256 digits, and at most 16 of a token's can
+// tau = 2^-k ~ min(1, S / 32): below tau a coefficient is three base-256 digits, and at most 32 of a token's can
 // be above it (they sum to at most S), whose further bits go into a list.  The sum over v is then three exact
 // int8 products of digits with W, each at twice the rate of a bf16 product, free of bf16's rounding and of any
 // order of summation, and a few listed rows of W.  A kernel first works out the tokens' factors and max|s_row|; then
@@ -29,7 +29,7 @@
 // At the end one kernel joins the digits, the listed rows and the label's row and applies the norm's backward.
 // The digits are stored as signed bytes (digit - 128); the column sums of W give the 128s back.
 //
-// 2048 tokens x 50288 rows x 2048: loss 165 us (2550 TOPS), loss and gradients 868 us (2430 TOPS of five products).
+// 2048 tokens x 50288 rows x 2048: loss 165 us (2550 TOPS), loss and gradients 875 us (2410 TOPS of five products).
 // Bound by power: with operands that do not change the products alone run at 3270 TOPS under the same cap.  What the
 // gradient takes beyond its products is the digits' epilogue (205 us for a product that alone takes 150).
 // Measured and dropped: the digits of a piece in one kernel with the second product of the piece before, tiles of both in
@@ -414,7 +414,9 @@ struct SmallForwardPolicy {
 
 // ------------------------------------------------------------------------------------ gradient
 
-constexpr int kListed = 16;  // coefficients of a token that may need more than 24 bits
+// Coefficients of a token that may need more than 24 bits: the more there may be, the finer the steps (11 tokens x
+// 30000 rows: dx off by 9.5e-7 with 16, 5.0e-7 with 32, 3.1e-7 with 64; 2048 x 50288 x 2048: 882, 889, 897 us).
+constexpr int kListed = 32;
 
 // Per-token factors of the gradient, and per CTA of the kernel that prepares them the largest |s_row| (bits) of its
 // rows with a flag for negative scales.
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(PrepareArgs a)
       const double g = (double)a.dloss[t];
       f = g * rest / (double)S;
       wy = -g * rest;
-      while (k < 4 && S * (float)(2 << k) <= (float)kListed) ++k;  // S 2^k <= 16
+      while (k < 4 && S * (float)(2 << k) <= (float)kListed) ++k;  // S 2^k <= kListed
       const float mk = m - (float)k;
       f *= exp2((double)mk - (double)m);
       m = mk;
