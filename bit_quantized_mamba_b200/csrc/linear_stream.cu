@@ -32,6 +32,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "rows.cuh"
 
 namespace dfssm {
 namespace stream {
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(NT, 1) stream_kernel(const __grid_constant__ P
       for (int v0 = lane; v0 < CH; v0 += 32 * U) {
         float4 t[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) t[u] = __ldg(xs + v0 + 32 * u);
+        for (int u = 0; u < U; ++u) t[u] = ld_f32x4(xs + v0 + 32 * u);
 #pragma unroll
         for (int u = 0; u < U; ++u)
           m = fmaxf(m, fmaxf(fmaxf(fabsf(t[u].x), fabsf(t[u].y)), fmaxf(fabsf(t[u].z), fabsf(t[u].w))));
@@ -717,7 +718,7 @@ __global__ void __launch_bounds__(NT, 1) stream_kernel(const __grid_constant__ P
       for (int v0 = lane; v0 < CH; v0 += 32 * U) {
         float4 t[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) t[u] = __ldg(xs + v0 + 32 * u);
+        for (int u = 0; u < U; ++u) t[u] = ld_f32x4(xs + v0 + 32 * u);
         // codes two float4 at a time (one rarely taken branch per eight values)
 #pragma unroll
         for (int u2 = 0; u2 < U; u2 += 2) {
@@ -773,7 +774,7 @@ __global__ void __launch_bounds__(NT, 1) stream_kernel(const __grid_constant__ P
 #pragma unroll
       for (int k = 0; k < XPT; ++k) {
         const int i = tid + k * NCW * 32;
-        const float v = b < B ? __ldg(p.x + (size_t)b * DIN + i) : 0.0f;
+        const float v = b < B ? ld_f32(p.x + (size_t)b * DIN + i) : 0.0f;
         if (XREG) xr[b * XPT + k] = v;
         m = fmaxf(m, fabsf(v));
       }
@@ -793,7 +794,7 @@ __global__ void __launch_bounds__(NT, 1) stream_kernel(const __grid_constant__ P
         float v[XPT];
 #pragma unroll
         for (int k = 0; k < XPT; ++k)
-          v[k] = XREG ? xr[b * XPT + k] : __ldg(p.x + (size_t)b * DIN + tid + k * NCW * 32);
+          v[k] = XREG ? xr[b * XPT + k] : ld_f32(p.x + (size_t)b * DIN + tid + k * NCW * 32);
         int cd[XPT];
         quant_codes<XPT>(v, s0, inv_s0, cd);
 #pragma unroll

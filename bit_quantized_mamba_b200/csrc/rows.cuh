@@ -7,9 +7,10 @@
 
 namespace dfssm {
 
-// What an earlier kernel of the stream may have written is read with these after pdl_wait(): the compiler may move a
-// read-only load (__ldg, or one through a __restrict__ parameter) above that wait, as nothing in the kernel itself
-// writes the memory; volatile assembly keeps its place.
+// What an earlier kernel of the stream may have written is read after pdl_wait(), with these or with plain loads.  Not
+// with a read-only load (__ldg, or one through a __restrict__ parameter): the compiler may move that above the
+// wait, as nothing in the kernel itself writes the memory.  The wait clobbers memory, which plain loads do not cross;
+// volatile assembly keeps its place as well, and its batches stay together.
 __device__ __forceinline__ uint32_t ld_u32(const void* p) {
   uint32_t r;
   asm volatile("ld.global.u32 %0, [%1];" : "=r"(r) : "l"(p));
@@ -21,6 +22,10 @@ __device__ __forceinline__ uint4 ld_u32x4(const void* p) {
   uint4 r;
   asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
+}
+__device__ __forceinline__ float4 ld_f32x4(const void* p) {
+  const uint4 r = ld_u32x4(p);
+  return make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w));
 }
 
 template <typename T>

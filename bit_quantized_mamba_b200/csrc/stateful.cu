@@ -8,6 +8,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "rows.cuh"
 
 namespace dfssm {
 
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(256, LMH_CTAS_PER_SM) int8_gemv_kernel(Int8Gem
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int i = threadIdx.x + 256 * (k0 + k);
-        v[k] = i < a.d ? __ldg(a.x + i) : 0.0f;
+        v[k] = i < a.d ? ld_f32(a.x + i) : 0.0f;
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) ss = fma((double)v[k], (double)v[k], ss);  // exact squares in fp64
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(256, LMH_CTAS_PER_SM) int8_gemv_kernel(Int8Gem
   }
   const auto value = [&](int i) {
     if (i >= a.d) return 0.0f;
-    const float xv = __ldg(a.x + i);
+    const float xv = ld_f32(a.x + i);
     return norm ? norm_value(xv, rn, __ldg(a.norm_w + i)) : xv;
   };
   float m = 0.0f;

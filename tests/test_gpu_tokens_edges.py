@@ -1,0 +1,80 @@
+"""The many-token operators on the int8 matrix where they can go wrong: followed by the single-token calls in one
+stream, signs of zero, tokens that are not finite, row scales of very different sizes, optional outputs, and the size of
+their rounding errors."""
+import numpy as np
+import pytest
+import torch
+
+from bit_quantized_mamba_b200 import inputs
+
+pytestmark = pytest.mark.gpu
+
+F8 = torch.float64
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_quantized_mamba_b200 import build, dfssm
+    build.build()
+    dfssm.lib()
+    return torch.device("cuda:0")
+
+
+def gen(seed, dev):
+    return torch.Generator(dev).manual_seed(seed)
+
+
+def matrix(g, V, d, dev):
+    """Codes and row scales, complete before any call is enqueued."""
+    W = torch.randint(-127, 128, (V, d), generator=g, device=dev, dtype=torch.int8)
+    s = torch.rand(V, generator=g, device=dev) * 9e-4 + 1e-4
+    torch.cuda.synchronize()
+    return W, s
+
+
+# ------------------------------------------------------------------------------------ one stream
+
+
+@pytest.mark.parametrize("B", [1, 4, 16])
+def test_single_token_calls_read_what_the_embedding_just_wrote(dev, B):
+    """embed_tokens lets the next kernel of the stream start before its rows are written.  The head, the greedy head
+    and the streaming linear on those rows, in a captured chain over one buffer, give the bits of calls made one
+    at a time."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(40 + B, dev)
+    V, d, n = 1187, 2048, 6
+    W, sr = matrix(g, V, d, dev)
+    nw = torch.rand(d, generator=g, device=dev) + 0.5
+    L = dfssm.Linear.from_host(inputs.linear(np.random.default_rng(B), 4096, d), dev)
+    tok = torch.randint(0, V, (n, B), generator=g, device=dev, dtype=torch.int32)
+    h = torch.zeros(B, d, device=dev)
+    size = dfssm.workspace_size
+    ws = [dfssm.workspace(size(op, *dims), dev) for op, dims in (
+        (dfssm.OP_EMBED_TOKENS, (0, 0, 0)), (dfssm.OP_HEAD_GREEDY, (1, d, V)), (dfssm.OP_LM_HEAD, (1, d, V)),
+        (dfssm.OP_LINEAR_DECODE, (B, d, 4096)))]
+    torch.cuda.synchronize()
+
+    def chain(pause):
+        outs = []
+        for k in range(n):
+            for call in (lambda: list(dfssm.head_greedy(W, sr, h[0], nw, ws=ws[1])),
+                         lambda: [dfssm.lm_head(W, sr, h[0], ws=ws[2])],
+                         lambda: [dfssm.linear_decode(L, h, ws=ws[3])]):
+                dfssm.embed_tokens(W, sr, tok[k], h=h, ws=ws[0])
+                pause()
+                outs += call()
+                pause()
+                dfssm.embed_tokens(W, sr, tok[(k + 1) % n], h=h, ws=ws[0])  # other rows, which none of them may see
+                pause()
+        return outs
+
+    want = [t.clone() for t in chain(torch.cuda.synchronize)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(lambda: None)
+    for _ in range(20):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
