@@ -23,9 +23,10 @@ namespace {
 using namespace gemm_i8;
 
 // fl32(acc s w) of the definition, its fp64 product rounded once, in fp32: with x = acc exact (|acc| < 2^24), p = fl(x s)
-// and e = x s - p, the product is y + r, y = fl(p w), r = (p w - y) + e w, where r alone is rounded, by less than
-// 2^-47 |y|.  Where y + r rounds the same with r moved by 2^-46 |y| either way, that is the definition's value;
-// otherwise (about one in 2^20) `sure` is cleared and the caller takes fp64.  (In fp64 throughout, the fp64 and
+// and e = x s - p, the product is y - r, y = fl(p w), r = (y - p w) - e w, where r alone is rounded, by less than
+// 2^-47 |y|.  Where y - r rounds the same with r moved by 2^-46 |y| either way, that is the definition's value;
+// otherwise (about one in 2^20) `sure` is cleared and the caller takes fp64.  (r is subtracted: for acc = 0 it is +0, so
+// that the result keeps the sign of y, -0 under a negative w.)  (In fp64 throughout, the fp64 and
 // conversion units bound the product: 2048 x 50288 x 2048 took 215 us of 133 us without an epilogue.)
 // s and w in [2^-40, 2^40] (ordinary) keep every term normal; s = 0 gives acc = 0.
 __device__ __forceinline__ bool ordinary(float s) { return fabsf(s) >= 0x1p-40f && fabsf(s) <= 0x1p40f; }
@@ -33,10 +34,10 @@ __device__ __forceinline__ bool ordinary(float s) { return fabsf(s) >= 0x1p-40f 
 __device__ __forceinline__ void scaled(uint32_t acc0, uint32_t acc1, f2 s, f2 ns, f2 w, f2 nw, bool& sure, float& out0,
                                        float& out1) {
   const float x0 = (float)(int)acc0, x1 = (float)(int)acc1;
-  const f2 x = pack2(x0, x1), t = pack2(0x1p-46f, 0x1p-46f), nt = pack2(-0x1p-46f, -0x1p-46f);
+  const f2 x = pack2(x0, x1), t = pack2(0x1p-46f, 0x1p-46f), nt = pack2(-0x1p-46f, -0x1p-46f), minus = pack2(-1.0f, -1.0f);
   const f2 np = mul2(x, ns), e = fma2(x, s, np);
-  const f2 y = mul2(np, nw), r = fma2(e, w, fma2(np, nw, mul2(np, w)));
-  const f2 lo = add2(y, fma2(y, nt, r)), hi = add2(y, fma2(y, t, r));
+  const f2 y = mul2(np, nw), r = fma2(e, nw, fma2(np, w, y));
+  const f2 lo = fma2(fma2(y, t, r), minus, y), hi = fma2(fma2(y, nt, r), minus, y);
   float hi0, hi1;
   unpack2(lo, out0, out1);
   unpack2(hi, hi0, hi1);

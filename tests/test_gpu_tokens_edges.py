@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_tokens as base
 from bit_quantized_mamba_b200 import inputs
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +79,36 @@ def test_single_token_calls_read_what_the_embedding_just_wrote(dev, B):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------------------------ signs of zero
+
+
+def bits(t):
+    return t.contiguous().view(torch.int32 if t.dtype == torch.float32 else torch.int16)
+
+
+@pytest.mark.parametrize("M", [1, 3, 16, 100, 300])
+def test_linear_int8_signs_of_zero(dev, M):
+    """A zero accumulator times a negative row scale is -0 in the definition, in the single-token head and here,
+    whatever the neighbouring outputs are."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(60 + M, dev)
+    V, d = 700, 512
+    W, sr = matrix(g, V, d, dev)
+    W[::5] = 0
+    sr = sr * (torch.randint(0, 2, (V,), generator=g, device=dev) * 2 - 1)
+    sr[7::50] *= 2.0 ** -45  # beyond what the fp32 pairs take
+    x = torch.randn(M, d, generator=g, device=dev)
+    x[::3] = 0.0
+    torch.cuda.synchronize()
+    acc = torch.zeros(M, V, dtype=torch.int32, device=dev)
+    scale = torch.zeros(M, device=dev)
+    y = dfssm.linear_int8(W, sr, x, debug=dict(acc=acc, xscale=scale))
+    want = (acc.double() * scale.double()[:, None] * sr.double()).float()
+    assert bool((bits(want) == -2 ** 31).any())
+    assert torch.equal(bits(y), bits(want))
+    yb = dfssm.linear_int8(W, sr, x, out_dtype=torch.bfloat16)
+    assert torch.equal(bits(yb), bits(want.bfloat16()))
+    for t in range(0, M, 37):
+        assert torch.equal(bits(dfssm.lm_head(W, sr, x[t].contiguous())), bits(y[t]))
