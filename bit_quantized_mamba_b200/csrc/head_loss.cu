@@ -218,11 +218,16 @@ __device__ __forceinline__ void write_loss(int t, float m, double S, int M, int 
   const bool bad = y >= V;
   if (bad) atomicExch(status, kBadTokenCode);
   float out = 0.0f, rest = 0.0f;
-  if (y >= 0 && !bad && S != 0.0) {
-    const double z = ((double)m + log2(S)) * kLn2 - (double)__ldcg(stats + 2 * (size_t)M + t);
-    const float e = expf(-fabsf((float)z));  // below 1
-    rest = z > 0.0 ? 1.0f / (1.0f + e) : e / (1.0f + e);
-    out = z > 0.0 ? (float)(z + (double)log1pf(e)) : log1pf(e);
+  if (y >= 0 && !bad) {
+    const float l = __ldcg(stats + 2 * (size_t)M + t);
+    if (S != 0.0) {
+      const double z = ((double)m + log2(S)) * kLn2 - (double)l;
+      const float e = expf(-fabsf((float)z));  // below 1
+      rest = z > 0.0 ? 1.0f / (1.0f + e) : e / (1.0f + e);
+      out = z > 0.0 ? (float)(z + (double)log1pf(e)) : log1pf(e);
+    } else if (l != l) {  // no other row, but the token is not finite
+      rest = out = l;
+    }
   }
   stats[t] = m;
   stats[(size_t)M + t] = (float)S;
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(PrepareArgs a)
     const double rest = (double)a.stats[2 * (size_t)a.M + t];  // 1 - p_y
     double f = 0.0, wy = 0.0;
     int k = 0;
-    if (y >= 0 && y < a.V && S != 0.0f) {
+    if (y >= 0 && y < a.V && (S != 0.0f || rest != 0.0)) {
       const double g = (double)a.dloss[t];
       f = g * rest / (double)S;
       wy = -g * rest;

@@ -112,3 +112,28 @@ def test_linear_int8_signs_of_zero(dev, M):
     assert torch.equal(bits(yb), bits(want.bfloat16()))
     for t in range(0, M, 37):
         assert torch.equal(bits(dfssm.lm_head(W, sr, x[t].contiguous())), bits(y[t]))
+
+
+# ------------------------------------------------------------------------------------ odd tokens
+
+
+@pytest.mark.parametrize("M", [1, 3, 40, 100, 300])
+def test_head_loss_of_one_row_and_tokens_that_are_not_finite(dev, M):
+    """A vocabulary of one row has loss and gradients zero, but a token that is not finite has NaN in its own."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(80 + M, dev)
+    W, sr = matrix(g, 1, 64, dev)
+    x = torch.randn(M, 64, generator=g, device=dev)
+    x[0, 5] = float("nan")
+    if M > 2:
+        x[2, 6] = float("inf")
+    labels = torch.zeros(M, dtype=torch.int32, device=dev)
+    if M > 2:
+        labels[1] = -1
+        x[1, 0] = float("nan")  # ignored
+    bad = torch.zeros(M, dtype=torch.bool, device=dev)
+    bad[0::2][:2] = True
+    loss, stats = dfssm.head_loss(W, sr, x, labels)
+    assert torch.equal(loss.isnan(), bad) and not loss[~bad].any()
+    dx, ds, _ = dfssm.head_loss_backward(W, sr, x, labels, stats, torch.ones(M, device=dev))
+    assert bool(dx[bad].isnan().all()) and not dx[~bad].any() and bool(ds.isnan().all())
