@@ -15,10 +15,11 @@
 // (1 - p_y) s_row_y W_y].  The coefficients c_v = exp(l_v - m) s_row_v / max|s_row| lie in [0, 1] (or [-1, 1] with
 // negative scales) whatever the token.  They are written in fixed point, in steps of 2^-24 tau with
 // tau = 2^-k ~ min(1, S / 32): below tau a coefficient is three base-256 digits, and at most 32 of a token's can
-// be above it (they sum to at most S), whose further bits go into a list.  The sum over v is then three exact
+// be above it (they sum to at most S), whose further bits go into a list.  (A few rows whose scales are far above the
+// others' are left out of the maximum; see scale_top().)  The sum over v is then three exact
 // int8 products of digits with W, each at twice the rate of a bf16 product, free of bf16's rounding and of any
-// order of summation, and a few listed rows of W.  A kernel first works out the tokens' factors and max|s_row|; then
-// the vocabulary is taken in pieces whose digits stay in L2:
+// order of summation, and a few listed rows of W.  Two kernels first quantize the tokens, look over the row scales and work
+// out the tokens' factors; then the vocabulary is taken in pieces whose digits stay in L2:
 //   1. the first product again, its epilogue turning logits into digits (and the row scales' gradient
 //      into partial column sums);
 //   2. the second product: digits x W, whose rows are its K dimension as they lie in memory ("MN-major" operand;
@@ -423,97 +424,205 @@ struct SmallForwardPolicy {
 // 30000 rows: dx off by 9.5e-7 with 16, 5.0e-7 with 32, 3.1e-7 with 64; 2048 x 50288 x 2048: 882, 889, 897 us).
 constexpr int kListed = 32;
 
-// Per-token factors of the gradient, and per CTA of the kernel that prepares them the largest |s_row| (bits) of its
-// rows with a flag for negative scales.
+// Per-token factors of the gradient.
 constexpr int kPrepareCtas = 128, kPrepareThreads = 512;
 struct TokenFactors {
   float4* tok;    // [M] {m', s, f s, w_y s}: m' = m - k, f = g p_max 2^-k, w_y = -g (1 - p_y)
   int* shift;     // [M] k
   double2* fac;   // [M] {f, w_y}
-  uint2* srow;    // [kPrepareCtas] {bits of max |s_row|, any negative}
+  uint2* srow;    // [kScanParts] {bits of max |s_row|, any negative} of the rows' parts
 };
+
+// The scale that coefficients are counted in.  It is the largest, unless that is far above the others': one such row would
+// cost every token its precision (steps 10000 times as wide, dx off by 5e-4), also those that give the row no weight.
+// "Far above" is beyond 8 times T, the least but an eighth of the parts' maxima; then it is the largest of the
+// maxima up to 8 T, and the rows beyond it are looked at token by token (outliers()).  The whole warp works it out, from
+// 128 numbers.
+constexpr int kLowParts = kScanParts / 8;
+struct ScaleTop {
+  float top, most;  // the scale, and the largest there is
+  bool outliers;    // rows beyond the top
+  bool neg;         // negative scales
+};
+__device__ __forceinline__ ScaleTop scale_top(const uint2* srow, int V) {
+  constexpr int N = kScanParts / 32;
+  const int lane = threadIdx.x & 31, run = scan_run(V), runs = (V + run - 1) / run;
+  const int parts = runs < kScanParts ? runs : kScanParts, low = parts * kLowParts / kScanParts;
+  uint32_t m[N], most = 0u, neg = 0u;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint2 r = srow[k * 32 + lane];
+    m[k] = k * 32 + lane < parts ? r.x : 0xFFFFFFFFu;
+    most = max(most, r.x);
+    neg |= r.y;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  ScaleTop t{__uint_as_float(most), __uint_as_float(most), false, __reduce_or_sync(0xffffffffu, neg) != 0u};
+  // more than `low` parts stay below x
+  const auto many_below = [&](uint32_t x) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) n += __popc(__ballot_sync(0xffffffffu, m[k] < x));
+    return n > low;
+  };
+  if (most < 0x7F800000u && many_below(__float_as_uint(t.top * 0.125f))) {
+    uint32_t x = 0u;  // the largest number that few parts stay below: the (low + 1)-th of the maxima
+    for (uint32_t bit = 1u << 30; bit > 0u; bit >>= 1)
+      if (!many_below(x | bit)) x |= bit;
+    const uint32_t bound = __float_as_uint(__uint_as_float(x) * 8.0f);
+    uint32_t top = 0u;
+#pragma unroll
+    for (int k = 0; k < N; ++k) top = max(top, m[k] <= bound ? m[k] : 0u);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (__uint_as_float(top) > 1e-30f && top < most) {
+      t.top = __uint_as_float(top);
+      t.outliers = true;
+    }
+  }
+  return t;
+}
+
 struct PrepareArgs {
   const float* stats;
   const int32_t* labels;
   const float* dloss;
+  const int8_t* q;  // [M][d] codes
   const double* s_tok;
+  const int8_t* W;
   const float* s_row;
-  int M, V;
+  int M, V, d;
   TokenFactors out;
   uint4* zero;      // to be zeroed
   size_t zeros;     // 16 bytes each
 };
-// The tokens' factors, the row scales' range, and zeros in what the products add to.
+// Up to kOutliers rows whose scale is beyond `top`, in order (whole CTA); their number, or -1 if there are more.
+// (2048 tokens x 50288 rows x 2048, loss and gradients: 755 us without such rows, 787 with one, 902 with 64, 1077 with 256.)
+constexpr int kOutliers = 1024;
+__device__ __forceinline__ int find_outliers(const PrepareArgs& a, float top, int* rows) {
+  __shared__ int cnt[kPrepareThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int n = 0;
+  for (int v0 = 0; v0 < a.V; v0 += kPrepareThreads) {
+    const int v = v0 + threadIdx.x;
+    const bool out = v < a.V && fabsf(ld_f32(a.s_row + v)) > top;
+    if (!__syncthreads_or(out)) continue;
+    const uint32_t b = __ballot_sync(0xffffffffu, out);
+    if (lane == 0) cnt[warp] = __popc(b);
+    __syncthreads();
+    int at = n;
+    for (int w = 0; w < kPrepareThreads / 32; ++w) {
+      if (w == warp) at = n + __popc(b & ((1u << lane) - 1u));
+      n += cnt[w];
+    }
+    if (out && at < kOutliers) rows[at] = v;
+    __syncthreads();
+  }
+  return n <= kOutliers ? n : -1;
+}
+// The largest and the sum of a token's coefficients exp(l - m) |s_row| in the outlying rows but its label's (whole warp).
+__device__ __forceinline__ void outliers(const PrepareArgs& a, const int* rows, int n, int t, int y, float m, float& most,
+                                         float& sum) {
+  const int lane = threadIdx.x & 31;
+  const float s = (float)a.s_tok[t];
+  most = sum = 0.0f;
+  for (int i = 0; i < n; ++i) {
+    const int v = rows[i];
+    const uint4* w = reinterpret_cast<const uint4*>(a.W + (size_t)v * a.d);
+    const uint4* q = reinterpret_cast<const uint4*>(a.q + (size_t)t * a.d);
+    int acc = 0;
+    for (int c = lane; c < a.d / 16; c += 32) {
+      const uint4 x = ld_u32x4(w + c), z = ld_u32x4(q + c);
+      acc = dp4a_ss(x.x, z.x, acc);
+      acc = dp4a_ss(x.y, z.y, acc);
+      acc = dp4a_ss(x.z, z.z, acc);
+      acc = dp4a_ss(x.w, z.w, acc);
+    }
+    acc = __reduce_add_sync(0xffffffffu, acc);
+    const float r = ld_f32(a.s_row + v), c = ex2(fmaf((float)acc * s, scale2(r), -m)) * fabsf(r);
+    if (v != y) {
+      most = fmaxf(most, c);
+      sum += c;
+    }
+  }
+}
+// The tokens' factors, and zeros in what the products add to.
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(PrepareArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ uint2 red[kPrepareThreads / 32];
+  __shared__ int rows[kOutliers];
   const int i = blockIdx.x * kPrepareThreads + threadIdx.x, n = kPrepareCtas * kPrepareThreads;
   const TokenFactors& o = a.out;
+  struct Token {
+    int y;
+    float m, S, rest, g;  // rest: 1 - p_y
+    double s;
+  };
+  const auto token = [&](int t) {
+    return Token{a.labels[t], a.stats[t], a.stats[(size_t)a.M + t], a.stats[2 * (size_t)a.M + t], a.dloss[t], a.s_tok[t]};
+  };
+  Token c = token(min(i, a.M - 1));  // requested before the row scales are looked at
   for (size_t z = i; z < a.zeros; z += n) a.zero[z] = make_uint4(0u, 0u, 0u, 0u);
-  uint32_t mb = 0u, neg = 0u;
-#pragma unroll 4
-  for (int v = i; v < a.V; v += n) {
-    const float s = ld_f32(a.s_row + v);
-    mb = max(mb, __float_as_uint(s) & 0x7FFFFFFFu);  // orders like |s|, a NaN above all
-    neg |= s < 0.0f ? 1u : 0u;
+  const ScaleTop top = scale_top(o.srow, a.V);
+  int outlying = 0;
+  if (top.outliers) {
+    outlying = find_outliers(a, top.top, rows);
+    __syncthreads();
   }
-  mb = __reduce_max_sync(0xffffffffu, mb);
-  neg = __reduce_or_sync(0xffffffffu, neg);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_uint2(mb, neg);
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const uint2 r = threadIdx.x < kPrepareThreads / 32 ? red[threadIdx.x] : make_uint2(0u, 0u);
-    const uint32_t m = __reduce_max_sync(0xffffffffu, r.x), g = __reduce_or_sync(0xffffffffu, r.y);
-    if (threadIdx.x == 0) o.srow[blockIdx.x] = make_uint2(m, g);
-  }
-  for (int t = i; t < a.M; t += n) {
-    const int y = a.labels[t];
-    float m = a.stats[t];
-    const float S = a.stats[(size_t)a.M + t];
-    const double rest = (double)a.stats[2 * (size_t)a.M + t];  // 1 - p_y
+  // a thread per token, or a warp (every lane the same) where there are outlying rows to look at
+  const bool by_warp = outlying > 0;
+  const int step = by_warp ? n >> 5 : n;
+  for (int t = by_warp ? i >> 5 : i; t < a.M; t += step) {
+    if (by_warp || t != i) c = token(t);
+    float m = c.m;
+    const float S = c.S;
     double f = 0.0, wy = 0.0;
     int k = 0;
-    if (y >= 0 && y < a.V && (S != 0.0f || rest != 0.0)) {
-      const double g = (double)a.dloss[t];
+    if (c.y >= 0 && c.y < a.V && (S != 0.0f || c.rest != 0.0f)) {
+      const double g = (double)c.g, rest = (double)c.rest;
       f = g * rest / (double)S;
       wy = -g * rest;
-      while (k < 4 && S * (float)(2 << k) <= (float)kListed) ++k;  // S 2^k <= kListed
-      const float mk = m - (float)k;
+      if (!top.outliers) {
+        while (k < 4 && S * (float)(2 << k) <= (float)kListed) ++k;  // S 2^k <= kListed
+      } else {
+        // tau in units of the top: half of the list for the rows below it, which are all below 1, half for the others
+        float most = top.most, sum = S * top.most;  // too many rows: what they may be at most
+        if (by_warp) outliers(a, rows, outlying, t, c.y, m, most, sum);
+        const float half = 2.0f / kListed;
+        const float tau = fmaxf(fminf(1.0f, S * half), fminf(most, sum * half) / top.top);
+        while (k < 4 && tau * (float)(2 << k) <= 1.0f) ++k;
+        if (tau > 1.0f) k = tau < 1e37f ? -1 - ilogbf(tau) : -123;  // (a NaN leaves 0)
+      }
+      const float mk = k < 0 ? __fsub_ru(m, (float)k) : m - (float)k;
       f *= exp2((double)mk - (double)m);
       m = mk;
     }
     if (m == -INFINITY) m = 0.0f;  // no other row
     o.shift[t] = k;
-    const double s = a.s_tok[t];
-    // a token without a gradient (ignored, or dloss 0) has none whatever its values are
+    // a token that is ignored has no gradient whatever its values are
     o.tok[t] = f == 0.0 && wy == 0.0 ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                     : make_float4(m, (float)s, (float)(f * s), (float)(wy * s));
+                                     : make_float4(m, (float)c.s, (float)(f * c.s), (float)(wy * c.s));
     o.fac[t] = make_double2(f, wy);
   }
 }
 
 // Fixed point: steps per unit of coefficient.  A number n is stored as n + offset, its low 24 bits as digits;
 // numbers up to 2^24 tau need no more (2^23 with negative scales, which take the sign's bit).  The margin of 64
-// steps takes up the rounding of exp(l - m) just above 1.
+// steps takes up the rounding of exp(l - m) just above 1; where a number may be larger, with outlying rows, it cannot be
+// cut off, and the margin is 2^-8.
 struct FixedPoint {
   float unit;    // steps per unit of exp(l - m') scale2(s_row)
   int offset;    // 0, or 2^23 with negative scales
   int range;     // 2^24, or 2^23
+  bool outliers;
   double step;   // what one step stands for, of exp(l - m') s_row
 };
-__device__ __forceinline__ FixedPoint fixed_point(const uint2* srow) {  // (whole warps)
-  uint2 r[kPrepareCtas / 32];
-#pragma unroll
-  for (int k = 0; k < kPrepareCtas / 32; ++k) r[k] = srow[k * 32 + (threadIdx.x & 31)];
-#pragma unroll
-  for (int k = 1; k < kPrepareCtas / 32; ++k) r[0] = make_uint2(max(r[0].x, r[k].x), r[0].y | r[k].y);
-  const float smax = __uint_as_float(__reduce_max_sync(0xffffffffu, r[0].x));
-  const bool neg = __reduce_or_sync(0xffffffffu, r[0].y) != 0u;
+__device__ __forceinline__ FixedPoint fixed_point(const uint2* srow, int V) {  // (whole warps)
+  const ScaleTop t = scale_top(srow, V);
   FixedPoint p;
-  p.range = neg ? 1 << 23 : 1 << 24;
-  p.unit = smax < 1e-30f ? 0.0f : (float)(p.range - 64) / scale2(smax);  // (so small, nothing of du is left either)
-  p.offset = neg ? 1 << 23 : 0;
+  p.range = t.neg ? 1 << 23 : 1 << 24;
+  p.unit = t.top < 1e-30f ? 0.0f : (float)(p.range - (t.outliers ? p.range >> 8 : 64)) / scale2(t.top);  // (so small, nothing of du is left either)
+  p.offset = t.neg ? 1 << 23 : 0;
+  p.outliers = t.outliers;
   p.step = p.unit == 0.0f ? 0.0 : 1.0 / ((double)p.unit * kLog2e);
   return p;
 }
@@ -545,7 +654,7 @@ struct DigitPolicy {
     int2* list;             // [M][kListed] {row of W, number / 2^24}
     unsigned char* digits;  // [3][M / tb][Vp / 16][tb][16]
     float* colpart;         // [ceil(M / 32)][Vp]
-    int M, v0, Vp, tb;
+    int M, V, v0, Vp, tb;
     size_t plane;           // bytes of one digit's plane
   };
   static __device__ __forceinline__ bool tile(const Args& a, int j, Tile& t) { return row_tile<CG, false>(a.r, j, t); }
@@ -570,14 +679,14 @@ struct DigitPolicy {
     int label, most;
     __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int part_, int lane_)
         : q(q_), part(part_), lane(lane_), sr(reinterpret_cast<float*>(sm) + (part_ * 4 + q_) * 2 * EPI_COLS),
-          cu(sr + EPI_COLS), fp(fixed_point(a.srow)) {}
+          cu(sr + EPI_COLS), fp(fixed_point(a.srow, a.V)) {}
     __device__ __forceinline__ void write_b(const Args&, unsigned char*, int) {}
     __device__ __forceinline__ void prepare(const Args& a, const Tile& t) {
       const int tk = t.a0 + q * 32 + lane;
       const bool valid = tk < a.M;
       tf = valid ? a.tok[tk] : make_float4(0.f, 0.f, 0.f, 0.f);
       label = valid ? a.labels[tk] - a.v0 : -1;
-      most = (fp.range << (valid ? a.shift[tk] : 0)) - 1 + fp.offset;
+      most = fp.outliers ? (1 << 30) - 1 : (fp.range << (valid ? a.shift[tk] : 0)) - 1 + fp.offset;
 #pragma unroll
       for (int k = 0; k < EPI_COLS / 32; ++k) {
         const int i = k * 32 + lane, c = ((i >> 4) * PARTS + part) * 16 + (i & 15);
@@ -877,7 +986,7 @@ __global__ void __launch_bounds__(256) grad_finish_kernel(GradFinishArgs a) {
   pdl_wait();
   __shared__ double red[2][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const FixedPoint fp = fixed_point(a.srow);
+  const FixedPoint fp = fixed_point(a.srow, a.V);
   // stored bytes are digit - 128 and the number itself is offset: both come back through W's column sums
   const long long back = 0x808080LL - (long long)fp.offset;
   float dn[CH][8];
@@ -1074,7 +1183,7 @@ BackwardWs backward_ws(int M, int d, int V) {
   w.shift = w.fac + al256(sizeof(double2) * (size_t)M);
   w.list = w.shift + al256(sizeof(int) * (size_t)M);
   w.srow = w.list + al256(sizeof(int2) * kListed * (size_t)M);
-  w.zero = w.srow + al256(sizeof(uint2) * kPrepareCtas);
+  w.zero = w.srow + al256(sizeof(uint2) * kScanParts);
   w.listed = w.zero;
   w.colsum = w.listed + al256(sizeof(int) * (size_t)M);
   w.acc = w.colsum + al256(sizeof(int32_t) * (size_t)d);
@@ -1212,6 +1321,7 @@ int piece_products(const Piece& p, cudaStream_t st) {
   a.digits = p.digits;
   a.colpart = p.colpart;
   a.M = p.M;
+  a.V = p.V;
   a.v0 = p.v0;
   a.Vp = p.Vp;
   a.tb = p.l.tb;
@@ -1338,11 +1448,14 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   char* base = static_cast<char*>(workspace);
   RowsQuantArgs qa = quant_args(x, x_type, ldx, M, d, norm_w, base, w.q, w.s);
   qa.rn = reinterpret_cast<float*>(base + w.rn);
+  qa.scan = s_row;
+  qa.V = V;
+  qa.range = reinterpret_cast<uint2*>(base + w.srow);
   cudaError_t e = launch_rows_quant(qa, s);
   if (e != cudaSuccess) return record_cuda_failure(e);
   TokenFactors tf{reinterpret_cast<float4*>(base + w.tok), reinterpret_cast<int*>(base + w.shift),
-                  reinterpret_cast<double2*>(base + w.fac), reinterpret_cast<uint2*>(base + w.srow)};
-  const PrepareArgs pa{stats, labels, dloss, qa.s, s_row, M, V, tf, reinterpret_cast<uint4*>(base + w.zero),
+                  reinterpret_cast<double2*>(base + w.fac), qa.range};
+  const PrepareArgs pa{stats, labels, dloss, qa.q, qa.s, W, s_row, M, V, d, tf, reinterpret_cast<uint4*>(base + w.zero),
                        (w.zero_end - w.zero) / 16};
   e = launch_pdl(prepare_kernel, dim3(kPrepareCtas), dim3(kPrepareThreads), 0, s, pa);
   if (e != cudaSuccess) return record_cuda_failure(e);

@@ -162,7 +162,15 @@ struct RowsQuantArgs {
   float* rn;              // [M] RMS factor or NULL
   int8_t* dbg_q;          // optional taps
   float* dbg_s;
+  // beside the tokens: the range of V numbers, one {bits of max |s|, any negative} for each of kScanParts parts of them (or
+  // NULL)
+  const float* scan;
+  int V;
+  uint2* range;
 };
+constexpr int kScanParts = 128;
+// Elements of part p: runs of scan_run(V) consecutive ones, every kScanParts-th run from run p on.
+__host__ __device__ constexpr int scan_run(int V) { return V <= 32 * kScanParts ? 1 : 32; }
 cudaError_t launch_rows_quant(const RowsQuantArgs& a, cudaStream_t st);
 
 // Density-field state representation of state rows [rows][N] (8 <= N <= 256, N % 8 == 0; rows 16-byte

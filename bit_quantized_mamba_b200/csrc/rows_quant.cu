@@ -16,8 +16,31 @@ namespace {
 
 constexpr int RQ_THREADS = 256;
 
-// CH: chunks of 2048 values a row may have.
-template <typename T, int CH>
+// Part `part` of the scan (whole CTA).
+__device__ __forceinline__ void scan_range(const RowsQuantArgs& a, int part) {
+  __shared__ uint2 red[RQ_THREADS / 32];
+  const int run = scan_run(a.V), per = RQ_THREADS / run;  // runs of the CTA at a time
+  const long long runs = (a.V + run - 1) / run;
+  uint32_t m = 0u, neg = 0u;
+#pragma unroll 4
+  for (long long r = part + (long long)kScanParts * (threadIdx.x / run); r < runs; r += (long long)kScanParts * per) {
+    const long long v = r * run + threadIdx.x % run;
+    const float s = v < a.V ? ld_f32(a.scan + v) : 0.0f;
+    m = max(m, __float_as_uint(s) & 0x7FFFFFFFu);  // orders like |s|, a NaN above all
+    neg |= s < 0.0f ? 1u : 0u;
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  neg = __reduce_or_sync(0xffffffffu, neg);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_uint2(m, neg);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < RQ_THREADS / 32; ++w) m = max(m, red[w].x), neg |= red[w].y;
+    a.range[part] = make_uint2(m, neg);
+  }
+}
+
+// CH: chunks of 2048 values a row may have.  SCAN: the last kScanParts CTAs look over a.scan.
+template <typename T, int CH, bool SCAN>
 __global__ void __launch_bounds__(RQ_THREADS) rows_quant_kernel(RowsQuantArgs a) {
   pdl_launch_dependents();
   pdl_wait();
@@ -26,6 +49,10 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_quant_kernel(RowsQuantArgs a)
   __shared__ uint32_t red_m[RQ_THREADS / 32];
   __shared__ float red_rn;
   const int tok = blockIdx.x;
+  if (SCAN && tok >= a.M) {
+    scan_range(a, tok - a.M);
+    return;
+  }
   const T* xr = reinterpret_cast<const T*>(a.x) + (size_t)tok * a.ldx;
   float v[CH][8], nw[CH][8];  // the row, and the norm's weight with it
 #pragma unroll
@@ -99,18 +126,19 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_quant_kernel(RowsQuantArgs a)
   }
 }
 
-template <typename T>
+template <typename T, bool SCAN>
 cudaError_t launch(const RowsQuantArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)a.M);
-  if (a.d <= 8 * RQ_THREADS) return launch_pdl(rows_quant_kernel<T, 1>, grid, dim3(RQ_THREADS), 0, st, a);
-  if (a.d <= 16 * RQ_THREADS) return launch_pdl(rows_quant_kernel<T, 2>, grid, dim3(RQ_THREADS), 0, st, a);
-  return launch_pdl(rows_quant_kernel<T, 4>, grid, dim3(RQ_THREADS), 0, st, a);
+  const dim3 grid((unsigned)a.M + (SCAN ? kScanParts : 0));
+  if (a.d <= 8 * RQ_THREADS) return launch_pdl(rows_quant_kernel<T, 1, SCAN>, grid, dim3(RQ_THREADS), 0, st, a);
+  if (a.d <= 16 * RQ_THREADS) return launch_pdl(rows_quant_kernel<T, 2, SCAN>, grid, dim3(RQ_THREADS), 0, st, a);
+  return launch_pdl(rows_quant_kernel<T, 4, SCAN>, grid, dim3(RQ_THREADS), 0, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_rows_quant(const RowsQuantArgs& a, cudaStream_t st) {
-  return a.x_type == DFSSM_BF16 ? launch<__nv_bfloat16>(a, st) : launch<float>(a, st);
+  if (a.scan) return a.x_type == DFSSM_BF16 ? launch<__nv_bfloat16, true>(a, st) : launch<float, true>(a, st);
+  return a.x_type == DFSSM_BF16 ? launch<__nv_bfloat16, false>(a, st) : launch<float, false>(a, st);
 }
 
 }  // namespace dfssm

@@ -417,9 +417,12 @@ int dfssm_head_loss(const int8_t* W, const float* s_row, int V, int d, const voi
  *   dx = r (du norm_w) - x r^3 / d sum_i(du norm_w x).   dx rows of x's type, lddx apart.
  *   ds_row[v] = sum_t G[t][v] acc[t][v] s[t]     device f32 [V] or NULL (not computed)
  *   dnorm_w[i] = sum_t du[t][i] x[t][i] r[t]     device f32 [d] or NULL (not computed; needs norm_w)
- * W's codes are frozen integers and get no gradient.  Within du the coefficients softmax s_row are rounded to 24
- * bits below a part of at least 1/16 of their largest possible value (23 and a sign when a row scale is negative), and
- * everything after that is exact up to the final rounding.  (Row scales all below 1e-30 leave dx its label's part.)
+ * W's codes are frozen integers and get no gradient.  Within du the coefficients softmax s_row of a token's rows other
+ * than its label are rounded (right on average) to steps of 2^-24 tau (2^-23 when a row scale is negative), and
+ * everything after that is exact up to the final rounding.  tau is about P s_top min(1, S / 32): P the largest softmax
+ * among those rows, S their sum in units of it, s_top the largest |s_row|.  Up to 1024 rows whose |s_row| is far above the
+ * others' (8 times what all but an eighth of 128 equal parts of the rows reach) are left out of s_top; they widen
+ * the steps only of tokens that give them weight.  (Row scales all below 1e-30 leave dx its label's part.)
  * workspace: dfssm_workspace_size(DFSSM_OP_HEAD_LOSS_BACKWARD, M, d, V).
  */
 int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int V, int d, const void* x, int x_type,

@@ -137,3 +137,119 @@ def test_head_loss_of_one_row_and_tokens_that_are_not_finite(dev, M):
     assert torch.equal(loss.isnan(), bad) and not loss[~bad].any()
     dx, ds, _ = dfssm.head_loss_backward(W, sr, x, labels, stats, torch.ones(M, device=dev))
     assert bool(dx[bad].isnan().all()) and not dx[~bad].any() and bool(ds.isnan().all())
+
+
+# ------------------------------------------------------------------------------------ size of the errors
+
+
+def scale_top(sr):
+    """The row scale that the fixed point of du counts in, and whether rows are beyond it: the largest, or, where an
+    eighth of 128 parts of the rows have nothing above an eighth of that, the largest part's maximum within 8 times the
+    least but an eighth of the parts' (include/dfssm.h; parts are runs of 32 rows in turn, of one up to 4096 rows)."""
+    s, V = sr.abs(), len(sr)
+    run = 1 if V <= 4096 else 32
+    part = torch.arange(V, device=s.device) // run % 128
+    m = torch.zeros(128, device=s.device).scatter_reduce_(0, part, s, "amax")[:min(128, -(-V // run))].sort().values
+    least = m[len(m) * 16 // 128]
+    top = m[m <= 8 * least].max()
+    return (float(top), True) if least < m[-1] / 8 and top < m[-1] else (float(m[-1]), False)
+
+
+def error_sizes(ref, W, sr, labels):
+    """Variances to expect of the errors of du [M][d] and ds_row [V].
+
+    A coefficient c = |G s_row| of a token (G the derivative by the logit) has a relative error of about
+    U (|l| + |m| + 4): the roundings of its logit and of the largest, the exponential, a few products.  In du it is
+    rounded to steps of its fixed point with a dither, which has the variance f (1 - f) <= min(c / step, 1/4) steps
+    squared.  Steps are 2^-24 (2^-23 with negative scales) of tau.  With p the token's largest |G| but the label's, S the
+    others' sum in units of it and `top` as above, tau is top p 2^-k, k <= 4 the largest with S 2^k <= 32; where rows are
+    beyond the top, C and A the largest and the sum of the token's c in those, it is the power of two above
+    max(top p min(1, S / 16), min(C, A / 16)), and 2^-8 more; more than 1024 such rows count as if C were the largest
+    scale times p, and A that times S.  The rows' errors are independent, so their squares add
+    up, weighted with the squares of W."""
+    u = base.U
+    at = torch.where(ref["kept"], labels, torch.zeros_like(labels)).long()[:, None]
+    s = sr.double().abs()
+    L = ref["acc_s"] * sr.double()
+    m = L.scatter(1, at, -float("inf")).amax(1, keepdim=True)
+    r = u * (L.abs() + m.abs() + 4)
+    c = ref["G"].abs() * s
+    rest = c.scatter(1, at, 0.0)
+    others = ref["G"].abs().scatter(1, at, 0.0)
+    p = others.amax(1)
+    S = others.sum(1) / p
+    top, beyond = scale_top(sr)
+    if beyond:
+        out = rest[:, sr.abs() > top]
+        C, A = (out.amax(1), out.sum(1)) if out.shape[1] <= 1024 else (s.max() * p, s.max() * p * S)
+        tau = 2.02 * torch.maximum(top * p * (S / 16).clamp(max=1), torch.minimum(C, A / 16))
+    else:
+        tau = top * p * 2.0 ** -torch.floor(torch.log2(32 / (S * 1.0001))).clamp(0, 4)
+    step = (2.0 ** -23 if bool((sr < 0).any()) else 2.0 ** -24) * tau[:, None]
+    var = (r * c).square() + torch.minimum(rest * step, step.square() / 4)
+    e_du = var @ W.double().square() + (u * ref["du"]).square()
+    # products of three fp32 numbers, sums of 32 tokens in fp32
+    e_ds = ((r + 6 * u) * ref["G"] * ref["acc_s"]).square().sum(0)
+    return e_du, e_ds
+
+
+def rms(x, dim=()):
+    return x.double().square().mean(dim).sqrt()
+
+
+ERROR_SHAPES = [(40, 20000, 512, 0.0), (40, 20000, 512, 0.5), (300, 20000, 512, 0.0), (300, 20000, 512, 0.5),
+                (3, 5000, 1024, 0.2), (100, 3001, 256, 1.0), (600, 50288, 1040, 0.1)]
+# row scales, and of how many rows (one by one, or side by side) they are larger, how much, and whether those rows have
+# codes
+ERROR_SCALES = [("even", 0, 1, False), ("even", 1, 10, False), ("even", 1, 1e2, False), ("even", 1, 1e4, False),
+                ("even", 1, 1e4, True), ("even", 2, 1e5, True), ("even", 200, 1e3, True), ("signed", 0, 1, False),
+                ("signed", 1, 1e3, True), ("decades", 0, 1, False), ("decades", 3, 1e3, True), ("even", -100, 1e3, False),
+                ("even", -2000, 1e3, False)]
+
+
+@pytest.mark.parametrize("kind,count,factor,codes", ERROR_SCALES)
+@pytest.mark.parametrize("M,V,d,peak", ERROR_SHAPES)
+def test_head_gradient_errors_in_the_mean(dev, M, V, d, peak, kind, count, factor, codes):
+    """Errors of dx, the row scales' and the norm weight's gradient against their expected root mean square, token by
+    token (three times) and altogether (twice), for flat and peaked distributions, and for row scales of very different
+    sizes: a row whose scale is large must not cost the tokens that give it no weight their precision."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(140 + M, dev)
+    W, sr = matrix(g, V, d, dev)
+    if kind == "decades":
+        sr = 10.0 ** (torch.rand(V, generator=g, device=dev) * -4 - 3)
+    elif kind == "signed":
+        sr = sr * (torch.randint(0, 2, (V,), generator=g, device=dev) * 2 - 1)
+    if count:
+        large = torch.randperm(V, generator=g, device=dev)[:count] if count > 0 else torch.arange(V + count - 7, V - 7)
+        sr[large] = factor * sr.abs().max()
+        if not codes:
+            W[large] = 0
+    labels = torch.randint(0, V, (M,), generator=g, device=dev, dtype=torch.int32)
+    other = torch.randint(0, V, (M,), generator=g, device=dev)
+    x = torch.randn(M, d, generator=g, device=dev) + peak * W[other].float() / 73
+    dloss = torch.rand(M, generator=g, device=dev) + 0.5
+    nw = torch.rand(d, generator=g, device=dev) + 0.5
+    torch.cuda.synchronize()
+    for w in (None, nw):
+        ref = base.head_reference(W, sr, x, w, labels, dloss)
+        e_du, e_ds = error_sizes(ref, W, sr, labels)
+        _, stats = dfssm.head_loss(W, sr, x, labels, norm_w=w)
+        dx, ds, dn = dfssm.head_loss_backward(W, sr, x, labels, stats, dloss, norm_w=w)
+        got, want = rms(ds.double() - ref["ds"]), e_ds.mean().sqrt()
+        print(f"ds {got / rms(ref['ds']):.2e} of {want / rms(ref['ds']):.2e}", end="; ")
+        assert got <= 2 * want
+        if w is None:
+            got, want = rms(dx.double() - ref["dx"]), e_du.mean().sqrt()
+            print(f"dx {got / rms(ref['dx']):.2e} of {want / rms(ref['dx']):.2e}", end="; ")
+            assert got <= 2 * want
+            got, want, size = rms(dx.double() - ref["dx"], 1), e_du.mean(1).sqrt(), rms(ref["dx"], 1)
+            print(f"tokens {(got / size).median():.2e}, {(got / size).max():.2e} at most {(got / want).max():.2f} of expected")
+            assert bool((got <= 3 * want).all())
+        else:
+            # a few fp32 roundings of each term, and of the sums
+            n = x.double() * ref["inv"]
+            got = rms(dn.double() - ref["dn"])
+            want = ((e_du + (4 * base.U * ref["du"]).square()) * n.square()).sum(0).mean().sqrt()
+            print(f"dnorm {got / rms(ref['dn']):.2e} of {want / rms(ref['dn']):.2e}")
+            assert got <= 2 * want
