@@ -417,6 +417,8 @@ int dfssm_head_loss(const int8_t* W, const float* s_row, int V, int d, const voi
  *   dx = r (du norm_w) - x r^3 / d sum_i(du norm_w x).   dx rows of x's type, lddx apart.
  *   ds_row[v] = sum_t G[t][v] acc[t][v] s[t]     device f32 [V] or NULL (not computed)
  *   dnorm_w[i] = sum_t du[t][i] x[t][i] r[t]     device f32 [d] or NULL (not computed; needs norm_w)
+ * A token that holds an infinity or a NaN makes its dx, ds_row and dnorm_w NaN, with a dloss of 0 as well; an ignored
+ * label leaves it out.
  * W's codes are frozen integers and get no gradient.  Within du the coefficients softmax s_row of a token's rows other
  * than its label are rounded (right on average) to steps of 2^-24 tau (2^-23 when a row scale is negative), and
  * everything after that is exact up to the final rounding.  tau is about P s_top min(1, S / 32): P the largest softmax

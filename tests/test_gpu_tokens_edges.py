@@ -139,6 +139,113 @@ def test_head_loss_of_one_row_and_tokens_that_are_not_finite(dev, M):
     assert bool(dx[bad].isnan().all()) and not dx[~bad].any() and bool(ds.isnan().all())
 
 
+@pytest.mark.parametrize("M", [3, 40, 100, 200, 300])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_head_loss_of_odd_tokens_in_every_kernel(dev, M, norm, dtype):
+    """Ignored labels, labels past the vocabulary, rows of zeros and rows that are not finite, at the sizes of every
+    variant of the products and with the norm's backward."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(100 + M, dev)
+    V, d = 700, 144
+    W, sr = matrix(g, V, d, dev)
+    nw = torch.rand(d, generator=g, device=dev) + 0.5 if norm else None
+    x = torch.randn(M, d, generator=g, device=dev).to(dtype)
+    ones = torch.ones(M, device=dev)
+    # all ignored, some of them not finite
+    none = torch.full((M,), -2 ** 31, dtype=torch.int32, device=dev)
+    none[1::2] = -1
+    xi = x.clone()
+    xi[0] = float("nan")
+    loss, stats = dfssm.head_loss(W, sr, xi, none, norm_w=nw)
+    dx, ds, dn = dfssm.head_loss_backward(W, sr, xi, none, stats, ones, norm_w=nw)
+    assert not loss.any() and not dx.any() and not ds.any() and (dn is None or not dn.any())
+    # finite losses and gradients beside a bad label, an ignored row that is not finite, and zeros
+    labels = torch.randint(0, V, (M,), generator=g, device=dev, dtype=torch.int32)
+    labels[0], labels[1] = V, -1
+    x[1, 7] = float("nan")
+    x[2] = 0.0
+    ws = dfssm.workspace(dfssm.workspace_size(dfssm.OP_HEAD_LOSS, M, d, V), dev)
+    loss, stats = dfssm.head_loss(W, sr, x, labels, norm_w=nw, ws=ws)
+    assert dfssm.device_status(ws) == -1 and dfssm.device_status(ws) == 0
+    assert float(loss[0]) == 0 and float(loss[1]) == 0 and bool(loss.isfinite().all())
+    # flat logits: the sum of V - 1 ones is exact, its logarithm and the loss are rounded
+    assert abs(float(loss[2]) - np.log(V)) <= 2.0 ** -22 * np.log(V)
+    dx, ds, dn = dfssm.head_loss_backward(W, sr, x, labels, stats, ones, norm_w=nw)
+    assert not dx[:2].any()
+    for t in (dx, ds, dn):
+        assert t is None or bool(t.isfinite().all())
+    # a row that is not finite and has a label: NaN in its own loss and dx, and in the sums over tokens
+    for value in (float("inf"), float("nan")):
+        x[2, 100] = value
+        loss, stats = dfssm.head_loss(W, sr, x, labels, norm_w=nw)
+        assert bool(loss[2].isnan()) and int(loss.isnan().sum()) == 1
+        dx, ds, dn = dfssm.head_loss_backward(W, sr, x, labels, stats, ones, norm_w=nw)
+        assert bool(dx[2].isnan().all()) and int(dx.isnan().sum()) == d
+        assert bool(ds.isnan().all()) and (dn is None or bool(dn.isnan().all()))
+
+
+@pytest.mark.parametrize("M", [1, 4, 20, 130, 300])
+@pytest.mark.parametrize("norm", [False, True])
+def test_linear_int8_of_odd_tokens_in_every_kernel(dev, M, norm):
+    """Rows of zeros, tiny rows and rows that are not finite among ordinary ones, at the sizes of every variant."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(120 + M, dev)
+    V, d = 500, 272
+    W, sr = matrix(g, V, d, dev)
+    nw = torch.rand(d, generator=g, device=dev) + 0.5 if norm else None
+    for first in range(3):  # every kind of row is the first token once
+        x = torch.randn(M, d, generator=g, device=dev)
+        kinds = [(first + k) % 4 for k in range(M)]
+        x[[k == 0 for k in kinds]] = 0.0
+        x[[k == 1 for k in kinds]] *= 1e-38
+        bad = torch.tensor([k == 2 for k in kinds], device=dev)
+        x[bad, 17] = float("nan") if first else float("-inf")
+        acc = torch.zeros(M, V, dtype=torch.int32, device=dev)
+        scale = torch.zeros(M, device=dev)
+        y = dfssm.linear_int8(W, sr, x, norm_w=nw, debug=dict(acc=acc, xscale=scale))
+        want = (acc.double() * scale.double()[:, None] * sr.double()).float()
+        assert bool(y[bad].isnan().all()) and torch.equal(y[~bad], want[~bad]) and bool(y[~bad].isfinite().all())
+        _, q, s, _ = base.quantized(x, nw)
+        assert torch.equal(scale[~bad], s[~bad, 0])
+        assert torch.equal(acc[~bad].double(), (q @ W.double().t())[~bad])
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("norm", [False, True])
+def test_head_gradient_of_weights_of_zero(dev, M, norm):
+    """A token whose dloss is 0 has no gradient, but 0 times NaN is NaN: one that is not finite has to be left out by its
+    label."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(130 + M, dev)
+    V, d = 900, 272
+    W, sr = matrix(g, V, d, dev)
+    nw = torch.rand(d, generator=g, device=dev) + 0.5 if norm else None
+    x = torch.randn(M, d, generator=g, device=dev)
+    labels = torch.randint(0, V, (M,), generator=g, device=dev, dtype=torch.int32)
+    dloss = torch.rand(M, generator=g, device=dev)
+    dloss[1] = 0
+    _, stats = dfssm.head_loss(W, sr, x, labels, norm_w=nw)
+    dx, ds, dn = dfssm.head_loss_backward(W, sr, x, labels, stats, dloss, norm_w=nw)
+    assert not dx[1].any() and bool(dx[0].any())
+    # the same as without its label (from the same statistics: the order of a token's sums in the forward pass may
+    # depend on where the labels around it are)
+    without = labels.clone()
+    without[1] = -1
+    for a, b in zip(dfssm.head_loss_backward(W, sr, x, without, stats, dloss, norm_w=nw), (dx, ds, dn)):
+        assert a is None or torch.equal(a, b)
+    _, stats = dfssm.head_loss(W, sr, x, without, norm_w=nw)
+    finite = dfssm.head_loss_backward(W, sr, x, without, stats, dloss, norm_w=nw)
+    x[1, 3] = float("inf")
+    _, stats = dfssm.head_loss(W, sr, x, without, norm_w=nw)
+    for a, b in zip(dfssm.head_loss_backward(W, sr, x, without, stats, dloss, norm_w=nw), finite):
+        assert a is None or torch.equal(a, b)
+    _, stats = dfssm.head_loss(W, sr, x, labels, norm_w=nw)
+    dx, ds, dn = dfssm.head_loss_backward(W, sr, x, labels, stats, dloss, norm_w=nw)
+    assert bool(dx[1].isnan().all()) and int(dx.isnan().sum()) == d
+    assert bool(ds.isnan().all()) and (dn is None or bool(dn.isnan().all()))
+
+
 # ------------------------------------------------------------------------------------ size of the errors
 
 
