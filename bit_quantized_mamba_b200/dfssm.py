@@ -569,10 +569,12 @@ def embed_tokens(W, s_row, tokens, h=None, dtype=torch.float32, ws=None, stream=
     return h
 
 
-def embed_tokens_backward(W, tokens, dh, dE=None, ds_row=None, accumulate=False, ws=None, stream=None):
+def embed_tokens_backward(W, tokens, dh, dE=None, ds_row=None, accumulate=False, ws=None, stream=None, table=True,
+                          scales=True):
     """Gradients of embed_tokens for dh [n][d]: (dE [V][d], ds_row [V]) (dfssm_embed_tokens_backward).  With
     accumulate the sums are added to the tensors given (either may be left out); otherwise both are written,
-    into new tensors where none are given."""
+    into new tensors where none are given.  table=False leaves out dE, scales=False ds_row (None unless a tensor is
+    given)."""
     V, d = _matrix(W)
     n = tokens.numel()
     st = _on(stream, W, tokens, dh, dE, ds_row, ws)
@@ -580,10 +582,12 @@ def embed_tokens_backward(W, tokens, dh, dE=None, ds_row=None, accumulate=False,
         if dE is None and ds_row is None:
             raise ValueError("accumulate needs dE or ds_row")
     else:
-        if dE is None:
+        if dE is None and table:
             dE = _new(stream, W, (V, d), torch.float32)
-        if ds_row is None:
+        if ds_row is None and scales:
             ds_row = _new(stream, W, (V,), torch.float32)
+        if dE is None and ds_row is None:
+            raise ValueError("nothing to compute: table and scales are both left out")
     ws = _ws(ws, stream, OP_EMBED_BACKWARD, n, d, V, W)
     pd, td, ld = _rows(dh, n, d, "dh")
     _check("dfssm_embed_tokens_backward", lib().dfssm_embed_tokens_backward(

@@ -246,6 +246,66 @@ def test_head_gradient_of_weights_of_zero(dev, M, norm):
     assert bool(ds.isnan().all()) and (dn is None or bool(dn.isnan().all()))
 
 
+# ------------------------------------------------------------------------------------ optional outputs
+
+
+@pytest.mark.parametrize("n,V,d", [(1, 40, 16), (700, 90, 272), (3000, 5000, 4096), (17000, 300, 64)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_gradient_of_one_kind(dev, n, V, d, accumulate):
+    """The table's or the row scales' gradient alone has the bits that it has beside the other, written or added."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(n + d, dev)
+    W, _ = matrix(g, V, d, dev)
+    tok = (torch.rand(n, generator=g, device=dev) ** 3 * V).int().clamp(max=V - 1)
+    dh = torch.randn(n, d, generator=g, device=dev)
+
+    def start():
+        return (torch.full((V, d), 0.5, device=dev), torch.full((V,), 0.25, device=dev)) if accumulate else (None, None)
+
+    both = dfssm.embed_tokens_backward(W, tok, dh, *start(), accumulate=accumulate)
+    dE, none = dfssm.embed_tokens_backward(W, tok, dh, start()[0], accumulate=accumulate, scales=False)
+    assert none is None and torch.equal(dE, both[0])
+    none, ds = dfssm.embed_tokens_backward(W, tok, dh, None, start()[1], accumulate=accumulate, table=False)
+    assert none is None and torch.equal(ds, both[1])
+
+
+def test_embed_gradient_of_nothing_is_refused(dev):
+    from bit_quantized_mamba_b200 import dfssm
+    W, _ = matrix(gen(1, dev), 10, 32, dev)
+    tok, dh = torch.zeros(2, dtype=torch.int32, device=dev), torch.zeros(2, 32, device=dev)
+    with pytest.raises(ValueError):
+        dfssm.embed_tokens_backward(W, tok, dh, table=False, scales=False)
+    with pytest.raises(ValueError):
+        dfssm.embed_tokens_backward(W, tok, dh, accumulate=True)
+
+
+@pytest.mark.parametrize("M", [5, 200])
+def test_head_gradient_without_the_norms(dev, M):
+    """dnorm_w may be left out although there is a norm (through the C ABI): dx and ds_row keep their bits, what lies
+    where it would be stays."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(M, dev)
+    V, d = 800, 144
+    W, sr = matrix(g, V, d, dev)
+    x = torch.randn(M, d, generator=g, device=dev)
+    nw = torch.rand(d, generator=g, device=dev) + 0.5
+    y = torch.randint(0, V, (M,), generator=g, device=dev, dtype=torch.int32)
+    dl = torch.rand(M, generator=g, device=dev)
+    _, stats = dfssm.head_loss(W, sr, x, y, norm_w=nw)
+    dx, ds, _ = dfssm.head_loss_backward(W, sr, x, y, stats, dl, norm_w=nw)
+    size = dfssm.workspace_size(dfssm.OP_HEAD_LOSS_BACKWARD, M, d, V)
+    ws, dx2, ds2 = dfssm.workspace(size, dev), torch.zeros_like(dx), torch.zeros_like(ds)
+    torch.cuda.synchronize()
+    p = [t.data_ptr() for t in (W, sr, x, nw, y, stats, dl, dx2, ds2, ws)]
+    for scale_grad in (p[8], None):
+        assert dfssm.lib().dfssm_head_loss_backward(p[0], p[1], V, d, p[2], 0, d, M, p[3], p[4], p[5], p[6], p[7], d,
+                                                    scale_grad, None, p[9], size, None) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(dx2, dx) and torch.equal(ds2, ds)
+        dx2.zero_()
+        torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------------------------ size of the errors
 
 
