@@ -470,6 +470,10 @@ def generate(stack: "LayerStack", W, s_row, final_norm_w, tokens, hidden_taps=No
 
 
 # ------------------------------------------------------- many tokens on the int8 matrix (embedding / LM head)
+#
+# W's codes must be complete before a call is enqueued: the kernels request them ahead of the preceding kernel's end
+# (include/dfssm.h).  After work that writes W on the GPU (a requantization, a copy), synchronize once.  Everything else,
+# row scales and norm weights among it, is read in stream order.
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
@@ -532,7 +536,8 @@ def _matrix(W):
 
 def linear_int8(W, s_row, x, y=None, norm_w=None, out_dtype=torch.float32, ws=None, debug=None, stream=None):
     """y [M][V] = the int8 head's product for every row of x [M][d] (dfssm_linear_int8); x f32 or bf16, rows may
-    be strided.  debug: dict of optional taps acc [M][V], xq [M][d], xscale [M]."""
+    be strided.  W must be complete before the call, not just earlier in the stream.  debug: dict of optional taps
+    acc [M][V], xq [M][d], xscale [M]."""
     V, d = _matrix(W)
     M = x.shape[0]
     st = _on(stream, W, s_row, x, y, norm_w, ws, *(debug.values() if debug else ()))
@@ -599,7 +604,8 @@ def embed_tokens_backward(W, tokens, dh, dE=None, ds_row=None, accumulate=False,
 
 def head_loss(W, s_row, x, labels, norm_w=None, loss=None, stats=None, ws=None, stream=None):
     """Cross entropy of the int8 head's logits for every row of x [M][d] (dfssm_head_loss); labels device int32
-    [M], negative = ignored.  Returns (loss [M], stats [3][M]); stats is what head_loss_backward needs."""
+    [M], negative = ignored.  W must be complete before the call, not just earlier in the stream.  Returns (loss [M],
+    stats [3][M]); stats is what head_loss_backward needs."""
     V, d = _matrix(W)
     M = x.shape[0]
     st = _on(stream, W, s_row, x, labels, norm_w, loss, stats, ws)
@@ -620,8 +626,8 @@ def head_loss(W, s_row, x, labels, norm_w=None, loss=None, stats=None, ws=None, 
 def head_loss_backward(W, s_row, x, labels, stats, dloss, norm_w=None, dx=None, ds_row=None, dnorm_w=None,
                        scales=True, ws=None, stream=None):
     """Gradients of sum(dloss * loss) (dfssm_head_loss_backward): (dx [M][d] of x's type, ds_row [V],
-    dnorm_w [d]).  scales=False leaves out ds_row (None unless a tensor is given); dnorm_w is None without
-    norm_w."""
+    dnorm_w [d]).  W must be complete before the call, not just earlier in the stream.  scales=False leaves out ds_row
+    (None unless a tensor is given); dnorm_w is None without norm_w."""
     V, d = _matrix(W)
     M = x.shape[0]
     st = _on(stream, W, s_row, x, labels, stats, dloss, norm_w, dx, ds_row, dnorm_w, ws)
