@@ -9,7 +9,7 @@
 //
 // Forward: the int8 product with tokens on the tensor memory's lanes and rows of W on its columns; a thread
 // owns a token's logits of a tile and folds them into a running (max, sum), one pass, 8 bytes kept per
-// token, tile and column half; a second kernel joins them.  (Up to 64 tokens: operands exchanged, one kernel.)
+// token, tile and column half; a second kernel joins them.  (Up to 16 tokens: operands exchanged, one kernel.)
 //
 // Gradient with respect to the (dequantised) normalised token:  du = g [sum_{v != y} p_v s_row_v W_v -
 // (1 - p_y) s_row_y W_y].  The coefficients c_v = exp(l_v - m) s_row_v / max|s_row| lie in [0, 1] (or [-1, 1] with
@@ -276,10 +276,13 @@ __global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float
 
 // ------------------------------------------------------------------------------------ forward, few tokens
 
-// Up to 64 tokens: rows of W on the lanes, tokens on the columns (sixteen per epilogue warp), so that W streams through
-// a deep ring of narrow stages.  A thread keeps a running (max, sum) over its rows for every token, lanes and
-// warps are joined at the end, and the last CTA to finish joins the CTAs and writes the losses.
-constexpr int SMALL_TOKENS = 64;
+// Up to 16 tokens: rows of W on the lanes, tokens on the columns, so that W streams through a deep ring of narrow
+// stages.  A thread of the four epilogue warps that sum (all sixteen quantize) keeps a running (max, sum) over its rows
+// for every token, lanes and warps are joined at the end, and the last CTA to finish joins the CTAs and writes the losses.
+// What it takes grows with every token, the other form's time hardly (rows of 2048 and of 1040 values, 50288 / 20011:
+// 5 tokens 24.7 / 14.9 us here, 32.2 / 17.2 there; 16 tokens 29.1 / 18.7 and 31.9 / 17.7; 32 tokens 34.4 / 24.2 and
+// 32.8 / 17.4; 64 tokens 45.7 / 34.1 and 27.3 / 17.4).
+constexpr int SMALL_TOKENS = 16;
 template <bool RESIDENT_>
 struct SmallForwardPolicy {
   static constexpr int CG = 1;
@@ -325,17 +328,17 @@ struct SmallForwardPolicy {
     Scratch* sc;
     int q, part, lane;
     float sw;
-    float m[16], S[16];
+    float m[SMALL_TOKENS], S[SMALL_TOKENS];
     __device__ __forceinline__ Epilogue(const Args& a, unsigned char* sm, int q_, int part_, int lane_)
         : sc(reinterpret_cast<Scratch*>(sm)), q(q_), part(part_), lane(lane_) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < SMALL_TOKENS; ++j) {
         m[j] = -INFINITY;
         S[j] = 0.0f;
       }
-      // each warp fills (and reads) its own tokens; the four quadrants write the same values
-      const int t = part * 16 + lane;
-      if (lane < 16) {
+      // the four quadrants write the same values, and each reads its own
+      const int t = lane;
+      if (part == 0 && t < SMALL_TOKENS) {
         sc->label[t] = t < a.M ? ld_s32(a.labels + t) : -1;
         if (!RESIDENT) sc->s[t] = t < a.M ? (float)a.s_tok[t] : 0.0f;
       }
@@ -353,18 +356,17 @@ struct SmallForwardPolicy {
     }
     __device__ __forceinline__ void tile(const Args& a, const Tile& t, uint32_t taddr) {
       const int r = q * 32 + lane, row = t.a0 + r;
-      if (part * 16 >= a.M) return;
-      uint32_t v[16];
-      tmem_ld16(taddr + (uint32_t)(part * 16), v);
+      if (part > 0) return;
+      uint32_t v[SMALL_TOKENS];
+      tmem_ld16(taddr, v);
       tmem_wait(v);
       if (r >= t.na) return;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int tok = part * 16 + j;
-        if (tok >= a.M) break;
-        const float st = scale(tok), x = (float)(int)v[j] * st;
-        if (row == sc->label[tok]) {  // the label's own logit stays out of the sum
-          a.stats[2 * (size_t)a.M + tok] =
+      for (int j = 0; j < SMALL_TOKENS; ++j) {
+        if (j >= a.M) break;
+        const float st = scale(j), x = (float)(int)v[j] * st;
+        if (row == sc->label[j]) {  // the label's own logit stays out of the sum
+          a.stats[2 * (size_t)a.M + j] =
               __double2float_rn(dmul(dmul(int_to_f64((int)v[j]), (double)st), (double)ld_f32(a.s_row + row)));
         } else {
           const float mx = fmaxf(m[j], x * sw), mz = mx == -INFINITY ? 0.0f : mx;
@@ -374,12 +376,14 @@ struct SmallForwardPolicy {
       }
     }
     __device__ __forceinline__ void finish(const Args& a) {
+      if (part == 0) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if (RESIDENT && part * 16 + j >= a.M) break;  // (1 token: 27 -> 26 us; with more the branches cost 2 us)
-        const float mx = warp_max(m[j]), mz = mx == -INFINITY ? 0.0f : mx;
-        const float s = warp_sum(S[j] * ex2(m[j] - mz));
-        if (lane == j) sc->red[q][part * 16 + j] = make_float2(mx, s);
+        for (int j = 0; j < SMALL_TOKENS; ++j) {
+          if (RESIDENT && j >= a.M) break;  // (1 token: 27 -> 26 us; with more the branches cost 2 us)
+          const float mx = warp_max(m[j]), mz = mx == -INFINITY ? 0.0f : mx;
+          const float s = warp_sum(S[j] * ex2(m[j] - mz));
+          if (lane == j) sc->red[q][j] = make_float2(mx, s);
+        }
       }
       epilogue_sync();
       const int tid = threadIdx.x - 64;

@@ -401,7 +401,7 @@ int dfssm_embed_tokens_backward(const int8_t* W, int V, int d, const int32_t* to
  *   loss[t] = log sum_v exp l[t][v] - l[t][labels[t]]     device f32 [M]
  * labels device i32 [M]; a negative label is ignored (loss 0, no gradient), one >= V is ignored too and gives
  * DFSSM_EINVAL from dfssm_device_status.  A token that holds an infinity or a NaN has loss NaN.
- * stats device f32 [3][M] receives what dfssm_head_loss_backward needs (opaque).  Up to 64 tokens the CTAs count
+ * stats device f32 [3][M] receives what dfssm_head_loss_backward needs (opaque).  Up to 16 tokens the CTAs count
  * themselves in the workspace: zero-filled before its first use, every call leaves the count zero.
  * workspace: dfssm_workspace_size(DFSSM_OP_HEAD_LOSS, M, d, V).
  */
