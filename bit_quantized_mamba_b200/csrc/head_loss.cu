@@ -1106,7 +1106,9 @@ struct ForwardWs {
   size_t q, s, part, total;
 };
 // How tokens and columns are tiled: up to 128 tokens by single CTAs (the stream of W bounds the products), above
-// by pairs.
+// by pairs.  (50288 x 2048, single against pairs: loss of 96 tokens 27.5 / 30.7 us, of 256 33.8 / 31.8; gradient of 96 101.7 /
+// 101.8, of 192 135 / 124.  Over 8191 x 1040 it is the other way round by up to 12 %: 14.4 us of 96 tokens' loss in pairs, 13.8
+// instead of 15.4 of 129's in single ones.)
 struct Layout {
   int cg, tb;      // CTAs per tile; tokens of a block of digits
   size_t mp, dp;   // tokens and columns of W, padded to whole tiles
@@ -1486,9 +1488,10 @@ extern "C" int dfssm_head_loss_backward(const int8_t* W, const float* s_row, int
   p.Vp = pc.rows;
   p.l = layout(M, d);
   // the digits are bound by their epilogue, which takes a tile's empty lanes as long as full ones: single CTAs where
-  // pairs would have a fifth more lanes (333 tokens x 20011 x 1040: 97.4 -> 95.0 us, 600: 131 -> 128; at 850, with an
-  // eighth more, 159 against 160)
-  const bool one = ceil_div(M, 2 * BM) * 2 * 5 >= ceil_div(M, BM) * 6;
+  // pairs would have an eighth more lanes (gradient, single against pairs, 50288 x 2048, 20011 x 1040 and 8191 x 1040: 333
+  // tokens, a third more lanes, 178 / 182, 64 / 68, 49 / 50 us; 850, a seventh more, 328 / 337, 110 / 113, 69 / 69; 1100, a
+  // ninth, 423 / 425, 151 / 150, 78 / 78; 450, none, 217 / 215, 76 / 75, 54 / 53)
+  const bool one = ceil_div(M, 2 * BM) * 2 * 8 >= ceil_div(M, BM) * 9;
   const auto products = p.l.cg == 1 ? (ds_row ? piece_products<1, 1, true> : piece_products<1, 1, false>)
                         : one       ? (ds_row ? piece_products<1, 2, true> : piece_products<1, 2, false>)
                                     : (ds_row ? piece_products<2, 2, true> : piece_products<2, 2, false>);

@@ -195,7 +195,8 @@ int launch_linear(const int8_t* W, const float* s_row, int V, const RowsQuantArg
 }
 
 // One to four tokens: one kernel does it all; up to 128 the stream of W bounds the product and single CTAs keep more of it
-// in flight; above, pairs halve the traffic of the tokens' codes.
+// in flight; above, pairs halve the traffic of the tokens' codes.  (50288 x 2048, single against pairs: 65 tokens 25.5 / 26.3
+// us, 128 28.6 / 28.8, 192 32.5 / 32.4, 256 37.9 / 35.7; 20011 x 1040: 65 13.9 / 15.7, 256 22.1 / 20.0.)
 template <typename Y>
 int launch_linear(const int8_t* W, const float* s_row, int V, const RowsQuantArgs& qa, void* y, int64_t ldy, int32_t* acc,
                   int* err, cudaStream_t st) {

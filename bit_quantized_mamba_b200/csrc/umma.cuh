@@ -34,16 +34,6 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
 }
-__device__ __forceinline__ f2 neg2(f2 a) {
-  f2 r;
-  r.v = a.v ^ 0x8000000080000000ull;
-  return r;
-}
-__device__ __forceinline__ f2 abs2(f2 a) {
-  f2 r;
-  r.v = a.v & 0x7FFFFFFF7FFFFFFFull;
-  return r;
-}
 
 constexpr long long kWaitBudget = 4000000000LL;  // clock cycles per wait (~2 s)
 
