@@ -92,7 +92,7 @@ struct ForwardPolicy {
     const double* s_tok;    // [M]
     const float* s_row;     // [V]
     const int32_t* labels;  // [M]
-    float* label_logit;     // [M]
+    int* label_acc;         // [M] the label's accumulator, in stats[2] until write_loss() takes it
     float2* part;           // [slots][M] (max, sum) in units of log 2
     int M, V;
   };
@@ -161,8 +161,7 @@ struct ForwardPolicy {
 #pragma unroll
         for (int j = 0; j < 16; ++j) x[j] = mul2(pack2((float)(int)v[2 * j], (float)(int)v[2 * j + 1]), st2);
         if (lc < 32u && c + (int)lc < t.nb) {
-          const int al = (int)pick(v, (int)lc);
-          a.label_logit[tok] = __double2float_rn(dmul(dmul(int_to_f64(al), a.s_tok[tok]), (double)ld_f32(a.s_row + label)));
+          a.label_acc[tok] = (int)pick(v, (int)lc);
         }
         if (c + 64 < t.nb) tmem_ld32(taddr + (uint32_t)c + 64, v);  // the next chunk, while this one is summed
         float mx = m;
@@ -210,24 +209,25 @@ struct ForwardPolicy {
   };
 };
 
-// Loss and stats of token t from the other rows' (max, sum); stats[2][t] holds the label's logit if there is one, and
-// 1 - p_y afterwards.  z is a difference of logits and wants fp64; exp z and what follows keep fp32's relative
-// precision without.
-__device__ __forceinline__ void write_loss(int t, float m, double S, int M, int V, const int32_t* labels, float* stats,
+// Loss and stats of token t from the other rows' (max, sum), its label y, and the scales of the token and of the label's
+// row; stats[2][t] holds the label's accumulator, and 1 - p_y afterwards.  z is a difference of logits and wants fp64 (the
+// label's logit too: rounded, it would be most of the error of a confident token's loss); exp z, with what fp32 leaves
+// of z as a factor, and what follows keep fp32's relative precision without.
+__device__ __forceinline__ void write_loss(int t, float m, double S, int y, double s, float s_label, int M, int V, float* stats,
                                            float* loss, int* status) {
-  const int y = labels[t];
   const bool bad = y >= V;
   if (bad) atomicExch(status, kBadTokenCode);
   float out = 0.0f, rest = 0.0f;
   if (y >= 0 && !bad) {
-    const float l = __ldcg(stats + 2 * (size_t)M + t);
+    const double l = dmul(dmul(int_to_f64(__ldcg(reinterpret_cast<const int*>(stats) + 2 * (size_t)M + t)), s), (double)s_label);
     if (S != 0.0) {
-      const double z = ((double)m + log2(S)) * kLn2 - (double)l;
-      const float e = expf(-fabsf((float)z));  // below 1
+      const double z = ((double)m + log2(S)) * kLn2 - l;
+      const float a = (float)fabs(z), e0 = expf(-a);
+      const float e = a < 104.0f ? fmaf(e0, (float)((double)a - fabs(z)), e0) : e0;  // below 1; from there on 0
       rest = z > 0.0 ? 1.0f / (1.0f + e) : e / (1.0f + e);
       out = z > 0.0 ? (float)(z + (double)log1pf(e)) : log1pf(e);
     } else if (l != l) {  // no other row, but the token is not finite
-      rest = out = l;
+      rest = out = (float)l;
     }
   }
   stats[t] = m;
@@ -239,13 +239,17 @@ __device__ __forceinline__ void write_loss(int t, float m, double S, int M, int 
 // Joins the partial (max, sum) of a token and forms its loss.  32 tokens per CTA, 32 slices of slots.
 constexpr int LF_SLICES = 32;
 __global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float2* part, int slots, int M, int V,
-                                                                     const int32_t* labels, float* stats, float* loss,
+                                                                     const int32_t* labels, const double* s_tok,
+                                                                     const float* s_row, float* stats, float* loss,
                                                                      int* status) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ float2 sm[LF_SLICES][33];
   const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
-  const int t = blockIdx.x * 32 + lane;
+  const int t = blockIdx.x * 32 + lane, tok = blockIdx.x * 32 + sl;  // summed by this lane, joined by this warp
+  const int y = tok < M ? labels[tok] : -1;
+  const double s_t = tok < M ? s_tok[tok] : 0.0;
+  const float s_label = y >= 0 && y < V ? ld_f32(s_row + y) : 0.0f;
   float m = -INFINITY, S = 0.0f;
   constexpr int U = 8;  // slots in flight
   for (int s0 = sl; s0 < slots; s0 += U * LF_SLICES) {
@@ -270,8 +274,7 @@ __global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float
   const float2 p = sm[lane][sl];
   const float mx = warp_max(p.x), mz = mx == -INFINITY ? 0.0f : mx;
   const double sum = warp_sum((double)(p.y * ex2(p.x - mz)));
-  const int tok = blockIdx.x * 32 + sl;
-  if (lane == 0 && tok < M) write_loss(tok, mx, sum, M, V, labels, stats, loss, status);
+  if (lane == 0 && tok < M) write_loss(tok, mx, sum, y, s_t, s_label, M, V, stats, loss, status);
 }
 
 // ------------------------------------------------------------------------------------ forward, few tokens
@@ -320,6 +323,7 @@ struct SmallForwardPolicy {
     ResidentScratch res;
     float s[SMALL_TOKENS];
     int label[SMALL_TOKENS];
+    float s_label[SMALL_TOKENS];  // the label's row scale
     float2 red[4][SMALL_TOKENS];
     int last;
   };
@@ -366,8 +370,7 @@ struct SmallForwardPolicy {
         if (j >= a.M) break;
         const float st = scale(j), x = (float)(int)v[j] * st;
         if (row == sc->label[j]) {  // the label's own logit stays out of the sum
-          a.stats[2 * (size_t)a.M + j] =
-              __double2float_rn(dmul(dmul(int_to_f64((int)v[j]), (double)st), (double)ld_f32(a.s_row + row)));
+          reinterpret_cast<int*>(a.stats)[2 * (size_t)a.M + j] = (int)v[j];
         } else {
           const float mx = fmaxf(m[j], x * sw), mz = mx == -INFINITY ? 0.0f : mx;
           S[j] = S[j] * ex2(m[j] - mz) + ex2(fmaf(x, sw, -mz));
@@ -377,6 +380,8 @@ struct SmallForwardPolicy {
     }
     __device__ __forceinline__ void finish(const Args& a) {
       if (part == 0) {
+        const int y = lane < a.M ? sc->label[lane] : -1;  // (a.M <= SMALL_TOKENS)
+        const float s_label = y >= 0 && y < a.V ? ld_f32(a.s_row + y) : 0.0f;
 #pragma unroll
         for (int j = 0; j < SMALL_TOKENS; ++j) {
           if (RESIDENT && j >= a.M) break;  // (1 token: 27 -> 26 us; with more the branches cost 2 us)
@@ -384,6 +389,7 @@ struct SmallForwardPolicy {
           const float s = warp_sum(S[j] * ex2(m[j] - mz));
           if (lane == j) sc->red[q][j] = make_float2(mx, s);
         }
+        if (lane < a.M) sc->s_label[lane] = s_label;
       }
       epilogue_sync();
       const int tid = threadIdx.x - 64;
@@ -416,7 +422,8 @@ struct SmallForwardPolicy {
           s += (double)(p.y * ex2(p.x - mz));
         }
         s = warp_sum(s);
-        if (lane == 0) write_loss(t, mx, s, a.M, a.V, a.labels, a.stats, a.loss, a.c.err);
+        if (lane == 0)
+          write_loss(t, mx, s, sc->label[t], (double)scale(t), sc->s_label[t], a.M, a.V, a.stats, a.loss, a.c.err);
       }
     }
   };
@@ -1277,7 +1284,7 @@ int forward(const int8_t* W, const float* s_row, int V, const RowsQuantArgs& qa,
   a.s_tok = qa.s;
   a.s_row = s_row;
   a.labels = labels;
-  a.label_logit = stats + 2 * (size_t)M;
+  a.label_acc = reinterpret_cast<int*>(stats + 2 * (size_t)M);
   a.part = part;
   a.M = M;
   a.V = V;
@@ -1287,7 +1294,7 @@ int forward(const int8_t* W, const float* s_row, int V, const RowsQuantArgs& qa,
   const int slots = 2 * (a.r.mode == kGrid ? ceil_div(V, a.r.tile_b) : groups);
   if (e == cudaSuccess)
     e = launch_pdl(loss_finish_kernel, dim3(ceil_div(M, 32)), dim3(32 * LF_SLICES), 0, st, (const float2*)part, slots, M, V,
-                   labels, stats, loss, err);
+                   labels, (const double*)qa.s, s_row, stats, loss, err);
   return e == cudaSuccess ? DFSSM_OK : record_cuda_failure(e);
 }
 

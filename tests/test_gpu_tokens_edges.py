@@ -420,3 +420,30 @@ def test_head_gradient_errors_in_the_mean(dev, M, V, d, peak, kind, count, facto
             want = ((e_du + (4 * base.U * ref["du"]).square()) * n.square()).sum(0).mean().sqrt()
             print(f"dnorm {got / rms(ref['dn']):.2e} of {want / rms(ref['dn']):.2e}")
             assert got <= 2 * want
+
+
+@pytest.mark.parametrize("M", [1, 3, 16, 40, 128, 500])
+def test_loss_of_confident_tokens_in_the_mean(dev, M):
+    """Tokens whose label's logit is tens above flat others: the relative error of a loss near exp(-z) is the error of z.
+    The label's logit, the largest number there, must not cost it fp32's rounding (U |l| / sqrt 3 in the mean, 2e-6 to
+    4e-6 here).  What remains: the others' logits (two roundings of at most max|l| = 6 each, independent over thousands of
+    rows), their exponentials (2^-22 each, likewise), the sums of up to 20000 positive terms by threads that each add
+    some tens or hundreds (a few U), and five roundings after z: 12 U in the mean."""
+    from bit_quantized_mamba_b200 import dfssm
+    d, V = 1024, 20000
+    got = []
+    for k in range(-(-60 // M)):
+        g = gen(500 + M + k, dev)
+        W, sr = matrix(g, V, d, dev)
+        labels = torch.randint(0, V, (M,), generator=g, device=dev, dtype=torch.int32)
+        x = torch.randn(M, d, generator=g, device=dev)
+        x += (torch.rand(M, 1, generator=g, device=dev) * 1.5 + 0.8) * W[labels.long()].float() / 73
+        torch.cuda.synchronize()
+        ref = base.head_reference(W, sr, x, None, labels)
+        loss, _ = dfssm.head_loss(W, sr, x, labels)
+        L = ref["loss"]
+        some = (L > 1e-30) & (L < 1e-6)
+        got.append(((loss.double() - L) / L)[some])
+    got = torch.cat(got)
+    print(f"{len(got)} tokens, {rms(got):.2e}")
+    assert len(got) >= 8 and float(rms(got)) <= 12 * base.U
