@@ -249,7 +249,6 @@ __global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float
   const int t = blockIdx.x * 32 + lane, tok = blockIdx.x * 32 + sl;  // summed by this lane, joined by this warp
   const int y = tok < M ? labels[tok] : -1;
   const double s_t = tok < M ? s_tok[tok] : 0.0;
-  const float s_label = y >= 0 && y < V ? ld_f32(s_row + y) : 0.0f;
   float m = -INFINITY, S = 0.0f;
   constexpr int U = 8;  // slots in flight
   for (int s0 = sl; s0 < slots; s0 += U * LF_SLICES) {
@@ -268,6 +267,7 @@ __global__ void __launch_bounds__(32 * LF_SLICES) loss_finish_kernel(const float
     for (int u = 0; u < U; ++u) S += p[u].y * ex2(p[u].x - mz);  // an empty part is (-inf, 0); a NaN sum stays one
     m = mx;
   }
+  const float s_label = y >= 0 && y < V ? ld_f32(s_row + y) : 0.0f;  // (its address waits for y: after the slots)
   sm[sl][lane] = make_float2(m, S);
   __syncthreads();
   // warp sl joins token sl: lane i holds slice i
