@@ -30,7 +30,7 @@
 // At the end one kernel joins the digits, the listed rows and the label's row and applies the norm's backward.
 // The digits are stored as signed bytes (digit - 128); the column sums of W give the 128s back.
 //
-// 2048 tokens x 50288 rows x 2048: loss 165 us (2550 TOPS), loss and gradients 875 us (2410 TOPS of five products).
+// 2048 tokens x 50288 rows x 2048: loss 166 us (2530 TOPS), loss and gradients 886 us (2380 TOPS of five products).
 // Bound by power: with operands that do not change the products alone run at 3270 TOPS under the same cap.  What the
 // gradient takes beyond its products is the digits' epilogue (205 us for a product that alone takes 150).
 // Measured and dropped: the digits of a piece in one kernel with the second product of the piece before, tiles of both in

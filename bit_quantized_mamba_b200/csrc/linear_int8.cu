@@ -9,8 +9,8 @@
 // The outputs are the head's bit for bit: the accumulators are exact, and the epilogue gives the definition's
 // value, an fp64 product rounded once to fp32 (bf16 outputs round that once more).
 //
-// W of 50288 x 2048: 1 token 21 us and 16 tokens 24.5 us (4.9 and 4.3 TB/s, the stream of W with a launch's
-// latency before it), 2048 tokens 191 us (2200 TOPS; bound by power: the loss's product, which stores nothing, runs
+// W of 50288 x 2048: 1 token 21 us and 16 tokens 24.9 us (4.8 and 4.2 TB/s, the stream of W with a launch's
+// latency before it), 2048 tokens 195 us (2170 TOPS; bound by power: the loss's product, which stores nothing, runs
 // at 2550).
 
 #include "gemm_i8.cuh"
