@@ -400,7 +400,8 @@ int dfssm_embed_tokens_backward(const int8_t* W, int V, int d, const int32_t* to
  * norm included when norm_w is given), without storing them:
  *   loss[t] = log sum_v exp l[t][v] - l[t][labels[t]]     device f32 [M]
  * labels device i32 [M]; a negative label is ignored (loss 0, no gradient), one >= V is ignored too and gives
- * DFSSM_EINVAL from dfssm_device_status.  A token that holds an infinity or a NaN has loss NaN.
+ * DFSSM_EINVAL from dfssm_device_status.  A token that holds an infinity or a NaN has loss NaN.  Logits are taken in
+ * fp32 inside the sum; past 2^30 in magnitude the loss need not be finite.
  * stats device f32 [3][M] receives what dfssm_head_loss_backward needs (opaque).  Up to 16 tokens the CTAs count
  * themselves in the workspace: zero-filled before its first use, every call leaves the count zero.
  * workspace: dfssm_workspace_size(DFSSM_OP_HEAD_LOSS, M, d, V).

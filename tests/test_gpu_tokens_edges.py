@@ -422,6 +422,41 @@ def test_head_gradient_errors_in_the_mean(dev, M, V, d, peak, kind, count, facto
             assert got <= 2 * want
 
 
+@pytest.mark.parametrize("M,V,d,count", [(3, 40, 64, 2), (20, 9000, 272, 1), (20, 9000, 272, 300), (300, 9000, 144, 30),
+                                         (300, 20000, 144, 1500), (700, 6000, 1040, 7)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_head_gradient_with_outlying_rows(dev, M, V, d, count, dtype):
+    """Some rows' scales a thousand times the others', their labels among the tokens', ignored labels, strides: within the
+    bounds, bit for bit again, and in a captured step."""
+    from bit_quantized_mamba_b200 import dfssm
+    g = gen(170 + M + count, dev)
+    W, sr = matrix(g, V, d, dev)
+    large = torch.randperm(V, generator=g, device=dev)[:count]
+    sr[large] *= 1000
+    x = base.rows(g, M, d, dev, dtype, pad=8)
+    nw = torch.rand(d, generator=g, device=dev) + 0.5
+    labels = torch.randint(0, V, (M,), generator=g, device=dev, dtype=torch.int32)
+    labels[::4] = large[torch.arange(len(labels[::4]), device=dev) % count].int()
+    labels[1::5] = -1
+    dloss = torch.randn(M, generator=g, device=dev)
+    base.check_head(dfssm, W, sr, x, nw, labels, dloss)
+    size = dfssm.workspace_size
+    ws = [dfssm.workspace(size(op, M, d, V), dev) for op in (dfssm.OP_HEAD_LOSS, dfssm.OP_HEAD_LOSS_BACKWARD)]
+
+    def step():
+        loss, stats = dfssm.head_loss(W, sr, x, labels, norm_w=nw, ws=ws[0])
+        return [loss, *dfssm.head_loss_backward(W, sr, x, labels, stats, dloss, norm_w=nw, ws=ws[1])]
+
+    want = step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("M", [1, 3, 16, 40, 128, 500])
 def test_loss_of_confident_tokens_in_the_mean(dev, M):
     """Tokens whose label's logit is tens above flat others: the relative error of a loss near exp(-z) is the error of z.
