@@ -14,8 +14,8 @@
 //      repeats; a run of equal tokens inside a window is final, one that crosses windows leaves partial sums, which
 //      the last of its CTAs to finish adds in order.
 //
-// 16384 tokens of 2048: forward (bf16) 18 us a call, 14.6 on the device alone (the 67 MB it writes at 4.6 TB/s); gradient of 50288 rows (bf16) 110 us
-// for 490 MB read and written (4.5 TB/s).  500 tokens: 16 us, three launches in a row.
+// 16384 tokens of 2048: forward (bf16) 18 us a call, 14.6 on the device alone (the 67 MB it writes at 4.6 TB/s); gradient of
+// 50288 rows (bf16) 110 us for 490 MB read and written (4.5 TB/s).  500 tokens: 17 us, two launches in a row.
 
 #include "common.cuh"
 #include "internal.h"

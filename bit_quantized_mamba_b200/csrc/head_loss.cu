@@ -631,7 +631,8 @@ __device__ __forceinline__ FixedPoint fixed_point(const uint2* srow, int V) {  /
   const ScaleTop t = scale_top(srow, V);
   FixedPoint p;
   p.range = t.neg ? 1 << 23 : 1 << 24;
-  p.unit = t.top < 1e-30f ? 0.0f : (float)(p.range - (t.outliers ? p.range >> 8 : 64)) / scale2(t.top);  // (so small, nothing of du is left either)
+  // (with scales below 1e-30, nothing of du is left either)
+  p.unit = t.top < 1e-30f ? 0.0f : (float)(p.range - (t.outliers ? p.range >> 8 : 64)) / scale2(t.top);
   p.offset = t.neg ? 1 << 23 : 0;
   p.outliers = t.outliers;
   p.step = p.unit == 0.0f ? 0.0 : 1.0 / ((double)p.unit * kLog2e);
